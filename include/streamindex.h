@@ -332,6 +332,167 @@ int si_sparse_attention(const void* qa, const void* ka, const void* va, const in
                         int S, int T, int H_a, int d_a, int topk, float scale, float* out,
                         const si_options* opt, void* stream);
 
+/* ---- attention with a sliding window and sinks ----------------------------- */
+
+/*
+ * si_window_attention: each query attends to the most recent tokens of its
+ * sequence and to its first few (the sinks), the branch of a sparse-attention
+ * layer beside the selected entries.  Row i of batch b (i < q_lens[b]) is the
+ * token at position t = lens[b] - q_lens[b] + i: the call's queries are the
+ * newest tokens of their sequences, a whole prompt (q_lens = lens), a chunk of
+ * one, or a single token.  Query head h reads kv head h / (H / H_k):
+ *   J(b,t) = { j : 0 <= j <= t, j < lens[b], j > t - window or j < sinks }
+ *   out[b,i,h,:] = sum_{j in J} softmax_j(scale * qa[b,i,h,:] . ka[b,j,h',:]) va[b,j,h',:]
+ *   lse[b,i,h]   = ln sum_{j in J} exp(scale * qa . ka)
+ * A row that sees no key (t < 0) gives zeros and -inf.  Rows i >= q_lens[b]
+ * of out and lse are left as they were.  Keys that a row does not see do not
+ * reach its result, whatever they hold (infinities and NaN too); keys at or
+ * past lens[b] are never used.
+ *   qa   bf16 [B,S,H,d]        queries
+ *   ka   bf16 [B,T,H_k,d]      keys; a buffer with room for more is fine
+ *   va   bf16 [B,T,H_k,d]      values
+ *   lens int32 [B]             tokens of each sequence, 0 .. T; NULL: T
+ *   q_lens int32 [B]           its query rows, 0 .. S; NULL: S
+ *   out  bf16 [B,S,H,d];  lse fp32 [B,S,H], or NULL
+ * Lengths outside their range count as its nearest end.
+ * Arithmetic: products of bf16 with fp32 accumulation, softmax in fp32, the
+ * probabilities rounded to bf16 for the weighted sum (2^-8 each), out rounded
+ * once.  The same inputs and plan give the same bits.
+ * Limits: B, S, T >= 1; T < 2^30; H a multiple of H_k; B*S*H, B*T*H_k < 2^31;
+ * d in {64, 128} (SI_ERR_DIM); window >= 1, sinks >= 0, scale finite and >= 0
+ * (SI_ERR_OPTIONS); tensors 16-byte aligned, lens, q_lens and lse 4-byte.
+ * Options: key_chunk > 0 fixes the keys that one CTA takes when few rows share
+ * many keys (0: the library's choice); timeout_ms; grid_ctas.
+ * Workspace: caller-provided, at least si_window_attention_workspace_size
+ * bytes (partial results of rows whose keys several CTAs share; 0 if none).
+ */
+int si_window_attention(const void* qa, const void* ka, const void* va, const int32_t* lens,
+                        const int32_t* q_lens, int B, int S, int T, int H, int H_k, int d,
+                        int window, int sinks, float scale, void* out, float* lse,
+                        const si_options* opt, void* workspace, size_t ws_bytes, void* stream);
+
+int si_window_attention_workspace_size(int B, int S, int T, int H, int H_k, int d, int window,
+                                       int sinks, const si_options* opt, size_t* bytes);
+
+/* ---- a key/value cache in 4 bits, in pages --------------------------------- */
+
+/*
+ * The cache: `pages` is a pool of n_pages pages of si_cache4_page_bytes bytes
+ * each; a page holds `page` tokens (a power of two, 16 .. 256) of every kv
+ * head.  Token j of sequence b lies in page table[b, j / page] at slot
+ * j % page; table is int32 [B, width], -1 for no page.  In a page, head after
+ * head: K codes [page, d/2], V codes [page, d/2], K scales [page, d/16],
+ * V scales [page, d/16].  Element e of a row is the low (e even) or high
+ * nibble of code byte e/2, an E2M1 number (sign, two exponent bits, one
+ * mantissa bit: 0, .5, 1, 1.5, 2, 3, 4, 6); its block of 16 elements has an
+ * E4M3 scale s, and keys and values have one fp32 scale g each (k_scale,
+ * v_scale): the number is g * s * code.  4.5 bits per element.
+ * For every call: d in {64, 128}; width * page < 2^30; lens[b] outside
+ * 0 .. width*page counts as the nearest end; a token whose table entry names
+ * no page of the pool is not there (not written, not read, not attended to).
+ * k_scale and v_scale lie in [2^-60, 2^60] (SI_ERR_OPTIONS).
+ */
+int si_cache4_page_bytes(int H_k, int d, int page, size_t* bytes);
+
+/*
+ * si_cache4_append: rounds the newest tokens' rows into the cache.  Row i of
+ * batch b (i < q_lens[b], NULL: S) is the token at lens[b] - q_lens[b] + i
+ * (lens counts the new tokens), the rows of si_window_attention's queries.
+ *   k, v  bf16 [B,S,H_k,d]
+ * Rounding of a block: s = E4M3(min(max|x| / (6 g), 448)), code =
+ * E2M1(x / (g s)), quotients in fp32, both to nearest with ties to even;
+ * quotients above 6 are stored as 6; a block with s = 0 as zeros; NaN as 0.
+ * Two rows of a call must not be the same token (a page in two table rows).
+ */
+int si_cache4_append(const void* k, const void* v, int B, int S, int H_k, int d, void* pages,
+                     int n_pages, const int32_t* table, int width, int page, const int32_t* lens,
+                     const int32_t* q_lens, float k_scale, float v_scale, void* stream);
+
+/* si_cache4_read: the same rows back as bf16 (g * s * code, rounded once) into
+ * k, v [B,S,H_k,d]; rows of tokens that are not there are left as they were. */
+int si_cache4_read(void* k, void* v, int B, int S, int H_k, int d, const void* pages, int n_pages,
+                   const int32_t* table, int width, int page, const int32_t* lens,
+                   const int32_t* q_lens, float k_scale, float v_scale, void* stream);
+
+/*
+ * si_cache4_attention: attention of the newest tokens' queries over the cache.
+ * idx NULL: over the keys that si_window_attention's rule gives, window 0
+ * standing for no window (and no sinks: every key j <= t).
+ * idx [B,S,topk]: over the entries that a row lists, si_sparse_attention's
+ * rule with lens[b] in T's place (window and sinks must be 0):
+ *   J(b,i) = { idx[b,i,r] : 0 <= r < topk, 0 <= idx[b,i,r] < lens[b] }
+ * entries count as often as they are listed.  out, lse, q_lens, H, H_k and
+ * options as in si_window_attention.
+ * Arithmetic: codes times block scales are exact in fp16; products in fp16
+ * with fp32 accumulation (a query row is scaled into fp16's range by a power
+ * of two), softmax in fp32, the probabilities rounded to fp16 (2^-11).
+ * Limits: H a multiple of H_k, B*S*H < 2^31, B*width < 2^31, topk <= 2048
+ * when idx is given (SI_ERR_TOPK).
+ */
+int si_cache4_attention(const void* qa, const void* pages, int n_pages, const int32_t* table,
+                        int width, int page, const int32_t* lens, const int32_t* q_lens,
+                        const int32_t* idx, int topk, int B, int S, int H, int H_k, int d,
+                        int window, int sinks, float scale, float k_scale, float v_scale,
+                        void* out, float* lse, const si_options* opt, void* workspace,
+                        size_t ws_bytes, void* stream);
+
+/* topk: 0 when idx is NULL. */
+int si_cache4_attention_workspace_size(int width, int page, int topk, int B, int S, int H, int H_k,
+                                       int d, int window, int sinks, const si_options* opt,
+                                       size_t* bytes);
+
+/* ---- the pages of a cache --------------------------------------------------- */
+
+/*
+ * Calls that keep the pages of a pool: refs int32 [n_pages] counts the table
+ * rows that hold a page (0: free); a row of table [B, width] lists its
+ * sequence's pages in its leading entries, -1 after them; lens int32 [B].
+ * The pool may hold any cache whose pages are page_bytes bytes (a multiple of
+ * 16, the pool 16-byte aligned).  All state is on the device and changes in
+ * place, in stream order.  The lowest free pages are taken first, in the order
+ * of the rows, so results depend on the inputs alone.  page is a power of two,
+ * 1 .. 2^16, in tokens.  The workspace is at least
+ * si_cache_workspace_size(n_pages, B, n) bytes, 16-byte aligned; two calls
+ * that may run at the same time need a workspace each (and must not change the
+ * same state).
+ */
+int si_cache_workspace_size(int n_pages, int B, int n, size_t* bytes);
+
+/* si_cache_extend: gives each row the pages it lacks for lens[b] tokens: the
+ * -1 entries among its first ceil(lens[b] / page) (at most width), in row
+ * order.  missing [1]: entries that got none because no page was free. */
+int si_cache_extend(int32_t* refs, int n_pages, int32_t* table, int B, int width,
+                    const int32_t* lens, int page, int32_t* missing, void* workspace,
+                    size_t ws_bytes, void* stream);
+
+/* si_cache_fork: makes row dst[i] a copy of row src[i] (i < n), as beam search
+ * or several answers to one prompt do: whole pages are shared, a partly filled
+ * last page is copied to a free one, lens[dst[i]] = lens[src[i]].  Parents are
+ * taken as they were before the call.  A child is not made when its rows are
+ * out of range or the same, its row dst[i] is not empty (length 0, no page),
+ * an earlier child has that row, its parent's length does not fit its row or
+ * lacks its last page, or no page is free.  missing [1]: children not made. */
+int si_cache_fork(void* pages, int64_t page_bytes, int32_t* refs, int n_pages, int32_t* table,
+                  int B, int width, int32_t* lens, const int32_t* src, const int32_t* dst, int n,
+                  int page, int32_t* missing, void* workspace, size_t ws_bytes, void* stream);
+
+/* si_cache_free: empties the rows listed (n of them; out-of-range ones are
+ * skipped, a row listed twice is emptied once): its pages lose a holder, its
+ * entries become -1, its length 0.  No workspace. */
+int si_cache_free(int32_t* refs, int n_pages, int32_t* table, int B, int width, int32_t* lens,
+                  const int32_t* rows, int n, void* stream);
+
+/* si_cache_compact: with L pages in use, moves those at L and above into the
+ * free pages below L, both in ascending order, so that pages 0 .. L-1 are the
+ * ones in use.  The new table and counts go to table_out [B, width] and
+ * refs_out [n_pages] (the old ones stay valid until a page is taken again;
+ * table_out = table and refs_out = refs are allowed).  Table entries that name
+ * a free page become -1.  live [1]: L. */
+int si_cache_compact(void* pages, int64_t page_bytes, const int32_t* refs, int n_pages,
+                     const int32_t* table, int B, int width, int32_t* refs_out,
+                     int32_t* table_out, int32_t* live, void* workspace, size_t ws_bytes,
+                     void* stream);
+
 /* ---- diagnostics ------------------------------------------------------ */
 
 /* Text for a status code (static storage). */

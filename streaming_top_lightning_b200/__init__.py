@@ -21,6 +21,8 @@ from ._lib import SiOptions, SiPlanInfo, StreamIndexError  # noqa: F401
 __all__ = [
     "indexer_topk", "indexer_topk_noalloc", "indexer_topk_fp8", "quantize_fp8_rows", "topk_scores",
     "workspace_size", "plan", "device_error", "options", "version", "StreamIndexError",
+    "window_attention", "cache4_page_bytes", "cache4_append", "cache4_read", "cache4_attention",
+    "cache_extend", "cache_fork", "cache_free", "cache_compact",
 ]
 
 
@@ -327,3 +329,304 @@ def topk_scores(scores, m: int, topk: int, *, out=None, opts: SiOptions | None =
 def device_error(stream=None) -> int:
     """Synchronise and return the device status word as an SI status code."""
     return _lib.load().si_get_last_device_error(_stream(stream))
+
+
+# ---- key/value cache: window attention, 4-bit pages, the pages' life
+
+
+class _Call:
+    """Where a call runs: on the device of its tensors, whichever is current,
+    and on ``stream`` or that device's current stream, whose memory pool the
+    call's own tensors come from."""
+
+    def __init__(self, device, stream):
+        torch = _torch()
+        self.device = device
+        self.stream = stream
+        self.guards = []
+        if device.index != torch.cuda.current_device():
+            self.guards.append(torch.cuda.device(device))
+        if stream is not None:
+            if stream.device != device:
+                raise ValueError("the stream is on another device than the tensors")
+            self.guards.append(torch.cuda.stream(stream))
+
+    def __enter__(self):
+        for g in self.guards:
+            g.__enter__()
+        s = self.stream if self.stream is not None else _torch().cuda.current_stream()
+        return ctypes.c_void_p(s.cuda_stream)
+
+    def __exit__(self, *exc):
+        for g in reversed(self.guards):
+            g.__exit__(*exc)
+
+
+def _need_on(device, t, dtype, shape, name):
+    """t is a contiguous tensor of this type and shape on the device (a None in
+    the shape: any size)."""
+    _need(t, dtype, len(shape), name)
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, the call's tensors are on {device}")
+    if any(want is not None and want != got for want, got in zip(shape, t.shape)):
+        raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
+
+
+def _opt_ptr(t):
+    return None if t is None else ctypes.c_void_p(t.data_ptr())
+
+
+def _attention_out(qa, out, lse):
+    torch = _torch()
+    B, S, H, D = qa.shape
+    if out is None:
+        out = torch.empty((B, S, H, D), dtype=torch.bfloat16, device=qa.device)
+    else:
+        _need_on(qa.device, out, torch.bfloat16, (B, S, H, D), "out")
+    if lse is None:
+        lse = torch.empty((B, S, H), dtype=torch.float32, device=qa.device)
+    else:
+        _need_on(qa.device, lse, torch.float32, (B, S, H), "lse")
+    return out, lse
+
+
+def _scratch(need, workspace, device):
+    """The call's workspace: the caller's, or one of its own."""
+    torch = _torch()
+    if workspace is not None:
+        _need_on(device, workspace, torch.uint8, (None,), "workspace")
+        return ctypes.c_void_p(workspace.data_ptr()), workspace.numel(), workspace
+    if need == 0:
+        return None, 0, None
+    w = torch.empty(need, dtype=torch.uint8, device=device)
+    return ctypes.c_void_p(w.data_ptr()), need, w
+
+
+def window_attention(qa, ka, va, window: int, sinks: int = 0, *, lens=None, q_lens=None,
+                     scale: float | None = None, out=None, lse=None,
+                     opts: SiOptions | None = None, workspace=None, stream=None):
+    """Attention of each query to the last ``window`` tokens up to its own and
+    to the first ``sinks`` ones (si_window_attention): qa [B,S,H,D] bf16, ka and
+    va [B,T,H_k,D] bf16, D 64 or 128, H a multiple of H_k.  ``lens`` [B] int32:
+    tokens of each sequence (default T); ``q_lens`` [B] int32: how many of the
+    S query rows it has (default S); they are its newest tokens.  ``scale``
+    defaults to 1/sqrt(D).  Returns (out [B,S,H,D] bf16, lse [B,S,H] fp32: the
+    logarithm of each row's sum of exponentials, which joins this result with
+    another over other keys); rows past q_lens are left as they were."""
+    torch = _torch()
+    _need(qa, torch.bfloat16, 4, "qa")
+    _need(ka, torch.bfloat16, 4, "ka")
+    B, S, H, D = qa.shape
+    T, Hk = ka.shape[1], ka.shape[2]
+    dev = qa.device
+    _need_on(dev, ka, torch.bfloat16, (B, T, Hk, D), "ka")
+    _need_on(dev, va, torch.bfloat16, (B, T, Hk, D), "va")
+    for t, name in ((lens, "lens"), (q_lens, "q_lens")):
+        if t is not None:
+            _need_on(dev, t, torch.int32, (B,), name)
+    lib = _lib.load()
+    o = ctypes.byref(opts) if opts else None
+    with _Call(dev, stream) as st:
+        need = ctypes.c_size_t(0)
+        _lib.check("si_window_attention_workspace_size",
+                   lib.si_window_attention_workspace_size(B, S, T, H, Hk, D, window, sinks, o,
+                                                          ctypes.byref(need)))
+        out, lse = _attention_out(qa, out, lse)
+        ws, ws_bytes, _keep = _scratch(need.value, workspace, dev)
+        rc = lib.si_window_attention(_ptr(qa), _ptr(ka), _ptr(va), _opt_ptr(lens),
+                                     _opt_ptr(q_lens), B, S, T, H, Hk, D, window, sinks,
+                                     float(D) ** -0.5 if scale is None else float(scale),
+                                     _ptr(out), _ptr(lse), o, ws, ws_bytes, st)
+    _lib.check("si_window_attention", rc)
+    return out, lse
+
+
+def cache4_page_bytes(heads: int, dim: int, page: int) -> int:
+    """Bytes of one page of a 4-bit cache (si_cache4_page_bytes): ``page`` tokens
+    of ``heads`` kv heads of ``dim`` elements."""
+    n = ctypes.c_size_t(0)
+    _lib.check("si_cache4_page_bytes",
+               _lib.load().si_cache4_page_bytes(heads, dim, page, ctypes.byref(n)))
+    return n.value
+
+
+def _cache4(pages, table, lens, q_lens, B, heads, dim, page):
+    torch = _torch()
+    _need(pages, torch.uint8, 2, "pages")
+    dev = pages.device
+    size = cache4_page_bytes(heads, dim, page)
+    _need_on(dev, pages, torch.uint8, (None, size), "pages")
+    _need_on(dev, table, torch.int32, (B, None), "table")
+    _need_on(dev, lens, torch.int32, (B,), "lens")
+    if q_lens is not None:
+        _need_on(dev, q_lens, torch.int32, (B,), "q_lens")
+    return dev
+
+
+def cache4_append(k, v, pages, table, lens, page: int, *, q_lens=None, k_scale: float = 1.0,
+                  v_scale: float = 1.0, stream=None):
+    """Round the newest tokens' key and value rows (k, v [B,S,H_k,D] bf16) into
+    the 4-bit pages (si_cache4_append): row i < q_lens[b] is token
+    lens[b] - q_lens[b] + i.  ``pages`` [n_pages, cache4_page_bytes] uint8,
+    ``table`` [B,width] int32, ``lens`` [B] int32 with the new tokens counted."""
+    torch = _torch()
+    _need(k, torch.bfloat16, 4, "k")
+    B, S, Hk, D = k.shape
+    dev = _cache4(pages, table, lens, q_lens, B, Hk, D, page)
+    _need_on(dev, k, torch.bfloat16, (B, S, Hk, D), "k")
+    _need_on(dev, v, torch.bfloat16, (B, S, Hk, D), "v")
+    with _Call(dev, stream) as st:
+        rc = _lib.load().si_cache4_append(_ptr(k), _ptr(v), B, S, Hk, D, _ptr(pages),
+                                          pages.shape[0], _ptr(table), table.shape[1], page,
+                                          _ptr(lens), _opt_ptr(q_lens), float(k_scale),
+                                          float(v_scale), st)
+    _lib.check("si_cache4_append", rc)
+    return pages
+
+
+def cache4_read(pages, table, lens, S: int, heads: int, dim: int, page: int, *, q_lens=None,
+                k_scale: float = 1.0, v_scale: float = 1.0, out=None, stream=None):
+    """The newest tokens' rows back as bf16 (si_cache4_read): (k, v), each
+    [B,S,heads,dim]; rows of tokens that are not in the cache are left as they
+    were in ``out``."""
+    torch = _torch()
+    B = table.shape[0]
+    dev = _cache4(pages, table, lens, q_lens, B, heads, dim, page)
+    with _Call(dev, stream) as st:
+        if out is None:
+            out = tuple(torch.empty((B, S, heads, dim), dtype=torch.bfloat16, device=dev)
+                        for _ in range(2))
+        k, v = out
+        _need_on(dev, k, torch.bfloat16, (B, S, heads, dim), "out[0]")
+        _need_on(dev, v, torch.bfloat16, (B, S, heads, dim), "out[1]")
+        rc = _lib.load().si_cache4_read(_ptr(k), _ptr(v), B, S, heads, dim, _ptr(pages),
+                                        pages.shape[0], _ptr(table), table.shape[1], page,
+                                        _ptr(lens), _opt_ptr(q_lens), float(k_scale),
+                                        float(v_scale), st)
+    _lib.check("si_cache4_read", rc)
+    return k, v
+
+
+def cache4_attention(qa, pages, table, lens, heads: int, page: int, window: int = 0,
+                     sinks: int = 0, *, q_lens=None, idx=None, scale: float | None = None,
+                     k_scale: float = 1.0, v_scale: float = 1.0, out=None, lse=None,
+                     opts: SiOptions | None = None, workspace=None, stream=None):
+    """Attention of the newest tokens' queries (qa [B,S,H,D] bf16) over a 4-bit
+    cache of ``heads`` kv heads (si_cache4_attention): over every key up to the
+    query's own (window 0), over a window and sinks as ``window_attention``, or
+    over the entries that ``idx`` [B,S,topk] int32 lists (the rows of
+    ``indexer_topk`` and ``indexer_decode``).  Returns (out, lse) as
+    ``window_attention``."""
+    torch = _torch()
+    _need(qa, torch.bfloat16, 4, "qa")
+    B, S, H, D = qa.shape
+    dev = _cache4(pages, table, lens, q_lens, B, heads, D, page)
+    _need_on(dev, qa, torch.bfloat16, (B, S, H, D), "qa")
+    topk = 0
+    if idx is not None:
+        _need_on(dev, idx, torch.int32, (B, S, None), "idx")
+        topk = idx.shape[2]
+    lib = _lib.load()
+    o = ctypes.byref(opts) if opts else None
+    width = table.shape[1]
+    with _Call(dev, stream) as st:
+        need = ctypes.c_size_t(0)
+        _lib.check("si_cache4_attention_workspace_size",
+                   lib.si_cache4_attention_workspace_size(width, page, topk, B, S, H, heads, D,
+                                                          window, sinks, o, ctypes.byref(need)))
+        out, lse = _attention_out(qa, out, lse)
+        ws, ws_bytes, _keep = _scratch(need.value, workspace, dev)
+        rc = lib.si_cache4_attention(_ptr(qa), _ptr(pages), pages.shape[0], _ptr(table), width,
+                                     page, _ptr(lens), _opt_ptr(q_lens), _opt_ptr(idx), topk, B, S,
+                                     H, heads, D, window, sinks,
+                                     float(D) ** -0.5 if scale is None else float(scale),
+                                     float(k_scale), float(v_scale), _ptr(out), _ptr(lse), o, ws,
+                                     ws_bytes, st)
+    _lib.check("si_cache4_attention", rc)
+    return out, lse
+
+
+def _pool(refs, table, lens):
+    torch = _torch()
+    _need(refs, torch.int32, 1, "refs")
+    dev = refs.device
+    _need_on(dev, table, torch.int32, (None, None), "table")
+    if lens is not None:
+        _need_on(dev, lens, torch.int32, (table.shape[0],), "lens")
+    return dev, refs.shape[0], table.shape[0], table.shape[1]
+
+
+def _pages_scratch(n_pages, B, n, workspace, device):
+    need = ctypes.c_size_t(0)
+    _lib.check("si_cache_workspace_size",
+               _lib.load().si_cache_workspace_size(n_pages, B, n, ctypes.byref(need)))
+    return _scratch(need.value, workspace, device)
+
+
+def cache_extend(refs, table, lens, page: int, *, workspace=None, stream=None):
+    """Give each row of ``table`` [B,width] the pages that it lacks for lens[b]
+    tokens, the lowest free ones first (si_cache_extend); ``refs`` [n_pages]
+    counts each page's holders.  Returns an int32 [1] tensor: entries for which
+    no page was free."""
+    torch = _torch()
+    dev, n, B, width = _pool(refs, table, lens)
+    with _Call(dev, stream) as st:
+        missing = torch.empty(1, dtype=torch.int32, device=dev)
+        ws, ws_bytes, _keep = _pages_scratch(n, B, 0, workspace, dev)
+        rc = _lib.load().si_cache_extend(_ptr(refs), n, _ptr(table), B, width, _ptr(lens), page,
+                                         _ptr(missing), ws, ws_bytes, st)
+    _lib.check("si_cache_extend", rc)
+    return missing
+
+
+def cache_fork(pages, refs, table, lens, src, dst, page: int, *, workspace=None, stream=None):
+    """Make each row dst[i] a copy of row src[i] (si_cache_fork): whole pages are
+    shared, a partly filled last one is copied.  The rows dst must be empty
+    (``cache_free``).  Returns an int32 [1] tensor: children not made."""
+    torch = _torch()
+    dev, n, B, width = _pool(refs, table, lens)
+    _need_on(dev, pages, torch.uint8, (n, None), "pages")
+    _need_on(dev, src, torch.int32, (None,), "src")
+    _need_on(dev, dst, torch.int32, (src.shape[0],), "dst")
+    with _Call(dev, stream) as st:
+        missing = torch.empty(1, dtype=torch.int32, device=dev)
+        ws, ws_bytes, _keep = _pages_scratch(n, B, src.shape[0], workspace, dev)
+        rc = _lib.load().si_cache_fork(_ptr(pages), pages.shape[1], _ptr(refs), n, _ptr(table), B,
+                                       width, _ptr(lens), _ptr(src), _ptr(dst), src.shape[0], page,
+                                       _ptr(missing), ws, ws_bytes, st)
+    _lib.check("si_cache_fork", rc)
+    return missing
+
+
+def cache_free(refs, table, lens, rows, *, stream=None):
+    """Empty the listed rows: their pages lose a holder (si_cache_free)."""
+    torch = _torch()
+    dev, n, B, width = _pool(refs, table, lens)
+    _need_on(dev, rows, torch.int32, (None,), "rows")
+    with _Call(dev, stream) as st:
+        rc = _lib.load().si_cache_free(_ptr(refs), n, _ptr(table), B, width, _ptr(lens), _ptr(rows),
+                                       rows.shape[0], st)
+    _lib.check("si_cache_free", rc)
+
+
+def cache_compact(pages, refs, table, *, out=None, workspace=None, stream=None):
+    """Move the pages in use to the front of the pool (si_cache_compact).
+    Returns (table, refs, live): the new table and counts (``out`` = (table,
+    refs) to write them in place, else new tensors) and an int32 [1] tensor with
+    the number of pages in use."""
+    torch = _torch()
+    dev, n, B, width = _pool(refs, table, None)
+    _need_on(dev, pages, torch.uint8, (n, None), "pages")
+    with _Call(dev, stream) as st:
+        if out is None:
+            out = (torch.empty_like(table), torch.empty_like(refs))
+        new_table, new_refs = out
+        _need_on(dev, new_table, torch.int32, (B, width), "out[0]")
+        _need_on(dev, new_refs, torch.int32, (n,), "out[1]")
+        live = torch.empty(1, dtype=torch.int32, device=dev)
+        ws, ws_bytes, _keep = _pages_scratch(n, B, 0, workspace, dev)
+        rc = _lib.load().si_cache_compact(_ptr(pages), pages.shape[1], _ptr(refs), n, _ptr(table),
+                                          B, width, _ptr(new_refs), _ptr(new_table), _ptr(live), ws,
+                                          ws_bytes, st)
+    _lib.check("si_cache_compact", rc)
+    return new_table, new_refs, live

@@ -25,7 +25,11 @@ EXPORTS = [
     "si_get_last_device_error", "si_version", "si_indexer_topk_noalloc", "si_indexer_topk_plan",
     "si_role_cycles", "si_indexer_decode", "si_indexer_decode_workspace_size",
     "si_indexer_decode_plan", "si_sparse_attention", "si_indexer_pivot",
-    "si_indexer_pivot_workspace_size",
+    "si_indexer_pivot_workspace_size", "si_window_attention",
+    "si_window_attention_workspace_size", "si_cache4_page_bytes", "si_cache4_append",
+    "si_cache4_read", "si_cache4_attention", "si_cache4_attention_workspace_size",
+    "si_cache_workspace_size", "si_cache_extend", "si_cache_fork", "si_cache_free",
+    "si_cache_compact",
 ]
 
 
@@ -97,6 +101,20 @@ def load(path: str | None = None) -> ctypes.CDLL:
     lib.si_indexer_pivot.argtypes = [P, P, P, I, I, I, I, I, I, I, I, P, P, OP, P, Z, P]
     lib.si_indexer_pivot_workspace_size.argtypes = [I, I, I, I, I, I, I, I, OP,
                                                     ctypes.POINTER(Z)]
+    F, ZP = ctypes.c_float, ctypes.POINTER(Z)
+    lib.si_window_attention.argtypes = [P] * 5 + [I] * 8 + [F, P, P, OP, P, Z, P]
+    lib.si_window_attention_workspace_size.argtypes = [I] * 8 + [OP, ZP]
+    lib.si_cache4_page_bytes.argtypes = [I, I, I, ZP]
+    lib.si_cache4_append.argtypes = [P, P, I, I, I, I, P, I, P, I, I, P, P, F, F, P]
+    lib.si_cache4_read.argtypes = [P, P, I, I, I, I, P, I, P, I, I, P, P, F, F, P]
+    lib.si_cache4_attention.argtypes = ([P, P, I, P, I, I, P, P, P] + [I] * 8 +
+                                        [F, F, F, P, P, OP, P, Z, P])
+    lib.si_cache4_attention_workspace_size.argtypes = [I] * 10 + [OP, ZP]
+    lib.si_cache_workspace_size.argtypes = [I, I, I, ZP]
+    lib.si_cache_extend.argtypes = [P, I, P, I, I, P, I, P, P, Z, P]
+    lib.si_cache_fork.argtypes = [P, L, P, I, P, I, I, P, P, P, I, I, P, P, Z, P]
+    lib.si_cache_free.argtypes = [P, I, P, I, I, P, P, I, P]
+    lib.si_cache_compact.argtypes = [P, L, P, I, P, I, I, P, P, P, P, Z, P]
     for name in EXPORTS:
         if name != "si_status_string":
             getattr(lib, name).restype = I

@@ -55,7 +55,7 @@ def build(force: bool = False, debug: bool = False, verbose: bool = False,
         return lib
     tmp = lib + f".tmp{os.getpid()}"
     cmd = [_nvcc(), *ARCH, "-lineinfo", "-O3", "-std=c++17", "--expt-relaxed-constexpr",
-           "-Xcompiler", "-fPIC", "-shared", "--cudart", "static", "-I", INCLUDE, "-I", CSRC,
+           "--threads", "0", "-Xcompiler", "-fPIC", "-shared", "--cudart", "static", "-I", INCLUDE, "-I", CSRC,
            "-o", tmp, *sources()]
     if debug:
         cmd.insert(1, "-DSI_DEBUG")

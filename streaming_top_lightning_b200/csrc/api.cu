@@ -16,6 +16,7 @@
 #include <mutex>
 
 #include "streamindex.h"
+#include "si_api.h"
 #include "si_kernels.h"
 
 namespace si {
@@ -30,18 +31,11 @@ __device__ unsigned long long g_role_cycles[kRoleCtas * kRoleSlots];
 
 namespace {
 
-struct DevInfo {
-  bool init = false;
-  bool ok = false;
-  int sms = 0;
-  int max_smem = 0;
-  uint32_t* err = nullptr;
-  unsigned long long* role = nullptr;  // profiling build: role counters
-};
-
 std::mutex g_mu;
 DevInfo g_dev[64];
 PFN_cuTensorMapEncodeTiled_v12000 g_encode = nullptr;
+
+}  // namespace
 
 int dev_info(DevInfo** out) {
   int dev = 0;
@@ -81,29 +75,6 @@ int dev_info(DevInfo** out) {
   return SI_OK;
 }
 
-// Shared memory and SM count to plan with: the current device's, or the
-// sm_100 limits (227 KB of opt-in shared memory per CTA, 148 SMs) on a host
-// with no usable device.  Used by the plan query only.
-void plan_limits(int* max_smem, int* sms) {
-  DevInfo* dev = nullptr;
-  if (dev_info(&dev) == SI_OK) {
-    *max_smem = dev->max_smem;
-    *sms = dev->sms;
-  } else {
-    *max_smem = 227 * 1024;
-    *sms = 148;
-  }
-}
-
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-
-// Keys a query at sequence position t sees: min(T, (t+1)/m).
-int visible_host(int t, int T, int m) {
-  const int v = (int)(((int64_t)t + 1) / m);
-  return v < T ? v : T;
-}
-size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
-
 // 2-D row-major [rows, cols] tensor map with a {box_inner, box_rows} box and
 // the given swizzle; out-of-range rows read as zero.
 int make_map(CUtensorMap* m, const void* base, CUtensorMapDataType dt, uint64_t rows,
@@ -118,15 +89,6 @@ int make_map(CUtensorMap* m, const void* base, CUtensorMapDataType dt, uint64_t 
                         CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return r == CUDA_SUCCESS ? SI_OK : SI_ERR_CUDA;
 }
-
-struct Opts {
-  int key_chunk, scratch_mb, grid_ctas, timeout_ms, debug_flags, row_finish, key_tile,
-      strip_slots;
-  cudaEvent_t ev_begin, ev_end;
-  cudaEvent_t* ev_list;  // [2i], [2i+1] around query block i's score launch
-  int ev_count;
-  int plan_heads, plan_dim, plan_fp8;  // si_topk_scores: the fused kernel's plan
-};
 
 int read_opts(const si_options* o, Opts* out) {
   Opts d{0, 512, 0, 2000, 0, 0, 0, 0, nullptr, nullptr, nullptr, 0, 0, 0, 0};
@@ -165,6 +127,27 @@ int read_opts(const si_options* o, Opts* out) {
   return SI_OK;
 }
 
+// Shared memory and SM count to plan with: the current device's, or the
+// sm_100 limits (227 KB of opt-in shared memory per CTA, 148 SMs) on a host
+// with no usable device.  Used by the plan query only.
+void plan_limits(int* max_smem, int* sms) {
+  DevInfo* dev = nullptr;
+  if (dev_info(&dev) == SI_OK) {
+    *max_smem = dev->max_smem;
+    *sms = dev->sms;
+  } else {
+    *max_smem = 227 * 1024;
+    *sms = 148;
+  }
+}
+
+namespace {
+
+// Keys a query at sequence position t sees: min(T, (t+1)/m).
+int visible_host(int t, int T, int m) {
+  const int v = (int)(((int64_t)t + 1) / m);
+  return v < T ? v : T;
+}
 // The plan of one problem: tiles, chunks and query blocks.  With several key
 // chunks every (tile, chunk) unit leaves an L-key partial list per query; the
 // query tiles of one launch block share a scratch of B * tb * nch_max * QT * L

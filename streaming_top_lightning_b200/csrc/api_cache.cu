@@ -1,0 +1,433 @@
+// The C ABI of the key/value cache (include/streamindex.h): attention with a
+// window and sinks, the 4-bit paged cache, and the life of its pages.
+#include <algorithm>
+#include <cmath>
+
+#include "si_api.h"
+#include "si_kernels.h"
+
+namespace si {
+namespace {
+
+bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+
+constexpr int kWindowMax = 1 << 30;  // longer than any sequence
+
+// log2 of a page size, or -1.
+int page_shift_of(int page, int lo, int hi) {
+  if (page < lo || page > hi || (page & (page - 1))) return -1;
+  int s = 0;
+  while ((1 << s) < page) ++s;
+  return s;
+}
+
+bool scale_ok(float g) { return g >= 0x1p-60f && g <= 0x1p60f; }  // false for NaN
+
+// CTAs that share a row tile's keys.  A decode step has B * H_k tiles or few
+// more, each with up to `keys` keys: with fewer tiles than the GPU holds CTAs
+// the keys are split so that they fill it, as long as a CTA's four warps keep
+// two steps of 32 keys each.
+int row_splits(int64_t tiles, int64_t keys, int key_chunk, int sms) {
+  if (key_chunk > 0) return (int)std::min<int64_t>(1024, std::max<int64_t>(1, (keys + key_chunk - 1) / key_chunk));
+  const int64_t room = (int64_t)sms * 3;
+  if (tiles >= room) return 1;
+  const int64_t want = (room + tiles - 1) / tiles;
+  const int64_t most = std::max<int64_t>(1, keys / 256);
+  return (int)std::min<int64_t>(std::min(want, most), 128);
+}
+
+// Sizes that the two attention calls share.
+int check_attention(int B, int S, int H, int H_k, int d) {
+  if (B < 1 || S < 1 || H < 1 || H_k < 1 || H % H_k || !(d == 64 || d == 128)) return SI_ERR_DIM;
+  if ((int64_t)B * S * H >= ((int64_t)1 << 31)) return SI_ERR_DIM;
+  return SI_OK;
+}
+
+// The rows kernel's plan: tiles and splits, and the bytes of partial results.
+// keys: what one query may see at most.
+int plan_rows(RowsParams* p, int64_t keys, bool listed, int key_chunk, int sms, int d,
+              size_t* bytes) {
+  const int64_t span = listed ? keys : std::min<int64_t>(p->T, keys + 16 / p->G + 64);
+  const int64_t per = listed ? (int64_t)p->S * ((p->G + 15) / 16)
+                             : ((int64_t)p->S * p->G + 15) / 16;
+  const int64_t tiles = (int64_t)p->B * p->Hk * per;
+  p->splits = row_splits(tiles, span, key_chunk, sms);
+  if (tiles * p->splits >= ((int64_t)1 << 31)) return SI_ERR_DIM;
+  p->tiles = (int)per;
+  const int64_t rows = (int64_t)p->B * p->S * p->H;
+  *bytes = 0;
+  if (p->splits > 1)
+    *bytes = align256((size_t)rows * p->splits * d * sizeof(float)) +
+             align256((size_t)rows * p->splits * sizeof(float2));
+  return SI_OK;
+}
+
+int place_partials(RowsParams* p, int d, size_t need, void* ws, size_t ws_bytes) {
+  if (!need) return SI_OK;
+  if (!ws || ws_bytes < need) return SI_ERR_WORKSPACE;
+  if (!aligned16(ws)) return SI_ERR_ALIGN;
+  const int64_t rows = (int64_t)p->B * p->S * p->H;
+  p->part_o = static_cast<float*>(ws);
+  p->part_ml = reinterpret_cast<float2*>(
+      static_cast<char*>(ws) + align256((size_t)rows * p->splits * d * sizeof(float)));
+  return SI_OK;
+}
+
+// Sizes of a window call and its plan.
+int window_problem(int B, int S, int T, int H, int H_k, int d, int window, int sinks,
+                   const si_options* opt, RowsParams* p, Opts* o, size_t* bytes) {
+  int rc = check_attention(B, S, H, H_k, d);
+  if (rc) return rc;
+  if (T < 1 || T >= (1 << 30) || (int64_t)B * T * H_k >= ((int64_t)1 << 31)) return SI_ERR_DIM;
+  if (window < 1 || sinks < 0) return SI_ERR_OPTIONS;
+  if ((rc = read_opts(opt, o))) return rc;
+  p->B = B, p->S = S, p->T = T, p->H = H, p->Hk = H_k, p->G = H / H_k;
+  p->window = std::min(window, kWindowMax);
+  p->sinks = std::min(sinks, kWindowMax);
+  int max_smem = 0, sms = 0;
+  plan_limits(&max_smem, &sms);
+  return plan_rows(p, std::min<int64_t>(T, (int64_t)p->window + p->sinks), false, o->key_chunk,
+                   sms, d, bytes);
+}
+
+int cache4_problem(int width, int page, int topk, int B, int S, int H, int H_k, int d, int window,
+                   int sinks, const si_options* opt, RowsParams* p, Opts* o, size_t* bytes) {
+  int rc = check_attention(B, S, H, H_k, d);
+  if (rc) return rc;
+  const int sh = page_shift_of(page, 16, 256);
+  if (sh < 0 || width < 1 || (int64_t)width * page >= (1 << 30) ||
+      (int64_t)B * width >= ((int64_t)1 << 31))
+    return SI_ERR_DIM;
+  if (topk < 0 || topk > SI_MAX_TOPK) return SI_ERR_TOPK;
+  if (window < 0 || sinks < 0 || (window == 0 && sinks) || (topk && window)) return SI_ERR_OPTIONS;
+  if ((rc = read_opts(opt, o))) return rc;
+  p->B = B, p->S = S, p->T = width * page, p->H = H, p->Hk = H_k, p->G = H / H_k;
+  p->width = width;
+  p->page_shift = sh;
+  p->page_bytes = (int64_t)H_k * page * (d + d / 8);
+  p->topk = topk;
+  p->window = window ? std::min(window, kWindowMax) : kWindowMax;
+  p->sinks = std::min(sinks, kWindowMax);
+  int max_smem = 0, sms = 0;
+  plan_limits(&max_smem, &sms);
+  const int64_t keys =
+      topk ? topk : std::min<int64_t>(p->T, (int64_t)p->window + p->sinks);
+  return plan_rows(p, keys, topk > 0, o->key_chunk, sms, d, bytes);
+}
+
+// The sizes of a call on the rows of a 4-bit cache.
+int cache4_rows(int B, int S, int H_k, int d, int n_pages, int width, int page, float k_scale,
+                float v_scale, Cache4Params* p) {
+  if (B < 1 || S < 1 || H_k < 1 || !(d == 64 || d == 128) || n_pages < 1 || width < 1)
+    return SI_ERR_DIM;
+  const int sh = page_shift_of(page, 16, 256);
+  if (sh < 0 || (int64_t)width * page >= (1 << 30) || (int64_t)B * width >= ((int64_t)1 << 31) ||
+      (int64_t)B * S * H_k >= ((int64_t)1 << 31))
+    return SI_ERR_DIM;
+  if (!scale_ok(k_scale) || !scale_ok(v_scale)) return SI_ERR_OPTIONS;
+  p->B = B, p->S = S, p->Hk = H_k, p->width = width, p->n_pages = n_pages;
+  p->page_shift = sh;
+  p->cap = width * page;
+  p->page_bytes = (int64_t)H_k * page * (d + d / 8);
+  p->k_scale = k_scale, p->v_scale = v_scale;
+  return SI_OK;
+}
+
+// Workspace of the page calls, laid out for any of them.
+struct PagesLayout {
+  size_t a, b, c, d, e, total;
+};
+PagesLayout pages_layout(int n_pages, int B, int n) {
+  PagesLayout l;
+  const size_t pool = align256((size_t)n_pages * 4);
+  size_t at = 0;
+  auto take = [&](size_t bytes) {
+    const size_t r = at;
+    at += bytes;
+    return r;
+  };
+  l.a = take(pool);                                    // order, or live ranks
+  l.b = take(std::max(pool, align256((size_t)B * 4))); // claims, or holes
+  l.c = take(std::max(pool, align256((size_t)n * sizeof(ForkChild))));  // children, or movers
+  l.d = take(pool);                                    // the movers' counts
+  l.e = take(256);                                     // the number of moves
+  l.total = at;
+  return l;
+}
+
+int check_pool(int n_pages, int B, int width) {
+  if (n_pages < 1 || B < 1 || width < 1 || (int64_t)B * width >= ((int64_t)1 << 31))
+    return SI_ERR_DIM;
+  return SI_OK;
+}
+
+int pages_call(int32_t* refs, int n_pages, int32_t* table, int B, int width, int32_t* lens,
+               int page, PagesParams* p) {
+  int rc = check_pool(n_pages, B, width);
+  if (rc) return rc;
+  const int sh = page_shift_of(page, 1, 1 << 16);
+  if (sh < 0) return SI_ERR_DIM;
+  if (!aligned4(refs) || !aligned4(table) || !aligned4(lens)) return SI_ERR_ALIGN;
+  p->refs = refs, p->n_pages = n_pages, p->table = table, p->B = B, p->width = width;
+  p->lens = lens;
+  p->page_shift = sh;
+  return SI_OK;
+}
+
+int place_pages(PagesParams* p, void* ws, size_t ws_bytes) {
+  const PagesLayout l = pages_layout(p->n_pages, p->B, p->n);
+  if (!ws || ws_bytes < l.total) return SI_ERR_WORKSPACE;
+  if (!aligned16(ws)) return SI_ERR_ALIGN;
+  char* w = static_cast<char*>(ws);
+  p->order = p->lr = reinterpret_cast<int32_t*>(w + l.a);
+  p->claim = p->hole = reinterpret_cast<int32_t*>(w + l.b);
+  p->mover = reinterpret_cast<int32_t*>(w + l.c);
+  p->child = reinterpret_cast<ForkChild*>(w + l.c);
+  p->mref = reinterpret_cast<int32_t*>(w + l.d);
+  p->moves = reinterpret_cast<int32_t*>(w + l.e);
+  return SI_OK;
+}
+
+// A pool's pages and the CTAs that copy n of them.
+int check_pages(const void* pages, int64_t page_bytes, int64_t n) {
+  if (page_bytes < 16 || page_bytes % 16 || page_bytes > ((int64_t)1 << 30)) return SI_ERR_DIM;
+  if (n * ((page_bytes + 16383) / 16384) >= ((int64_t)1 << 31)) return SI_ERR_DIM;
+  return aligned16(pages) ? SI_OK : SI_ERR_ALIGN;
+}
+
+int status(cudaError_t e) { return e == cudaSuccess ? SI_OK : SI_ERR_CUDA; }
+
+}  // namespace
+}  // namespace si
+
+using namespace si;
+
+extern "C" {
+
+// ------------------------------------------------------------ window attention
+int si_window_attention_workspace_size(int B, int S, int T, int H, int H_k, int d, int window,
+                                       int sinks, const si_options* opt, size_t* bytes) {
+  if (!bytes) return SI_ERR_NULL;
+  RowsParams p{};
+  Opts o;
+  size_t need = 0;
+  const int rc = window_problem(B, S, T, H, H_k, d, window, sinks, opt, &p, &o, &need);
+  if (rc == SI_OK) *bytes = need;
+  return rc;
+}
+
+int si_window_attention(const void* qa, const void* ka, const void* va, const int32_t* lens,
+                        const int32_t* q_lens, int B, int S, int T, int H, int H_k, int d,
+                        int window, int sinks, float scale, void* out, float* lse,
+                        const si_options* opt, void* workspace, size_t ws_bytes, void* stream) {
+  if (!qa || !ka || !va || !out) return SI_ERR_NULL;
+  RowsParams p{};
+  Opts o;
+  size_t need = 0;
+  int rc = window_problem(B, S, T, H, H_k, d, window, sinks, opt, &p, &o, &need);
+  if (rc) return rc;
+  if (!(scale >= 0.0f) || scale == INFINITY) return SI_ERR_OPTIONS;
+  if (!aligned16(qa) || !aligned16(ka) || !aligned16(va) || !aligned16(out) || !aligned4(lens) ||
+      !aligned4(q_lens) || !aligned4(lse))
+    return SI_ERR_ALIGN;
+  if ((rc = place_partials(&p, d, need, workspace, ws_bytes))) return rc;
+  DevInfo* dev;
+  if ((rc = dev_info(&dev))) return rc;
+  p.q = static_cast<const uint16_t*>(qa);
+  p.k = static_cast<const uint16_t*>(ka);
+  p.v = static_cast<const uint16_t*>(va);
+  p.out = static_cast<uint16_t*>(out);
+  p.lse = lse;
+  p.lens = lens;
+  p.q_lens = q_lens;
+  p.scale_log2 = scale * 1.4426950408889634f;
+  p.v_scale = 1.0f;
+  return status(launch_attn_rows(p, d, static_cast<cudaStream_t>(stream)));
+}
+
+// ------------------------------------------------------------ 4-bit cache
+int si_cache4_page_bytes(int H_k, int d, int page, size_t* bytes) {
+  if (!bytes) return SI_ERR_NULL;
+  if (H_k < 1 || H_k > (1 << 16) || !(d == 64 || d == 128) || page_shift_of(page, 16, 256) < 0)
+    return SI_ERR_DIM;
+  *bytes = (size_t)H_k * page * (d + d / 8);
+  return SI_OK;
+}
+
+int si_cache4_append(const void* k, const void* v, int B, int S, int H_k, int d, void* pages,
+                     int n_pages, const int32_t* table, int width, int page, const int32_t* lens,
+                     const int32_t* q_lens, float k_scale, float v_scale, void* stream) {
+  if (!k || !v || !pages || !table || !lens) return SI_ERR_NULL;
+  Cache4Params p{};
+  int rc = cache4_rows(B, S, H_k, d, n_pages, width, page, k_scale, v_scale, &p);
+  if (rc) return rc;
+  if (!aligned16(k) || !aligned16(v) || !aligned16(pages) || !aligned4(table) ||
+      !aligned4(lens) || !aligned4(q_lens))
+    return SI_ERR_ALIGN;
+  DevInfo* dev;
+  if ((rc = dev_info(&dev))) return rc;
+  p.pages = static_cast<uint8_t*>(pages);
+  p.table = table;
+  p.lens = lens;
+  p.q_lens = q_lens;
+  p.k = static_cast<const uint16_t*>(k);
+  p.v = static_cast<const uint16_t*>(v);
+  return status(launch_cache4_rows(p, d, true, static_cast<cudaStream_t>(stream)));
+}
+
+int si_cache4_read(void* k, void* v, int B, int S, int H_k, int d, const void* pages, int n_pages,
+                   const int32_t* table, int width, int page, const int32_t* lens,
+                   const int32_t* q_lens, float k_scale, float v_scale, void* stream) {
+  if (!k || !v || !pages || !table || !lens) return SI_ERR_NULL;
+  Cache4Params p{};
+  int rc = cache4_rows(B, S, H_k, d, n_pages, width, page, k_scale, v_scale, &p);
+  if (rc) return rc;
+  if (!aligned16(k) || !aligned16(v) || !aligned16(pages) || !aligned4(table) ||
+      !aligned4(lens) || !aligned4(q_lens))
+    return SI_ERR_ALIGN;
+  DevInfo* dev;
+  if ((rc = dev_info(&dev))) return rc;
+  p.pages = const_cast<uint8_t*>(static_cast<const uint8_t*>(pages));
+  p.table = table;
+  p.lens = lens;
+  p.q_lens = q_lens;
+  p.k_out = static_cast<uint16_t*>(k);
+  p.v_out = static_cast<uint16_t*>(v);
+  return status(launch_cache4_rows(p, d, false, static_cast<cudaStream_t>(stream)));
+}
+
+int si_cache4_attention_workspace_size(int width, int page, int topk, int B, int S, int H, int H_k,
+                                       int d, int window, int sinks, const si_options* opt,
+                                       size_t* bytes) {
+  if (!bytes) return SI_ERR_NULL;
+  RowsParams p{};
+  Opts o;
+  size_t need = 0;
+  const int rc =
+      cache4_problem(width, page, topk, B, S, H, H_k, d, window, sinks, opt, &p, &o, &need);
+  if (rc == SI_OK) *bytes = need;
+  return rc;
+}
+
+int si_cache4_attention(const void* qa, const void* pages, int n_pages, const int32_t* table,
+                        int width, int page, const int32_t* lens, const int32_t* q_lens,
+                        const int32_t* idx, int topk, int B, int S, int H, int H_k, int d,
+                        int window, int sinks, float scale, float k_scale, float v_scale,
+                        void* out, float* lse, const si_options* opt, void* workspace,
+                        size_t ws_bytes, void* stream) {
+  if (!qa || !pages || !table || !lens || !out) return SI_ERR_NULL;
+  if (idx ? topk < 1 : topk != 0) return SI_ERR_TOPK;
+  if (n_pages < 1) return SI_ERR_DIM;
+  RowsParams p{};
+  Opts o;
+  size_t need = 0;
+  int rc = cache4_problem(width, page, topk, B, S, H, H_k, d, window, sinks, opt, &p, &o, &need);
+  if (rc) return rc;
+  if (!(scale >= 0.0f) || scale == INFINITY || !scale_ok(k_scale) || !scale_ok(v_scale))
+    return SI_ERR_OPTIONS;
+  if (!aligned16(qa) || !aligned16(pages) || !aligned16(out) || !aligned4(table) ||
+      !aligned4(lens) || !aligned4(q_lens) || !aligned4(idx) || !aligned4(lse))
+    return SI_ERR_ALIGN;
+  if ((rc = place_partials(&p, d, need, workspace, ws_bytes))) return rc;
+  DevInfo* dev;
+  if ((rc = dev_info(&dev))) return rc;
+  p.q = static_cast<const uint16_t*>(qa);
+  p.pages = static_cast<const uint8_t*>(pages);
+  p.n_pages = n_pages;
+  p.table = table;
+  p.lens = lens;
+  p.q_lens = q_lens;
+  p.idx = idx;
+  p.out = static_cast<uint16_t*>(out);
+  p.lse = lse;
+  p.scale_log2 = scale * k_scale * 1.4426950408889634f;
+  p.v_scale = v_scale;
+  return status(launch_attn_rows(p, d, static_cast<cudaStream_t>(stream)));
+}
+
+// ------------------------------------------------------------ pages
+int si_cache_workspace_size(int n_pages, int B, int n, size_t* bytes) {
+  if (!bytes) return SI_ERR_NULL;
+  if (n_pages < 1 || B < 1 || n < 0) return SI_ERR_DIM;
+  *bytes = pages_layout(n_pages, B, n).total;
+  return SI_OK;
+}
+
+int si_cache_extend(int32_t* refs, int n_pages, int32_t* table, int B, int width,
+                    const int32_t* lens, int page, int32_t* missing, void* workspace,
+                    size_t ws_bytes, void* stream) {
+  if (!refs || !table || !lens || !missing) return SI_ERR_NULL;
+  PagesParams p{};
+  int rc = pages_call(refs, n_pages, table, B, width, const_cast<int32_t*>(lens), page, &p);
+  if (rc) return rc;
+  if (!aligned4(missing)) return SI_ERR_ALIGN;
+  if ((rc = place_pages(&p, workspace, ws_bytes))) return rc;
+  DevInfo* dev;
+  if ((rc = dev_info(&dev))) return rc;
+  p.missing = missing;
+  return status(launch_pages_extend(p, static_cast<cudaStream_t>(stream)));
+}
+
+int si_cache_fork(void* pages, int64_t page_bytes, int32_t* refs, int n_pages, int32_t* table,
+                  int B, int width, int32_t* lens, const int32_t* src, const int32_t* dst, int n,
+                  int page, int32_t* missing, void* workspace, size_t ws_bytes, void* stream) {
+  if (!pages || !refs || !table || !lens || !missing || (n > 0 && (!src || !dst)))
+    return SI_ERR_NULL;
+  if (n < 0) return SI_ERR_DIM;
+  PagesParams p{};
+  int rc = pages_call(refs, n_pages, table, B, width, lens, page, &p);
+  if (rc) return rc;
+  if ((rc = check_pages(pages, page_bytes, n))) return rc;
+  if (!aligned4(missing) || !aligned4(src) || !aligned4(dst)) return SI_ERR_ALIGN;
+  p.pages = static_cast<uint8_t*>(pages);
+  p.page_bytes = page_bytes;
+  p.src = src, p.dst = dst, p.n = n;
+  p.missing = missing;
+  if ((rc = place_pages(&p, workspace, ws_bytes))) return rc;
+  DevInfo* dev;
+  if ((rc = dev_info(&dev))) return rc;
+  return status(launch_pages_fork(p, static_cast<cudaStream_t>(stream)));
+}
+
+int si_cache_free(int32_t* refs, int n_pages, int32_t* table, int B, int width, int32_t* lens,
+                  const int32_t* rows, int n, void* stream) {
+  if (!refs || !table || !lens || (n > 0 && !rows)) return SI_ERR_NULL;
+  if (n < 0) return SI_ERR_DIM;
+  PagesParams p{};
+  int rc = pages_call(refs, n_pages, table, B, width, lens, 1, &p);
+  if (rc) return rc;
+  if (!aligned4(rows)) return SI_ERR_ALIGN;
+  p.rows = rows;
+  p.n = n;
+  DevInfo* dev;
+  if ((rc = dev_info(&dev))) return rc;
+  return status(launch_pages_free(p, static_cast<cudaStream_t>(stream)));
+}
+
+int si_cache_compact(void* pages, int64_t page_bytes, const int32_t* refs, int n_pages,
+                     const int32_t* table, int B, int width, int32_t* refs_out,
+                     int32_t* table_out, int32_t* live, void* workspace, size_t ws_bytes,
+                     void* stream) {
+  if (!pages || !refs || !table || !refs_out || !table_out || !live) return SI_ERR_NULL;
+  int rc = check_pool(n_pages, B, width);
+  if (rc) return rc;
+  if ((rc = check_pages(pages, page_bytes, 1))) return rc;
+  if (!aligned4(refs) || !aligned4(table) || !aligned4(refs_out) || !aligned4(table_out) ||
+      !aligned4(live))
+    return SI_ERR_ALIGN;
+  PagesParams p{};
+  p.pages = static_cast<uint8_t*>(pages);
+  p.page_bytes = page_bytes;
+  p.refs = const_cast<int32_t*>(refs);
+  p.n_pages = n_pages;
+  p.table = const_cast<int32_t*>(table);
+  p.B = B, p.width = width;
+  p.refs_out = refs_out, p.table_out = table_out;
+  p.missing = live;
+  if ((rc = place_pages(&p, workspace, ws_bytes))) return rc;
+  DevInfo* dev;
+  if ((rc = dev_info(&dev))) return rc;
+  return status(launch_pages_compact(p, dev->sms, static_cast<cudaStream_t>(stream)));
+}
+
+}  // extern "C"

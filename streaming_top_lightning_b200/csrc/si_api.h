@@ -1,0 +1,51 @@
+// Host helpers that the files of the C ABI share (defined in api.cu).
+#pragma once
+
+#include <cuda.h>
+#include <cuda_runtime.h>
+#include <stddef.h>
+#include <stdint.h>
+
+#include "streamindex.h"
+
+namespace si {
+
+struct DevInfo {
+  bool init = false;
+  bool ok = false;
+  int sms = 0;
+  int max_smem = 0;
+  uint32_t* err = nullptr;
+  unsigned long long* role = nullptr;  // profiling build: role counters
+};
+
+// The current device, checked to be an sm_100 part; SI_OK or an error.
+int dev_info(DevInfo** out);
+
+// Shared memory and SM count to plan with: the current device's, or the
+// sm_100 limits on a host with no usable device.
+void plan_limits(int* max_smem, int* sms);
+
+inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+
+inline size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
+
+// 2-D row-major [rows, cols] tensor map with a {box_inner, box_rows} box and
+// the given swizzle; out-of-range rows read as zero.
+int make_map(CUtensorMap* m, const void* base, CUtensorMapDataType dt, uint64_t rows,
+             uint64_t cols, uint32_t esz, uint32_t box_inner, uint32_t box_rows,
+             CUtensorMapSwizzle sw);
+
+struct Opts {
+  int key_chunk, scratch_mb, grid_ctas, timeout_ms, debug_flags, row_finish, key_tile,
+      strip_slots;
+  cudaEvent_t ev_begin, ev_end;
+  cudaEvent_t* ev_list;  // [2i], [2i+1] around query block i's score launch
+  int ev_count;
+  int plan_heads, plan_dim, plan_fp8;  // si_topk_scores: the fused kernel's plan
+};
+
+// The options of a call, checked; o may be null.
+int read_opts(const si_options* o, Opts* out);
+
+}  // namespace si

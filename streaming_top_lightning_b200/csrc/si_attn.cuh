@@ -1,0 +1,190 @@
+// Shared pieces of the attention kernels that read a key/value cache: which
+// keys a query sees, and small PTX wrappers.
+//
+// Query row i of batch b (i < q_len) sits at position t = len - q_len + i of a
+// sequence of len tokens, and sees key j when
+//   j <= t  and  j < len  and  (j > t - window  or  j < sinks).
+#pragma once
+
+#include <cuda_fp16.h>
+
+#include "si_common.cuh"
+#include "si_kernels.h"
+
+namespace si {
+
+SI_DEV float neg_inf() { return __int_as_float(0xFF800000); }
+
+SI_DEV bool sees(int j, int t, int len, int window, int sinks) {
+  return j <= t && j < len && (j > t - window || j < sinks);
+}
+
+SI_DEV int clampi(int x, int lo, int hi) { return x < lo ? lo : (x > hi ? hi : x); }
+
+// Length of sequence b and how many of the S query rows it has.
+SI_DEV int seq_len(const int32_t* lens, int b, int cap) {
+  return lens ? clampi(__ldg(lens + b), 0, cap) : cap;
+}
+
+// The keys that some query of a tile sees, [lo, end) and the sinks before it,
+// as steps of KS keys: first the sinks' steps, then those from `base` on (lo
+// rounded down to a step).
+struct KeySpan {
+  int lo, base, end, sink_end, sink_steps, steps;
+};
+
+template <int KS>
+SI_DEV KeySpan key_span(int t_min, int t_max, int len, int window, int sinks) {
+  KeySpan s;
+  s.end = min(len, t_max + 1);
+  s.lo = max(0, t_min - window + 1);
+  if (s.end <= 0) return KeySpan{0, 0, 0, 0, 0, 0};
+  s.base = s.lo / KS * KS;
+  if (s.base > s.end) s.base = s.end / KS * KS;
+  s.sink_end = min(min(sinks, s.base), s.end);
+  s.sink_steps = (s.sink_end + KS - 1) / KS;
+  s.steps = s.sink_steps + (s.end - s.base + KS - 1) / KS;
+  return s;
+}
+
+// First key of a step, and whether a key of it is one that the span holds.
+template <int KS>
+SI_DEV int step_key(const KeySpan& s, int u) {
+  return u < s.sink_steps ? u * KS : s.base + (u - s.sink_steps) * KS;
+}
+SI_DEV bool span_holds(const KeySpan& s, int u, int j, int sinks) {
+  return u < s.sink_steps ? j < s.sink_end : (j < s.end && (j >= s.lo || j < sinks));
+}
+
+SI_DEV void cp_async16(uint32_t dst, const void* src, uint32_t bytes) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes)
+               : "memory");
+}
+template <int N>
+SI_DEV void cp_async_small(uint32_t dst, const void* src, uint32_t bytes) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(dst), "l"(src), "n"(N),
+               "r"(bytes)
+               : "memory");
+}
+SI_DEV void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+SI_DEV void cp_async_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+SI_DEV float bf16_lo(uint32_t w) { return __uint_as_float(w << 16); }
+SI_DEV float bf16_hi(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
+SI_DEV uint32_t pack_bf16x2(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+SI_DEV uint32_t pack_f16x2(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+// 2^x, -inf to 0.
+SI_DEV float ex2(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+
+// D (+)= A B, 16 x 8 x 16, fp32 accumulation.
+SI_DEV void mma_f16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+      "{%0,%1,%2,%3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+SI_DEV void mma_bf16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+      "{%0,%1,%2,%3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+SI_DEV void ldmatrix4(uint32_t (&r)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+SI_DEV void ldmatrix4_t(uint32_t (&r)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+
+// Two E2M1 numbers of a byte, and two E4M3 numbers of a half-word, as fp16
+// (both exact; the lower bits give the lower half).
+template <int BYTE>
+SI_DEV uint32_t e2m1x2(uint32_t w) {
+  uint32_t r;
+  asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\t"
+      "mov.b32 {b0, b1, b2, b3}, %1;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %0, b%2;\n\t}"
+      : "=r"(r)
+      : "r"(w), "n"(BYTE));
+  return r;
+}
+SI_DEV uint32_t e4m3x2(uint32_t w) {
+  uint32_t r;
+  asm("{\n\t.reg .b16 lo, hi;\n\t"
+      "mov.b32 {lo, hi}, %1;\n\t"
+      "cvt.rn.f16x2.e4m3x2 %0, lo;\n\t}"
+      : "=r"(r)
+      : "r"(w));
+  return r;
+}
+SI_DEV uint32_t hmul2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+
+// The block of one kv head in a 4-bit page: K codes, V codes, K scales, V
+// scales, each [page, ...].
+template <int D>
+SI_DEV int64_t cache4_block(int page) {
+  return (int64_t)page * (D + D / 8);
+}
+
+// One query row by the formula, by a whole warp: the keys [j_lo, j_hi) of a
+// bf16 source that the row sees, D/32 dims per lane.  Kernels that multiply
+// whole tiles give a row NaN when a key that it does not see holds an infinity
+// or NaN (0 times that value); such rows are computed again here.
+template <int D>
+SI_DEV void exact_row_keys(const uint16_t* qr, const uint16_t* k, const uint16_t* v,
+                           int64_t key_stride, int j_lo, int j_hi, int t, int len, int window,
+                           int sinks, float scale_log2, int lane, float& m, float& l,
+                           float (&o)[D / 32]) {
+  for (int j = j_lo; j < j_hi; ++j) {
+    if (!sees(j, t, len, window, sinks)) continue;
+    float dot = 0.0f;
+#pragma unroll
+    for (int e = 0; e < D / 32; ++e) {
+      const int d = lane * (D / 32) + e;
+      dot = fmaf(__uint_as_float((uint32_t)qr[d] << 16),
+                 __uint_as_float((uint32_t)k[j * key_stride + d] << 16), dot);
+    }
+#pragma unroll
+    for (int x = 16; x > 0; x >>= 1) dot += __shfl_xor_sync(0xFFFFFFFFu, dot, x);
+    const float s = dot * scale_log2;
+    const float mn = fmaxf(m, s);  // ignores a NaN score, which makes the weight NaN below
+    const float a = mn == neg_inf() ? 1.0f : ex2(m - mn);
+    const float w = mn == neg_inf() && s == s ? 0.0f : ex2(s - mn);
+    l = l * a + w;
+#pragma unroll
+    for (int e = 0; e < D / 32; ++e) {
+      const float vv = __uint_as_float((uint32_t)v[j * key_stride + lane * (D / 32) + e] << 16);
+      o[e] = fmaf(o[e], a, w * vv);
+    }
+    m = mn;
+  }
+}
+
+}  // namespace si

@@ -107,6 +107,74 @@ cudaError_t launch_sort_rows(int32_t* idx, float* score, int64_t rows, int K, in
 cudaError_t launch_quantize_fp8(const uint16_t* x, int64_t rows, int cols, uint8_t* x8,
                                 float* scale, cudaStream_t stream);
 
+// Attention of few query rows over a key/value cache (k_attn_rows.cu).
+struct RowsParams {
+  const uint16_t* q;   // [B,S,H,D] bf16
+  uint16_t* out;       // [B,S,H,D] bf16
+  float* lse;          // [B,S,H] fp32, or null
+  const uint16_t *k, *v;  // bf16 keys and values [B,T,Hk,D]; null: 4-bit pages
+  const uint8_t* pages;   // [n_pages, page_bytes]
+  const int32_t* table;   // [B, width] pages of each sequence
+  int width, n_pages, page_shift;
+  int64_t page_bytes;
+  const int32_t* idx;  // [B,S,topk] listed entries, or null: the keys a query sees
+  int topk;
+  const int32_t* lens;    // [B] tokens of each sequence, or null: T
+  const int32_t* q_lens;  // [B] its query rows, or null: S
+  int B, S, T, H, Hk, G;
+  int window, sinks;   // window <= 2^30
+  float scale_log2;    // softmax scale (and K scale) times log2(e)
+  float v_scale;
+  int tiles, splits;   // row tiles per kv head; CTAs that share a tile's keys
+  float* part_o;       // splits > 1: [B*Hk*S*G, splits, D] partial sums
+  float2* part_ml;     //             [B*Hk*S*G, splits] (maximum in log2 units, sum)
+};
+cudaError_t launch_attn_rows(const RowsParams& p, int D, cudaStream_t stream);
+
+// Rows of a 4-bit paged cache (k_cache4.cu): append reads k, v [B,S,Hk,D]
+// bf16, read writes k_out, v_out of that shape.
+struct Cache4Params {
+  uint8_t* pages;
+  const int32_t* table;
+  const int32_t* lens;    // [B]
+  const int32_t* q_lens;  // [B], or null: S
+  int B, S, Hk, width, n_pages, page_shift;
+  int cap;                // tokens that a table row can hold
+  int64_t page_bytes;
+  const uint16_t *k, *v;
+  uint16_t *k_out, *v_out;
+  float k_scale, v_scale;
+};
+cudaError_t launch_cache4_rows(const Cache4Params& p, int D, bool append, cudaStream_t stream);
+
+// The life of a cache's pages (k_cache_pages.cu).
+struct ForkChild {
+  int32_t len;          // its length; -1: not made
+  int32_t full;         // pages shared with its parent
+  int32_t last, fresh;  // the parent's partly filled page and the copy, or -1
+};
+struct PagesParams {
+  uint8_t* pages;       // [n_pages, page_bytes]
+  int64_t page_bytes;
+  int32_t* refs;        // [n_pages]
+  int32_t* table;       // [B, width]
+  int32_t* lens;        // [B]
+  int B, width, n_pages, page_shift;
+  const int32_t *rows, *src, *dst;  // [n] rows of a call
+  int n;
+  int32_t* missing;     // extend, fork: what was not done; compact: live pages
+  int32_t *refs_out, *table_out;  // compact
+  // workspace
+  int32_t* order;       // extend, fork: [n_pages] pages taken, by rank
+  int32_t* claim;       // fork: [B]
+  ForkChild* child;     // fork: [n]
+  int32_t *lr, *hole, *mover, *mref, *moves;  // compact: [n_pages] each, [1]
+};
+cudaError_t launch_pages_extend(const PagesParams& p, cudaStream_t stream);
+cudaError_t launch_pages_free(const PagesParams& p, cudaStream_t stream);
+cudaError_t launch_pages_fork(const PagesParams& p, cudaStream_t stream);
+cudaError_t launch_pages_compact(const PagesParams& p, int sms, cudaStream_t stream);
+
 // Number of units (query tile x key chunk x batch) in a launch.
 int host_count_units(const UnitGrid& u);
 int host_tile_chunks(const UnitGrid& u, int g);
