@@ -1,6 +1,7 @@
 // The C ABI of the key/value cache (include/streamindex.h): attention with a
 // window and sinks, the 4-bit paged cache, and the life of its pages.
 #include <algorithm>
+#include <cfloat>
 #include <cmath>
 
 #include "si_api.h"
@@ -73,6 +74,13 @@ int place_partials(RowsParams* p, int d, size_t need, void* ws, size_t ws_bytes)
   return SI_OK;
 }
 
+// Whether a window call runs in 128-row tensor-core tiles: from so many
+// (query, head) rows per kv head on, unless the caller fixed key chunks.
+constexpr int kTileRows = 64;
+bool window_in_tiles(int S, int G, int key_chunk) {
+  return G <= 128 && (int64_t)S * G >= kTileRows && key_chunk == 0;
+}
+
 // Sizes of a window call and its plan.
 int window_problem(int B, int S, int T, int H, int H_k, int d, int window, int sinks,
                    const si_options* opt, RowsParams* p, Opts* o, size_t* bytes) {
@@ -84,6 +92,8 @@ int window_problem(int B, int S, int T, int H, int H_k, int d, int window, int s
   p->B = B, p->S = S, p->T = T, p->H = H, p->Hk = H_k, p->G = H / H_k;
   p->window = std::min(window, kWindowMax);
   p->sinks = std::min(sinks, kWindowMax);
+  *bytes = 0;
+  if (window_in_tiles(S, p->G, o->key_chunk)) return SI_OK;
   int max_smem = 0, sms = 0;
   plan_limits(&max_smem, &sms);
   return plan_rows(p, std::min<int64_t>(T, (int64_t)p->window + p->sinks), false, o->key_chunk,
@@ -242,7 +252,28 @@ int si_window_attention(const void* qa, const void* ka, const void* va, const in
   p.q_lens = q_lens;
   p.scale_log2 = scale * 1.4426950408889634f;
   p.v_scale = 1.0f;
-  return status(launch_attn_rows(p, d, static_cast<cudaStream_t>(stream)));
+  if (!window_in_tiles(S, p.G, o.key_chunk))
+    return status(launch_attn_rows(p, d, static_cast<cudaStream_t>(stream)));
+  if (window_tiles_smem(d) > (size_t)dev->max_smem) return SI_ERR_UNSUPPORTED;
+  WinParams w{};
+  w.q = p.q, w.k = p.k, w.v = p.v, w.out = p.out, w.lse = lse;
+  w.lens = lens, w.q_lens = q_lens;
+  w.B = B, w.S = S, w.T = T, w.H = H, w.Hk = H_k, w.G = p.G;
+  w.QT = 128 / p.G;
+  w.pairs = (int)(((int64_t)S + 2 * w.QT - 1) / (2 * w.QT));
+  w.items = (int64_t)B * H_k * w.pairs;
+  w.window = p.window, w.sinks = p.sinks;
+  w.scale_log2 = std::max(p.scale_log2, FLT_MIN);  // times -inf for an unseen key: not NaN
+  w.err = dev->err;
+  w.timeout_ns = (uint64_t)o.timeout_ms * 1000000ull;
+  CUtensorMap tm_q, tm_k, tm_v;
+  if ((rc = make_map4(&tm_q, qa, d, H, S, B, p.G, w.QT)) ||
+      (rc = make_map4(&tm_k, ka, d, H_k, T, B, 1, 32)) ||
+      (rc = make_map4(&tm_v, va, d, H_k, T, B, 1, 32)))
+    return rc;
+  const int most = o.grid_ctas > 0 ? o.grid_ctas : dev->sms;
+  return status(launch_window_tiles(tm_q, tm_k, tm_v, w, d, (int)std::min<int64_t>(most, w.items),
+                                    static_cast<cudaStream_t>(stream)));
 }
 
 // ------------------------------------------------------------ 4-bit cache

@@ -1,0 +1,541 @@
+// Window attention of many query rows (prompts and their chunks) on the tensor
+// cores.  The formula and the key rule are those of k_attn_rows.cu's bf16 path.
+//
+//   o[row] = sum_j softmax_j(scale * q[row] . k[j]) v[j] over j <= t with
+//            j > t - window or j < sinks
+//
+// What bounds it: 4 D operations per (row, key) pair on the tensor cores, and
+// as many cycles of exponentials (a 128 x 128 score tile takes 512 + 512 cycles
+// of MMA at D = 128, and 1,024 of the SM's 16 exponentials a cycle).  K and V
+// come from L2: neighbouring tiles share nearly all of their keys.
+//
+// The G = H / H_k query heads of a kv head share its keys, so a tile's 128 rows
+// are (query, head) pairs, 128 / G whole queries of them.  One persistent CTA
+// per SM takes two such tiles at a time over the union of their keys, so every
+// key block is loaded once for 256 rows, and the softmax of one tile runs while
+// the tensor cores work for the other:
+//   warp 0       K and V blocks by TMA into a ring, in the order of use
+//                (K0 V0 K1 V1 ...); rows of V past the sequence's end are
+//                overwritten with zeros (0 times whatever they hold would
+//                reach the sums)
+//   warp 2       the two Q tiles by TMA
+//   warp 1       S_i = Q_i K^T into TMEM, then O_i += P_i V with P_i read from
+//                TMEM: PV_0(n-1) S_0(n) PV_1(n-1) S_1(n) ...  An MMA's
+//                completion covers those before it, so when S_i(n) is there
+//                O_i holds everything up to n-1 and nobody writes it.
+//   warps 4-11   softmax, four warps a tile, a thread a row: the maximum over
+//                the tile's columns, then P = 2^(s - m) in bf16 over the first
+//                half of S's columns (the columns read by then), and the row's
+//                sum.  O is rescaled only when a row's maximum has grown by more
+//                than 2^8 since it was last fixed; P stays below 2^8, and the
+//                sum is over the same P's, so the result does not depend on it.
+// Keys are taken from the first one that the pair of tiles sees, 128 at a time,
+// the last block and the sinks' block cut to multiples of 32 columns, so a
+// window costs about its own length and not whole tiles of it.  Only columns
+// that a boundary crosses are compared with positions.
+//
+// A masked column's probability is 0, and 0 times an infinity or NaN in V is
+// NaN; a row that comes out NaN is computed again by the formula
+// (exact_row_keys), so what a row does not see does not reach it.
+// Every wait is bounded; a CTA that gives up records the error word, lets its
+// copies land and leaves.
+#include "si_attn.cuh"
+
+namespace si {
+namespace {
+
+constexpr int kM = 128;        // rows of a tile (MMA M)
+constexpr int kN = 128;        // keys of a block
+constexpr int kWinThreads = 384;
+constexpr int kSoftWarp = 4;   // softmax warps 4-7: tile 0, 8-11: tile 1
+constexpr float kGrow = 8.0f;  // log2 growth of a maximum that rescales O
+
+template <int D>
+struct WinCfg {
+  static constexpr uint32_t kBlock = kN * D * 2;  // one K, V or Q block
+  static constexpr uint32_t kHalf = kN * 128;     // its 64-column half
+  static constexpr int kSlots = D == 128 ? 5 : 8;
+  static constexpr size_t kSmem = (2 + kSlots) * (size_t)kBlock + 1024 + 512;
+};
+
+struct WinCtl {
+  uint64_t kv_full[8], kv_empty[8], kv_land;
+  uint64_t q_full, q_empty, s_full[2], p_ready[2], o_full[2];
+  uint32_t tmem_base;
+  uint32_t abort;
+};
+
+SI_DEV void fence_async() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+
+SI_DEV void tma_load_4d(uint32_t dst, const CUtensorMap* map, uint32_t bar, int c0, int c1, int c2,
+                        int c3) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
+      "[%0], [%1, {%3, %4, %5, %6}], [%2];" ::"r"(dst),
+      "l"(map), "r"(bar), "r"(c0), "r"(c1), "r"(c2), "r"(c3)
+      : "memory");
+}
+
+// D[tmem] (+)= A[tmem] * B[smem].
+SI_DEV void umma_ts_bf16(uint32_t d, uint32_t a, uint64_t bdesc, uint32_t idesc, uint32_t acc) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+      "r"(a), "l"(bdesc), "r"(idesc), "r"(acc)
+      : "memory");
+}
+
+SI_DEV uint64_t sdesc_mn(uint32_t saddr, uint32_t lbo_bytes) {
+  return (uint64_t)((saddr >> 4) & 0x3FFFu) | ((uint64_t)((lbo_bytes >> 4) & 0x3FFFu) << 16) |
+         ((uint64_t)64u << 32) | ((uint64_t)1u << 46) | ((uint64_t)2u << 61);
+}
+
+SI_DEV void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
+      "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
+      "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
+}
+SI_DEV void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+// Keeps values read from TMEM behind the wait for them.
+SI_DEV void pin32(float (&v)[32]) {
+#pragma unroll
+  for (int i = 0; i < 32; i += 8)
+    asm volatile("" : "+f"(v[i]), "+f"(v[i + 1]), "+f"(v[i + 2]), "+f"(v[i + 3]), "+f"(v[i + 4]),
+                 "+f"(v[i + 5]), "+f"(v[i + 6]), "+f"(v[i + 7]));
+}
+
+// A pair of tiles: its queries, their positions and the key blocks.
+struct WinItem {
+  int b, hk, i0;     // batch, kv head, first query
+  int len, q_len;
+  int nq[2];         // live queries of each tile (0: none)
+  int t0[2];         // position of each tile's first query
+  KeySpan span;      // of both tiles
+  int blocks, sink_blocks;
+};
+
+SI_DEV bool win_item(const WinParams& p, int64_t id, WinItem& it) {
+  const int pair = (int)(id % p.pairs);
+  const int64_t bh = id / p.pairs;
+  it.b = (int)(bh / p.Hk);
+  it.hk = (int)(bh % p.Hk);
+  it.i0 = pair * 2 * p.QT;
+  it.len = seq_len(p.lens, it.b, p.T);
+  it.q_len = seq_len(p.q_lens, it.b, p.S);
+  const int live = it.q_len - it.i0;
+  if (live <= 0) return false;
+  it.nq[0] = min(live, p.QT);
+  it.nq[1] = max(0, min(live - p.QT, p.QT));
+  it.t0[0] = it.len - it.q_len + it.i0;
+  it.t0[1] = it.t0[0] + p.QT;
+  it.span = key_span<1>(it.t0[0], it.t0[0] + it.nq[0] + it.nq[1] - 1, it.len, p.window, p.sinks);
+  it.sink_blocks = (it.span.sink_end + kN - 1) / kN;
+  it.blocks = it.sink_blocks + (it.span.end - it.span.base + kN - 1) / kN;
+  return true;
+}
+
+// First key of block n, the keys it holds, and its columns (a multiple of 32).
+SI_DEV int block_key(const WinItem& it, int n) {
+  return n < it.sink_blocks ? n * kN : it.span.base + (n - it.sink_blocks) * kN;
+}
+SI_DEV int block_keys(const WinItem& it, int n) {
+  return min(kN, (n < it.sink_blocks ? it.span.sink_end : it.span.end) - block_key(it, n));
+}
+SI_DEV int columns(int keys) { return (keys + 31) & ~31; }
+
+// Whether tile i sees a key of block n.
+SI_DEV bool tile_sees(const WinParams& p, const WinItem& it, int i, int n) {
+  if (it.nq[i] == 0) return false;
+  const int j0 = block_key(it, n), j1 = j0 + block_keys(it, n) - 1;
+  const int ta = it.t0[i], tb = ta + it.nq[i] - 1;
+  return j0 <= tb && (n < it.sink_blocks || j1 > ta - p.window || j0 < p.sinks);
+}
+
+}  // namespace
+
+template <int D>
+__global__ void __launch_bounds__(kWinThreads, 1)
+    k_window_tiles(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
+                   const __grid_constant__ CUtensorMap tm_v, const WinParams p) {
+  using C = WinCfg<D>;
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                             ~uintptr_t(1023));
+  // [Q0 | Q1 | ring | ctl]
+  const uint32_t base = smem_u32(smem);
+  const uint32_t ring = base + 2 * C::kBlock;
+  WinCtl* cs = reinterpret_cast<WinCtl*>(smem + (2 + C::kSlots) * (size_t)C::kBlock);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+
+  if (tid == 0) {
+    for (int i = 0; i < C::kSlots; ++i) {
+      mbar_init(smem_u32(&cs->kv_full[i]), 1);
+      mbar_init(smem_u32(&cs->kv_empty[i]), 1);
+    }
+    mbar_init(smem_u32(&cs->kv_land), 1);
+    mbar_init(smem_u32(&cs->q_full), 1);
+    mbar_init(smem_u32(&cs->q_empty), 1);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(smem_u32(&cs->s_full[i]), 1);
+      mbar_init(smem_u32(&cs->p_ready[i]), kM);
+      mbar_init(smem_u32(&cs->o_full[i]), 1);
+    }
+    cs->abort = 0u;
+    mbar_fence_init();
+  }
+  if (warp == 1) {
+    tmem_alloc(smem_u32(&cs->tmem_base), 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = cs->tmem_base;
+  const Ctl ctl{p.err, &cs->abort, p.timeout_ns, nullptr};
+
+  if (warp == 0) {
+    // ------------------------------------------------------------ K and V
+    uint32_t at = 0, lands = 0;  // blocks issued; blocks mended
+    bool ok = true;
+    for (int64_t id = blockIdx.x; ok && id < p.items; id += gridDim.x) {
+      WinItem it;
+      if (!win_item(p, id, it)) continue;
+      for (int x = 0; ok && x < 2 * it.blocks; ++x, ++at) {
+        const int n = x >> 1;
+        const bool is_v = (x & 1) != 0;
+        const int slot = (int)(at % C::kSlots);
+        if (!mbar_wait_warp(smem_u32(&cs->kv_empty[slot]), ((at / C::kSlots) & 1u) ^ 1u, ctl)) {
+          ok = false;
+          break;
+        }
+        const int j0 = block_key(it, n), cols = columns(block_keys(it, n));
+        const uint32_t dst = ring + slot * C::kBlock;
+        // keys past the sequence's end lie in the block's last columns
+        const bool mend = is_v && j0 + cols > it.len;
+        const uint32_t bar = smem_u32(mend ? &cs->kv_land : &cs->kv_full[slot]);
+        if (lane == 0) {
+          mbar_arrive_expect_tx(bar, (uint32_t)cols * D * 2);
+          for (int c = 0; c < cols; c += 32)
+#pragma unroll
+            for (int h = 0; h < D / 64; ++h)
+              tma_load_4d(dst + h * C::kHalf + c * 128, is_v ? &tm_v : &tm_k, bar, 64 * h, it.hk,
+                          j0 + c, it.b);
+        }
+        __syncwarp();
+        if (mend) {
+          if (!mbar_wait_warp(bar, lands & 1u, ctl)) {
+            ok = false;
+            break;
+          }
+          ++lands;
+          // whole 128-byte rows, so the swizzle does not matter
+          const int first = max(0, it.len - j0);
+          for (int y = lane; y < (cols - first) * 8 * (D / 64); y += 32) {
+            const int h = y / ((cols - first) * 8), z = y % ((cols - first) * 8);
+            asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(
+                             dst + h * C::kHalf + first * 128 + z * 16),
+                         "r"(0)
+                         : "memory");
+          }
+          fence_async();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(smem_u32(&cs->kv_full[slot]));
+        }
+      }
+    }
+    if (*ctl.abort && lane == 0) {
+      // let the copies in flight land before the CTA leaves
+      const uint64_t t_end = globaltimer() + 1000000ull;
+      for (uint32_t x = at > C::kSlots ? at - C::kSlots : 0; x < at; ++x)
+        while (!mbar_try_wait(smem_u32(&cs->kv_full[x % C::kSlots]), (x / C::kSlots) & 1u) &&
+               globaltimer() < t_end) {
+        }
+    }
+  } else if (warp == 2) {
+    // ------------------------------------------------------------ Q
+    if (lane == 0) {
+      uint32_t n = 0;
+      for (int64_t id = blockIdx.x; id < p.items; id += gridDim.x) {
+        WinItem it;
+        if (!win_item(p, id, it) || it.blocks == 0) continue;
+        if (!mbar_wait(smem_u32(&cs->q_empty), (n & 1u) ^ 1u, ctl)) break;
+        ++n;
+        const int tiles = it.nq[1] > 0 ? 2 : 1;
+        const uint32_t bar = smem_u32(&cs->q_full);
+        mbar_arrive_expect_tx(bar, (uint32_t)(tiles * p.QT * p.G * D * 2));
+        for (int i = 0; i < tiles; ++i)
+#pragma unroll
+          for (int h = 0; h < D / 64; ++h)
+            tma_load_4d(base + i * C::kBlock + h * C::kHalf, &tm_q, bar, 64 * h, it.hk * p.G,
+                        it.i0 + i * p.QT, it.b);
+      }
+      if (*ctl.abort && n > 0) {
+        const uint64_t t_end = globaltimer() + 1000000ull;
+        while (!mbar_try_wait(smem_u32(&cs->q_full), (n - 1) & 1u) && globaltimer() < t_end) {
+        }
+      }
+    }
+    __syncwarp();
+  } else if (warp == 1) {
+    // ------------------------------------------------------------ MMA
+    if (lane == 0) {
+      constexpr uint32_t idesc_o = idesc_make(1, 1, kM, D) | (1u << 16);  // V is MN-major
+      uint32_t at = 0, items = 0, np[2] = {0, 0};
+      bool ok = true;
+      for (int64_t id = blockIdx.x; ok && id < p.items; id += gridDim.x) {
+        WinItem it;
+        if (!win_item(p, id, it) || it.blocks == 0) continue;
+        if (!mbar_wait(smem_u32(&cs->q_full), items & 1u, ctl)) break;
+        ++items;
+        bool begun[2] = {false, false};
+        int last[2] = {-1, -1};
+        for (int n = 0; n < it.blocks; ++n)
+          for (int i = 0; i < 2; ++i)
+            if (tile_sees(p, it, i, n)) last[i] = n;
+        for (int n = 0; ok && n <= it.blocks; ++n) {
+          const uint32_t kb = at + 2 * n, vb = at + 2 * n - 1;  // this K block, the V before it
+          const int ks = (int)(kb % C::kSlots), vs = (int)(vb % C::kSlots);
+          if (n > 0 && !mbar_wait(smem_u32(&cs->kv_full[vs]), (vb / C::kSlots) & 1u, ctl)) {
+            ok = false;
+            break;
+          }
+          bool k_in = false;
+          for (int i = 0; ok && i < 2; ++i) {
+            if (n > 0 && tile_sees(p, it, i, n - 1)) {
+              if (!mbar_wait(smem_u32(&cs->p_ready[i]), np[i] & 1u, ctl)) {
+                ok = false;
+                break;
+              }
+              ++np[i];
+              tc_fence_after();
+              const uint32_t va = ring + vs * C::kBlock;
+              const int steps = columns(block_keys(it, n - 1)) / 16;
+              for (int kk = 0; kk < steps; ++kk)
+                umma_ts_bf16(tmem + 256 + i * 128, tmem + i * 128 + kk * 8,
+                             sdesc_mn(va + kk * 2048, C::kHalf), idesc_o,
+                             (kk > 0 || begun[i]) ? 1u : 0u);
+              begun[i] = true;
+              if (last[i] == n - 1) umma_commit(smem_u32(&cs->o_full[i]));
+            }
+            if (n < it.blocks && tile_sees(p, it, i, n)) {
+              if (!k_in && !mbar_wait(smem_u32(&cs->kv_full[ks]), (kb / C::kSlots) & 1u, ctl)) {
+                ok = false;
+                break;
+              }
+              k_in = true;
+              tc_fence_after();
+              const uint32_t ka = ring + ks * C::kBlock, qa = base + i * C::kBlock;
+              const uint32_t idesc_s =
+                  idesc_make(1, 1, kM, (uint32_t)columns(block_keys(it, n)));
+#pragma unroll
+              for (int kk = 0; kk < D / 16; ++kk) {
+                const uint32_t off = (kk >> 2) * C::kHalf + (kk & 3) * 32;
+                umma_bf16(tmem + i * 128, sdesc_sw128(qa + off), sdesc_sw128(ka + off), idesc_s,
+                          kk > 0 ? 1u : 0u);
+              }
+              umma_commit(smem_u32(&cs->s_full[i]));
+            }
+          }
+          // a slot is given back only once it has been filled
+          if (ok && n < it.blocks && !k_in)
+            ok = mbar_wait(smem_u32(&cs->kv_full[ks]), (kb / C::kSlots) & 1u, ctl);
+          if (!ok) break;
+          if (n > 0) umma_commit(smem_u32(&cs->kv_empty[vs]));
+          if (n < it.blocks) umma_commit(smem_u32(&cs->kv_empty[ks]));
+          if (n == it.blocks - 1) umma_commit(smem_u32(&cs->q_empty));
+        }
+        at += 2 * it.blocks;
+      }
+    }
+    __syncwarp();
+  } else if (warp >= kSoftWarp) {
+    // ------------------------------------------------------------ softmax
+    const int i = (warp - kSoftWarp) >> 2;
+    const int row = (warp & 3) * 32 + lane;
+    const uint32_t lane_base = tmem + ((uint32_t)((warp & 3) * 32) << 16);
+    const uint32_t s_col = lane_base + i * 128, o_col = lane_base + 256 + i * 128;
+    const float sl2 = p.scale_log2;
+    uint32_t ns = 0, no = 0;
+    bool stop = false;
+    for (int64_t id = blockIdx.x; !stop && id < p.items; id += gridDim.x) {
+      WinItem it;
+      if (!win_item(p, id, it) || it.nq[i] == 0) continue;
+      const int qi = row / p.G;  // query of the row within the tile
+      const int ta = it.t0[i], tb = ta + it.nq[i] - 1;
+      const int t = ta + min(qi, it.nq[i] - 1);
+      float m = neg_inf(), l = 0.0f;
+      bool any = false;
+      for (int n = 0; n < it.blocks; ++n) {
+        if (!tile_sees(p, it, i, n)) continue;
+        if (!mbar_wait_warp(smem_u32(&cs->s_full[i]), ns & 1u, ctl)) {
+          stop = true;
+          break;
+        }
+        ++ns;
+        tc_fence_after();
+        const int j0 = block_key(it, n), keys = block_keys(it, n), chunks = columns(keys) / 32;
+        // whether every row of the tile sees all of chunk c
+        auto whole = [&](int c) {
+          const int a = j0 + 32 * c, z = a + 31;
+          return 32 * c + 32 <= keys && z <= ta && (a > tb - p.window || z < p.sinks);
+        };
+        auto mask = [&](int c, float (&v)[32]) {
+#pragma unroll
+          for (int e = 0; e < 32; ++e) {
+            const int j = j0 + 32 * c + e;
+            if (32 * c + e >= keys || !sees(j, t, it.len, p.window, p.sinks)) v[e] = neg_inf();
+          }
+        };
+        float v[32], mx[4] = {neg_inf(), neg_inf(), neg_inf(), neg_inf()};
+#pragma unroll 1
+        for (int c = 0; c < chunks; ++c) {
+          tmem_ld32(s_col + c * 32, v);
+          tmem_ld_wait();
+          pin32(v);
+          if (!whole(c)) mask(c, v);
+#pragma unroll
+          for (int e = 0; e < 32; ++e) mx[e & 3] = fmaxf(mx[e & 3], v[e]);
+        }
+        const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * sl2;
+        // the first maximum is taken as it is; later ones once they pass it by 2^8
+        const bool grow = top > (m == neg_inf() ? m : m + kGrow);
+        if (__any_sync(0xFFFFFFFFu, grow)) {
+          const float a = grow ? ex2(m - top) : 1.0f;
+          if (any) {
+            l *= a;
+#pragma unroll 1
+            for (int c = 0; c < D / 32; ++c) {
+              tmem_ld32(o_col + c * 32, v);
+              tmem_ld_wait();
+              pin32(v);
+#pragma unroll
+              for (int e = 0; e < 32; ++e) v[e] *= a;
+              uint32_t w[2][16];
+#pragma unroll
+              for (int e = 0; e < 32; ++e) w[e >> 4][e & 15] = __float_as_uint(v[e]);
+              tmem_st16(o_col + c * 32, w[0]);
+              tmem_st16(o_col + c * 32 + 16, w[1]);
+            }
+            tmem_st_wait();
+          }
+          if (grow) m = top;
+        }
+        any = true;
+        const float sub = m == neg_inf() ? 0.0f : m;
+        float ls[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll 1
+        for (int c = 0; c < chunks; ++c) {
+          tmem_ld32(s_col + c * 32, v);
+          tmem_ld_wait();
+          pin32(v);
+          if (!whole(c)) mask(c, v);
+          uint32_t w[16];
+#pragma unroll
+          for (int e = 0; e < 32; e += 2) {
+            const float x = ex2(fmaf(v[e], sl2, -sub)), y = ex2(fmaf(v[e + 1], sl2, -sub));
+            ls[(e >> 1) & 3] += x + y;
+            w[e >> 1] = pack_bf16x2(x, y);
+          }
+          tmem_st16(s_col + c * 16, w);
+        }
+        l += (ls[0] + ls[1]) + (ls[2] + ls[3]);
+        tmem_st_wait();
+        tc_fence_before();
+        mbar_arrive(smem_u32(&cs->p_ready[i]));
+      }
+      if (stop) break;
+      const bool live = qi < it.nq[i];
+      const int64_t orow =
+          ((int64_t)it.b * p.S + it.i0 + i * p.QT + qi) * p.H + it.hk * p.G + row % p.G;
+      bool bad = false;
+      if (any) {
+        if (!mbar_wait_warp(smem_u32(&cs->o_full[i]), no & 1u, ctl)) break;
+        ++no;
+        tc_fence_after();
+        const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+        float v[32];
+#pragma unroll 1
+        for (int c = 0; c < D / 32; ++c) {
+          tmem_ld32(o_col + c * 32, v);
+          tmem_ld_wait();
+          pin32(v);
+          uint32_t w[16];
+#pragma unroll
+          for (int e = 0; e < 32; e += 2) {
+            const float x = v[e] * inv, y = v[e + 1] * inv;
+            bad |= x != x || y != y;
+            w[e >> 1] = pack_bf16x2(x, y);
+          }
+          if (live) {
+            uint4* dst = reinterpret_cast<uint4*>(p.out + orow * D + c * 32);
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              dst[e] = make_uint4(w[4 * e], w[4 * e + 1], w[4 * e + 2], w[4 * e + 3]);
+          }
+        }
+        tc_fence_before();
+      } else if (live) {
+        for (int c = 0; c < D / 8; ++c)
+          reinterpret_cast<uint4*>(p.out + orow * D)[c] = make_uint4(0u, 0u, 0u, 0u);
+      }
+      if (live && p.lse)
+        p.lse[orow] = l == 0.0f ? neg_inf() : (m + log2f(l)) * 0.6931471805599453f;
+      // rows by the formula (see the head of the file)
+      __syncwarp();
+      uint32_t again = __ballot_sync(0xFFFFFFFFu, bad && live);
+      while (again) {
+        const int r = __ffs(again) - 1;
+        again &= again - 1;
+        const int tr = __shfl_sync(0xFFFFFFFFu, t, r);
+        const int64_t orr = __shfl_sync(0xFFFFFFFFu, orow, r);
+        const int64_t stride = (int64_t)p.Hk * D;
+        const int64_t first = (int64_t)it.b * p.T * stride + (int64_t)it.hk * D;
+        float rm = neg_inf(), rl = 0.0f, ro[D / 32];
+#pragma unroll
+        for (int e = 0; e < D / 32; ++e) ro[e] = 0.0f;
+        exact_row_keys<D>(p.q + orr * D, p.k + first, p.v + first, stride, 0, it.span.sink_end, tr,
+                          it.len, p.window, p.sinks, sl2, lane, rm, rl, ro);
+        exact_row_keys<D>(p.q + orr * D, p.k + first, p.v + first, stride, it.span.base,
+                          it.span.end, tr, it.len, p.window, p.sinks, sl2, lane, rm, rl, ro);
+        const float rinv = rl == 0.0f ? 0.0f : 1.0f / rl;
+        uint32_t* dst = reinterpret_cast<uint32_t*>(p.out + orr * D) + lane * (D / 64);
+#pragma unroll
+        for (int e = 0; e < D / 64; ++e) dst[e] = pack_bf16x2(ro[2 * e] * rinv, ro[2 * e + 1] * rinv);
+        if (lane == 0 && p.lse)
+          p.lse[orr] = rl == 0.0f ? neg_inf() : (rm + log2f(rl)) * 0.6931471805599453f;
+      }
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+size_t window_tiles_smem(int D) { return D == 128 ? WinCfg<128>::kSmem : WinCfg<64>::kSmem; }
+
+cudaError_t launch_window_tiles(const CUtensorMap& tm_q, const CUtensorMap& tm_k,
+                                const CUtensorMap& tm_v, const WinParams& p, int D, int grid,
+                                cudaStream_t stream) {
+  const size_t smem = window_tiles_smem(D);
+  const void* fn = D == 128 ? reinterpret_cast<const void*>(k_window_tiles<128>)
+                            : reinterpret_cast<const void*>(k_window_tiles<64>);
+  const cudaError_t e =
+      cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  if (e != cudaSuccess) return e;
+  if (D == 128)
+    k_window_tiles<128><<<grid, kWinThreads, smem, stream>>>(tm_q, tm_k, tm_v, p);
+  else
+    k_window_tiles<64><<<grid, kWinThreads, smem, stream>>>(tm_q, tm_k, tm_v, p);
+  return cudaGetLastError();
+}
+
+}  // namespace si

@@ -131,6 +131,26 @@ struct RowsParams {
 };
 cudaError_t launch_attn_rows(const RowsParams& p, int D, cudaStream_t stream);
 
+// Window attention of many rows on the tensor cores (k_window_tiles.cu).
+struct WinParams {
+  const uint16_t *q, *k, *v;  // [B,S,H,D], [B,T,Hk,D] bf16
+  uint16_t* out;
+  float* lse;                 // or null
+  const int32_t *lens, *q_lens;  // [B], or null
+  int B, S, T, H, Hk, G;
+  int QT;                     // queries of a 128-row tile: 128 / G
+  int pairs;                  // pairs of tiles per batch and kv head
+  int64_t items;              // B * Hk * pairs
+  int window, sinks;
+  float scale_log2;
+  uint32_t* err;
+  uint64_t timeout_ns;
+};
+size_t window_tiles_smem(int D);
+cudaError_t launch_window_tiles(const CUtensorMap& tm_q, const CUtensorMap& tm_k,
+                                const CUtensorMap& tm_v, const WinParams& p, int D, int grid,
+                                cudaStream_t stream);
+
 // Rows of a 4-bit paged cache (k_cache4.cu): append reads k, v [B,S,Hk,D]
 // bf16, read writes k_out, v_out of that shape.
 struct Cache4Params {

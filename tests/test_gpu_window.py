@@ -204,3 +204,43 @@ def test_graph_and_streams():
     other.synchronize()
     for g, w in zip(got, want):
         assert torch.equal(g[0], w[0]) and torch.equal(g[1], w[1])
+
+
+TILE_CASES = [
+    # B, S, T, H, Hk, D, window, sinks
+    (1, 64, 64, 1, 1, 128, 64, 0),
+    (1, 129, 400, 2, 2, 64, 100, 4),      # one head a group: 128 queries a tile
+    (2, 300, 300, 3, 1, 128, 57, 1),      # three heads a group: rows that no query has
+    (1, 33, 1000, 128, 1, 128, 300, 200), # one query a tile, two sink blocks
+    (1, 500, 777, 12, 4, 64, 128, 0),
+    (1, 200, 2000, 8, 1, 128, 1500, 5),
+    (1, 70, 70, 100, 1, 64, 10 ** 9, 0),
+]
+
+
+@pytest.mark.parametrize("B,S,T,H,Hk,D,window,sinks", TILE_CASES)
+def test_tiles_against_formula(B, S, T, H, Hk, D, window, sinks):
+    q, k, v = inputs(B, S, T, H, Hk, D, seed=S + T)
+    out, lse = run(q, k, v, window, sinks)
+    rows = {(b, i) for b in range(B) for i in {*range(0, S, 7), S - 1, S - 2, 127 % S, 128 % S}}
+    check(q, k, v, window, sinks, [T] * B, [S] * B, out, lse, rows=rows)
+
+
+def test_tiles_zero_scale():
+    q, k, v = inputs(1, 80, 80, 2, 1, 64, seed=12)
+    out, lse = run(q, k, v, 50, 0, scale=0.0)
+    for i in (0, 10, 79):
+        seen = v[0, max(0, i - 49):i + 1, 0].double()
+        err = (out[0, i].double() - seen.mean(0)).abs()
+        assert (err <= 2.0 ** -7 * (seen.abs().mean(0) + 1e-3)).all()
+        assert (lse[0, i] - np.log(len(seen))).abs().max() < 1e-5
+
+
+def test_tiles_agree_with_rows():
+    """The two kernels of the window attention on the same call (key chunks fix the rows kernel)."""
+    q, k, v = inputs(2, 90, 600, 16, 2, 128, seed=13)
+    a = run(q, k, v, 333, 3, [600, 411], [90, 77])
+    b = run(q, k, v, 333, 3, [600, 411], [90, 77], opts=stl.options(key_chunk=1024))
+    assert (a[0].float() - b[0].float()).abs().max() <= 2.0 ** -6 * v.abs().max()
+    assert (a[1] - b[1]).abs().max() <= 1e-4
+    check(q, k, v, 333, 3, [600, 411], [90, 77], *b, rows={(0, 0), (0, 89), (1, 40), (1, 76)}, fill=None)
