@@ -24,19 +24,6 @@ int page_shift_of(int page, int lo, int hi) {
 
 bool scale_ok(float g) { return g >= 0x1p-60f && g <= 0x1p60f; }  // false for NaN
 
-// CTAs that share a row tile's keys.  A decode step has B * H_k tiles or few
-// more, each with up to `keys` keys: with fewer tiles than the GPU holds CTAs
-// the keys are split so that they fill it, as long as a CTA's four warps keep
-// two steps of 32 keys each.
-int row_splits(int64_t tiles, int64_t keys, int key_chunk, int sms) {
-  if (key_chunk > 0) return (int)std::min<int64_t>(1024, std::max<int64_t>(1, (keys + key_chunk - 1) / key_chunk));
-  const int64_t room = (int64_t)sms * 3;
-  if (tiles >= room) return 1;
-  const int64_t want = (room + tiles - 1) / tiles;
-  const int64_t most = std::max<int64_t>(1, keys / 256);
-  return (int)std::min<int64_t>(std::min(want, most), 128);
-}
-
 // Sizes that the two attention calls share.
 int check_attention(int B, int S, int H, int H_k, int d) {
   if (B < 1 || S < 1 || H < 1 || H_k < 1 || H % H_k || !(d == 64 || d == 128)) return SI_ERR_DIM;
@@ -44,22 +31,42 @@ int check_attention(int B, int S, int H, int H_k, int d) {
   return SI_OK;
 }
 
-// The rows kernel's plan: tiles and splits, and the bytes of partial results.
-// keys: what one query may see at most.
-int plan_rows(RowsParams* p, int64_t keys, bool listed, int key_chunk, int sms, int d,
+// The rows kernel's plan: the tile width (the narrowest of 8, 16 and 32 rows
+// that holds a kv head's rows, so that keys are read once), the keys of a CTA,
+// and the bytes of partial results.  keys: what one query may see at most.
+// With fewer tiles than three waves of CTAs the keys are split into chunks, of
+// one length for all sequences, so that they make up three waves at full
+// length (ragged sequences leave some out); a chunk keeps a CTA's four warps at
+// two steps of 32 keys, and a row's chunks stay at 128.
+int plan_rows(RowsParams* p, int64_t keys, bool cache4, int key_chunk, int sms, int d,
               size_t* bytes) {
-  const int64_t span = listed ? keys : std::min<int64_t>(p->T, keys + 16 / p->G + 64);
-  const int64_t per = listed ? (int64_t)p->S * ((p->G + 15) / 16)
-                             : ((int64_t)p->S * p->G + 15) / 16;
+  const bool listed = p->topk > 0;
+  const int64_t rows = listed ? p->G : std::min<int64_t>((int64_t)p->S * p->G, 1 << 20);
+  p->row_tile = rows <= 8 ? 8 : rows <= 16 ? 16 : 32;
+  const int rt = p->row_tile;
+  const int64_t per = listed ? (int64_t)p->S * ((p->G + rt - 1) / rt)
+                             : ((int64_t)p->S * p->G + rt - 1) / rt;
+  // a tile's queries see a little more than one of them, the sinks and the
+  // window's two ends come in whole steps
+  const int64_t span = listed ? keys : std::min<int64_t>(p->T, keys + rt / p->G + 1);
+  const int64_t steps = (span + 31) / 32 + (listed ? 0 : 3);
   const int64_t tiles = (int64_t)p->B * p->Hk * per;
-  p->splits = row_splits(tiles, span, key_chunk, sms);
+  const int64_t room = 3 * (int64_t)sms * attn_rows_ctas(d, cache4, rt);
+  int64_t chunk = steps;
+  if (key_chunk > 0) {
+    chunk = std::max<int64_t>(key_chunk / 32, (steps + 1023) / 1024);
+  } else if (tiles < room) {
+    chunk = std::max<int64_t>(8, std::max((tiles * steps + room - 1) / room, (steps + 127) / 128));
+  }
+  p->splits = (int)((steps + chunk - 1) / chunk);
+  p->chunk_keys = (int)chunk * 32;
   if (tiles * p->splits >= ((int64_t)1 << 31)) return SI_ERR_DIM;
   p->tiles = (int)per;
-  const int64_t rows = (int64_t)p->B * p->S * p->H;
+  const int64_t all = (int64_t)p->B * p->S * p->H;
   *bytes = 0;
   if (p->splits > 1)
-    *bytes = align256((size_t)rows * p->splits * d * sizeof(float)) +
-             align256((size_t)rows * p->splits * sizeof(float2));
+    *bytes = align256((size_t)all * p->splits * d * sizeof(float)) +
+             align256((size_t)all * p->splits * sizeof(float2));
   return SI_OK;
 }
 
@@ -122,7 +129,7 @@ int cache4_problem(int width, int page, int topk, int B, int S, int H, int H_k, 
   plan_limits(&max_smem, &sms);
   const int64_t keys =
       topk ? topk : std::min<int64_t>(p->T, (int64_t)p->window + p->sinks);
-  return plan_rows(p, keys, topk > 0, o->key_chunk, sms, d, bytes);
+  return plan_rows(p, keys, true, o->key_chunk, sms, d, bytes);
 }
 
 // The sizes of a call on the rows of a 4-bit cache.

@@ -5,24 +5,32 @@
 //
 // over the keys the row's query sees (si_attn.cuh), or over the entries that a
 // row of the indexer lists.  The G = H / H_k query heads of a kv head share its
-// keys, so (query, head) pairs are the rows of a tile of 16.
+// keys, so (query, head) pairs are the rows of a tile of 8, 16 or 32.
 //
 // What bounds it: a decode step reads every visible key once and multiplies it
-// with few rows, so HBM does.  One warp takes KS keys at a time from a ring of
-// its own in shared memory (cp.async, no barrier between warps), the running
-// maximum and sum stay in registers, and the warps of a CTA (and, with few
-// sequences, several CTAs: `splits`) share a sequence's keys; their results
-// are joined at the end, by k_attn_join when there are several CTAs.  16-row
-// mma.sync tiles are what this shape needs: tcgen05's 128 rows would be empty
-// but for a few, and its operands would have to pass through shared memory as
-// 16-bit numbers, four times the bytes of the 4-bit codes.
+// with few rows, so HBM does, and for 4-bit keys the instructions that turn
+// codes into fp16 come near it.  One warp takes KS keys at a time from a ring
+// of its own in shared memory (cp.async, no barrier between warps), the running
+// maximum and sum stay in registers, and the warps of a CTA (and several CTAs,
+// each with a chunk of the keys, unless there are tiles enough) share a
+// sequence's keys; their results are joined at the end, by k_attn_join when
+// there are several CTAs.  Chunks have one length for all sequences, so ragged
+// ones keep the CTAs equally busy.
+//
+// Keys are the M side of the products, rows the N side (mma.sync m16n8k16):
+//   S^T = K Q^T,   O^T += V^T P^T
+// so a tile can be as small as 8 rows, and a key's fragment, once built, serves
+// all of the tile's rows.  S^T's fragments become P^T's by one 8 x 8
+// transposition each (movmatrix).  tcgen05's 128 rows would be empty but for a
+// few, and its operands would have to pass through shared memory as 16-bit
+// numbers, four times the bytes of the 4-bit codes.
 //
 // 4-bit keys (E2M1 codes, an E4M3 scale per 16 elements): code x scale has six
 // significant bits, so it is exact in fp16, and the products run in fp16 with
 // fp32 accumulation.  A query row is scaled by a power of two into fp16's
 // range (bf16 to fp16 drops no bit of an element within 2^-25 of the row's
 // largest).  The dot product does not depend on the order of its terms, so a
-// thread's fragment of a key row is simply 16 consecutive bytes of codes: no
+// thread's fragment of a key row is simply D/8 consecutive bytes of codes: no
 // shuffle, no transposition.  A value fragment pairs two keys for one element;
 // taking the nibbles of two code words together gives the pairs without a
 // transposition too.  Probabilities are rounded to fp16 after a scale of 2^10
@@ -38,105 +46,120 @@ namespace si {
 namespace {
 
 constexpr int kRowWarps = 4;
-constexpr int kRowTile = 16;
 constexpr float kProbShift = 10.0f;  // 4-bit path: probabilities times 2^10
 
-// What a warp holds of its tile while it walks over keys.
-template <int D>
+SI_DEV uint32_t transpose8x8(uint32_t x) {
+  uint32_t r;
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
+  return r;
+}
+
+// What a warp holds of its tile while it walks over keys.  Accumulators and
+// running values of n-tile x: the thread's rows are 8 x + 2 c and the next.
+template <int D, int NT>
 struct RowState {
-  float o[D / 8][4];
-  float m[2], l[2];
+  float o[NT][D / 16][4];
+  float m[NT][2], l[NT][2];
 };
 
 // ------------------------------------------------------------ 4-bit pages
-// Key order inside a group of 16: column n of score tile t is this key.  A
-// quad's columns 2c, 2c+1 then are keys whose value rows lie in different
-// banks, and so are the key rows that a quarter-warp reads.
+// Key order inside a group of 16: row 8 t + n of a fragment is this key.  A
+// quad's pairs 2c, 2c+1 then are keys whose value rows lie in different banks,
+// and so are the key rows that a quarter-warp reads.
 SI_DEV int group_key(int t, int n) { return 8 * t + ((n & 1) ? 4 + ((n >> 1) ^ 1) : (n >> 1)); }
 
-template <int D>
+template <int D, int NT>
 struct Cache4 {
   static constexpr int KS = 32;
   static constexpr int kStages = 3;
   static constexpr int kCodes = KS * D / 2, kScales = KS * D / 16;
   static constexpr int kStageBytes = 2 * kCodes + 2 * kScales;
 
-  uint32_t qf[D / 16][4];
-  float row_factor[2];
+  uint32_t qf[NT][D / 16][2];
+  float row_factor[NT];  // of row 8 x + lane / 4
 
   // Byte of a value row's 16-byte chunk in its stage (a swizzle by key).
   static SI_DEV int v_off(int key, int chunk) {
     return key * (D / 2) + ((D == 128 ? chunk ^ (((key >> 1) & 1) << 1) : chunk) << 4);
   }
 
-  SI_DEV void load_q(const RowsParams& p, const uint16_t* const (&qr)[2], int lane) {
+  // Fragments of n-tile x: the thread's row is 8 x + lane / 4.
+  SI_DEV void load_q(int x, const uint16_t* qr, int lane) {
     const int c = lane & 3;
+    uint32_t w[D / 8];  // D/4 elements of the row: D/4 * c ...
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      uint32_t w[D / 8];  // D/4 elements of the row: D/4 * c ...
+    for (int i = 0; i < D / 32; ++i) {
+      const uint4 v = qr ? __ldg(reinterpret_cast<const uint4*>(qr + (D / 4) * c) + i)
+                         : make_uint4(0, 0, 0, 0);
+      w[4 * i] = v.x, w[4 * i + 1] = v.y, w[4 * i + 2] = v.z, w[4 * i + 3] = v.w;
+    }
+    float top = 0.0f;
 #pragma unroll
-      for (int i = 0; i < D / 32; ++i) {
-        const uint4 x = qr[h] ? __ldg(reinterpret_cast<const uint4*>(qr[h] + (D / 4) * c) + i)
-                              : make_uint4(0, 0, 0, 0);
-        w[4 * i] = x.x, w[4 * i + 1] = x.y, w[4 * i + 2] = x.z, w[4 * i + 3] = x.w;
-      }
-      float top = 0.0f;
+    for (int i = 0; i < D / 8; ++i)
+      top = fmaxf(top, fmaxf(fabsf(bf16_lo(w[i])), fabsf(bf16_hi(w[i]))));
+    top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
+    top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 2));
+    // 2^(10 - e) for a largest element in [2^e, 2^(e+1)); 1 for rows of zeros
+    // or with an infinity, 2^126 at most
+    const int e = (int)(__float_as_uint(top) >> 23);
+    const int up = (e == 0 || e == 255) ? 0 : max(-126, min(126, 137 - e));
+    const float f = __uint_as_float((uint32_t)(127 + up) << 23);
+    row_factor[x] = __uint_as_float((uint32_t)(127 - up) << 23);
 #pragma unroll
-      for (int i = 0; i < D / 8; ++i)
-        top = fmaxf(top, fmaxf(fabsf(bf16_lo(w[i])), fabsf(bf16_hi(w[i]))));
-      top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
-      top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 2));
-      // 2^(10 - e) for a largest element in [2^e, 2^(e+1)); 1 for rows of
-      // zeros or with an infinity, 2^126 at most
-      const int e = (int)(__float_as_uint(top) >> 23);
-      const int up = (e == 0 || e == 255) ? 0 : min(126, 137 - e);
-      const float f = __uint_as_float((uint32_t)(127 + max(up, -126)) << 23);
-      row_factor[h] = __uint_as_float((uint32_t)(127 - max(up, -126)) << 23);
-#pragma unroll
-      for (int s = 0; s < D / 16; ++s) {
-        qf[s][h] = pack_f16x2(bf16_lo(w[2 * s]) * f, bf16_hi(w[2 * s]) * f);
-        qf[s][2 + h] = pack_f16x2(bf16_lo(w[2 * s + 1]) * f, bf16_hi(w[2 * s + 1]) * f);
-      }
+    for (int s = 0; s < D / 16; ++s) {
+      qf[x][s][0] = pack_f16x2(bf16_lo(w[2 * s]) * f, bf16_hi(w[2 * s]) * f);
+      qf[x][s][1] = pack_f16x2(bf16_lo(w[2 * s + 1]) * f, bf16_hi(w[2 * s + 1]) * f);
     }
   }
 
-  // Scores of 16 keys (two tiles of 8 columns) from a stage.
-  SI_DEV void scores(uint32_t kc, uint32_t ks, int lane, float (&s)[2][4]) const {
+  // Scores of 16 keys from a stage: s[x][t] are the keys group_key(t, lane / 4)
+  // against the rows 8 x + 2 c + (0, 1), [2 t] and [2 t + 1].
+  SI_DEV void scores(uint32_t kc, uint32_t ks, int lane, float (&s)[NT][4]) const {
     const int r = lane >> 2, c = lane & 3;
+    uint32_t w[2][D / 32], slo[2], shi[2];
 #pragma unroll
     for (int t = 0; t < 2; ++t) {
       const int key = group_key(t, r);
-      uint32_t w[D / 32];
       uint32_t sc;
       if constexpr (D == 128) {
         asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];"
-                     : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
+                     : "=r"(w[t][0]), "=r"(w[t][1]), "=r"(w[t][2]), "=r"(w[t][3])
                      : "r"(kc + key * 64 + c * 16));
         asm volatile("{\n\t.reg .b16 h;\n\tld.shared.b16 h, [%1];\n\tcvt.u32.u16 %0, h;\n\t}"
                      : "=r"(sc)
                      : "r"(ks + key * 8 + c * 2));
       } else {
         asm volatile("ld.shared.v2.b32 {%0,%1}, [%2];"
-                     : "=r"(w[0]), "=r"(w[1])
+                     : "=r"(w[t][0]), "=r"(w[t][1])
                      : "r"(kc + key * 32 + c * 8));
         asm volatile("ld.shared.u8 %0, [%1];" : "=r"(sc) : "r"(ks + key * 4 + c));
       }
       const uint32_t s2 = e4m3x2(sc);
-      const uint32_t slo = __byte_perm(s2, 0, 0x1010), shi = __byte_perm(s2, 0, 0x3232);
-      s[t][0] = s[t][1] = s[t][2] = s[t][3] = 0.0f;
+      slo[t] = __byte_perm(s2, 0, 0x1010);
+      shi[t] = __byte_perm(s2, 0, 0x3232);
+    }
 #pragma unroll
-      for (int i = 0; i < D / 32; ++i) {
-        const uint32_t sf = (D == 128 && i >= 2) ? shi : slo;
-        mma_f16(s[t], qf[2 * i], hmul2(e2m1x2<0>(w[i]), sf), hmul2(e2m1x2<1>(w[i]), sf));
-        mma_f16(s[t], qf[2 * i + 1], hmul2(e2m1x2<2>(w[i]), sf), hmul2(e2m1x2<3>(w[i]), sf));
-      }
+    for (int x = 0; x < NT; ++x) s[x][0] = s[x][1] = s[x][2] = s[x][3] = 0.0f;
+#pragma unroll
+    for (int i = 0; i < D / 32; ++i) {
+      const uint32_t f0 = (D == 128 && i >= 2) ? shi[0] : slo[0];
+      const uint32_t f1 = (D == 128 && i >= 2) ? shi[1] : slo[1];
+      uint32_t a[4] = {hmul2(e2m1x2<0>(w[0][i]), f0), hmul2(e2m1x2<0>(w[1][i]), f1),
+                       hmul2(e2m1x2<1>(w[0][i]), f0), hmul2(e2m1x2<1>(w[1][i]), f1)};
+#pragma unroll
+      for (int x = 0; x < NT; ++x) mma_f16(s[x], a, qf[x][2 * i][0], qf[x][2 * i][1]);
+      uint32_t b[4] = {hmul2(e2m1x2<2>(w[0][i]), f0), hmul2(e2m1x2<2>(w[1][i]), f1),
+                       hmul2(e2m1x2<3>(w[0][i]), f0), hmul2(e2m1x2<3>(w[1][i]), f1)};
+#pragma unroll
+      for (int x = 0; x < NT; ++x) mma_f16(s[x], b, qf[x][2 * i + 1][0], qf[x][2 * i + 1][1]);
     }
   }
 
-  // o += P V over 16 keys; `live`: which keys of the group may be read (their
-  // codes count as zero else).
-  SI_DEV void values(uint32_t vc, uint32_t vs, int lane, const uint32_t (&pf)[4], uint32_t live,
-                     RowState<D>& st) const {
+  // O^T += V^T P^T over 16 keys; MASKED: `live` says which keys of the group may
+  // be read (the others' codes count as zero).
+  template <bool MASKED>
+  SI_DEV void values(uint32_t vc, uint32_t vs, int lane, const uint32_t (&pf)[NT][2], uint32_t live,
+                     RowState<D, NT>& st) const {
     const int n = lane >> 2, c = lane & 3;
     uint32_t sp[2], w[4][D / 64];
 #pragma unroll
@@ -156,25 +179,27 @@ struct Cache4 {
                        : "r"(vc + key * 32 + n * 4));
           asm volatile("ld.shared.u8 %0, [%1];" : "=r"(b[i]) : "r"(vs + key * 4 + (n >> 1)));
         }
-        if (!((live >> key) & 1u)) b[i] = 0u;
+        if (MASKED && !((live >> key) & 1u)) b[i] = 0u;
       }
-      sp[t] = e4m3x2(b[0] | (b[1] << 8));
+      sp[t] = e4m3x2(__byte_perm(b[0], b[1], 0x0040));
     }
 #pragma unroll
-    for (int x = 0; x < D / 64; ++x) {
+    for (int y = 0; y < D / 64; ++y) {
       // even elements of both keys of a pair in the bytes of lo, odd ones in hi
       uint32_t lo[2], hi[2];
 #pragma unroll
       for (int t = 0; t < 2; ++t) {
-        const uint32_t a = w[2 * t][x], b = w[2 * t + 1][x];
+        const uint32_t a = w[2 * t][y], b = w[2 * t + 1][y];
         lo[t] = (a & 0x0F0F0F0Fu) | ((b << 4) & 0xF0F0F0F0u);
         hi[t] = ((a >> 4) & 0x0F0F0F0Fu) | (b & 0xF0F0F0F0u);
       }
-#define SI_PV(BYTE)                                                                          \
-  mma_f16(st.o[8 * x + 2 * BYTE], pf, hmul2(e2m1x2<BYTE>(lo[0]), sp[0]),                     \
-          hmul2(e2m1x2<BYTE>(lo[1]), sp[1]));                                                \
-  mma_f16(st.o[8 * x + 2 * BYTE + 1], pf, hmul2(e2m1x2<BYTE>(hi[0]), sp[0]),                 \
-          hmul2(e2m1x2<BYTE>(hi[1]), sp[1]));
+#define SI_PV(BYTE)                                                                             \
+  {                                                                                             \
+    uint32_t a[4] = {hmul2(e2m1x2<BYTE>(lo[0]), sp[0]), hmul2(e2m1x2<BYTE>(hi[0]), sp[0]),      \
+                     hmul2(e2m1x2<BYTE>(lo[1]), sp[1]), hmul2(e2m1x2<BYTE>(hi[1]), sp[1])};     \
+    _Pragma("unroll") for (int x = 0; x < NT; ++x)                                              \
+        mma_f16(st.o[x][4 * y + BYTE], a, pf[x][0], pf[x][1]);                                  \
+  }
       SI_PV(0)
       SI_PV(1)
       SI_PV(2)
@@ -183,66 +208,62 @@ struct Cache4 {
     }
   }
 
-  // Element of the row that accumulator o[i][.] column e (0, 1) of a thread is.
-  static SI_DEV int element(int i, int c, int e) { return (D / 8) * (2 * c + e) + i; }
+  // Element of the row that accumulator o[.][i] row half h of a thread is.
+  static SI_DEV int element(int i, int r, int h) { return (D / 8) * r + 2 * i + h; }
 };
 
 // ------------------------------------------------------------ bf16 rows
-template <int D>
+template <int D, int NT>
 struct Bf16Rows {
   static constexpr int KS = D == 128 ? 16 : 32;
   static constexpr int kStages = 3;
   static constexpr int kRows = KS * D * 2;
   static constexpr int kStageBytes = 2 * kRows;
 
-  uint32_t qf[D / 16][4];
-  float row_factor[2];
+  uint32_t qf[NT][D / 16][2];
+  float row_factor[NT];
 
   static SI_DEV int off(int key, int chunk) {
     return key * (D * 2) + ((chunk ^ (key & 7)) << 4);
   }
 
-  SI_DEV void load_q(const RowsParams& p, const uint16_t* const (&qr)[2], int lane) {
+  SI_DEV void load_q(int x, const uint16_t* qr, int lane) {
     const int c = lane & 3;
+    row_factor[x] = 1.0f;
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      row_factor[h] = 1.0f;
-#pragma unroll
-      for (int s = 0; s < D / 16; ++s) {
-        qf[s][h] = qr[h] ? __ldg(reinterpret_cast<const uint32_t*>(qr[h] + 16 * s + 2 * c)) : 0u;
-        qf[s][2 + h] =
-            qr[h] ? __ldg(reinterpret_cast<const uint32_t*>(qr[h] + 16 * s + 8 + 2 * c)) : 0u;
-      }
+    for (int s = 0; s < D / 16; ++s) {
+      qf[x][s][0] = qr ? __ldg(reinterpret_cast<const uint32_t*>(qr + 16 * s + 2 * c)) : 0u;
+      qf[x][s][1] = qr ? __ldg(reinterpret_cast<const uint32_t*>(qr + 16 * s + 8 + 2 * c)) : 0u;
     }
   }
 
-  SI_DEV void scores(uint32_t kb, int g, int lane, float (&s)[2][4]) const {
+  SI_DEV void scores(uint32_t kb, int g, int lane, float (&s)[NT][4]) const {
 #pragma unroll
-    for (int t = 0; t < 2; ++t) {
-      s[t][0] = s[t][1] = s[t][2] = s[t][3] = 0.0f;
-      const int key = 16 * g + 8 * t + (lane & 7);
-#pragma unroll
-      for (int i = 0; i < D / 32; ++i) {
-        uint32_t b[4];
-        ldmatrix4(b, kb + off(key, 4 * i + (lane >> 3)));
-        mma_bf16(s[t], qf[2 * i], b[0], b[1]);
-        mma_bf16(s[t], qf[2 * i + 1], b[2], b[3]);
-      }
-    }
-  }
-
-  SI_DEV void values(uint32_t vb, int g, int lane, const uint32_t (&pf)[4], RowState<D>& st) const {
+    for (int x = 0; x < NT; ++x) s[x][0] = s[x][1] = s[x][2] = s[x][3] = 0.0f;
     const int key = 16 * g + (lane & 15);
 #pragma unroll
     for (int i = 0; i < D / 16; ++i) {
-      uint32_t b[4];
-      ldmatrix4_t(b, vb + off(key, 2 * i + (lane >> 4)));
-      mma_bf16(st.o[2 * i], pf, b[0], b[1]);
-      mma_bf16(st.o[2 * i + 1], pf, b[2], b[3]);
+      uint32_t a[4];
+      ldmatrix4(a, kb + off(key, 2 * i + (lane >> 4)));
+#pragma unroll
+      for (int x = 0; x < NT; ++x) mma_bf16(s[x], a, qf[x][i][0], qf[x][i][1]);
     }
   }
 
-  static SI_DEV int element(int i, int c, int e) { return 8 * i + 2 * c + e; }
+  SI_DEV void values(uint32_t vb, int g, int lane, const uint32_t (&pf)[NT][2],
+                     RowState<D, NT>& st) const {
+    // matrices: keys 0-7 and elements 0-7, then 8-15; keys 8-15 the same
+    const int key = 16 * g + (lane & 7) + ((lane >> 4) << 3);
+#pragma unroll
+    for (int i = 0; i < D / 16; ++i) {
+      uint32_t a[4];
+      ldmatrix4_t(a, vb + off(key, 2 * i + ((lane >> 3) & 1)));
+#pragma unroll
+      for (int x = 0; x < NT; ++x) mma_bf16(st.o[x][i], a, pf[x][0], pf[x][1]);
+    }
+  }
+
+  static SI_DEV int element(int i, int r, int h) { return 16 * i + r + 8 * h; }
 };
 
 // The tile's rows and what its queries see.
@@ -252,6 +273,7 @@ struct Tile {
   int64_t part;           // index of its first row among all rows
 };
 
+template <int RT>
 SI_DEV bool find_tile(const RowsParams& p, int64_t id, Tile& ti) {
   const int tile = (int)(id % p.tiles);
   const int64_t bh = id / p.tiles;
@@ -261,15 +283,15 @@ SI_DEV bool find_tile(const RowsParams& p, int64_t id, Tile& ti) {
   ti.q_len = seq_len(p.q_lens, ti.b, p.S);
   int last;  // one past the tile's last row
   if (p.idx) {  // a tile's rows belong to one query
-    const int per = (p.G + kRowTile - 1) / kRowTile;
+    const int per = (p.G + RT - 1) / RT;
     const int i = tile / per;
-    ti.row0 = i * p.G + (tile % per) * kRowTile;
+    ti.row0 = i * p.G + (tile % per) * RT;
     last = min((i + 1) * p.G, ti.q_len * p.G);
   } else {
-    ti.row0 = tile * kRowTile;
+    ti.row0 = tile * RT;
     last = ti.q_len * p.G;
   }
-  ti.rows = min(kRowTile, last - ti.row0);
+  ti.rows = min(RT, last - ti.row0);
   if (ti.rows <= 0) return false;
   ti.t_min = ti.len - ti.q_len + ti.row0 / p.G;
   ti.t_max = ti.len - ti.q_len + (ti.row0 + ti.rows - 1) / p.G;
@@ -277,54 +299,70 @@ SI_DEV bool find_tile(const RowsParams& p, int64_t id, Tile& ti) {
   return true;
 }
 
+// The steps of KS keys that a tile takes.
+template <int KS>
+SI_DEV KeySpan tile_span(const RowsParams& p, const Tile& ti) {
+  if (p.idx) return KeySpan{0, 0, p.topk, 0, 0, (p.topk + KS - 1) / KS};
+  return key_span<KS>(ti.t_min, ti.t_max, ti.len, p.window, p.sinks);
+}
+
 SI_DEV int64_t out_row(const RowsParams& p, const Tile& ti, int row) {
   const int i = row / p.G;
   return ((int64_t)ti.b * p.S + i) * p.H + ti.hk * p.G + row % p.G;
 }
 
+// MODE 0: bf16 keys; 1: 4-bit pages; 2: 4-bit pages, listed entries.
+template <int D, int MODE, int NT>
+using Source = typename std::conditional<MODE == 0, Bf16Rows<D, NT>, Cache4<D, NT>>::type;
+
+// CTAs that an SM's registers hold.
+constexpr int row_ctas(int D, int MODE, int NT) {
+  return NT == 4 ? 2 : (D == 128 && MODE == 0 ? 2 : (NT == 1 ? 4 : 3));
+}
+
 }  // namespace
 
-// MODE 0: bf16 keys [B,T,H_k,D]; 1: 4-bit pages; 2: 4-bit pages, listed entries.
-template <int D, int MODE>
-__global__ void __launch_bounds__(kRowWarps * 32, 3)
+template <int D, int MODE, int NT>
+__global__ void __launch_bounds__(kRowWarps * 32, row_ctas(D, MODE, NT))
     k_attn_rows(const __grid_constant__ RowsParams p) {
-  using Src = typename std::conditional<MODE == 0, Bf16Rows<D>, Cache4<D>>::type;
-  constexpr int KS = Src::KS, NST = Src::kStages, NG = KS / 16;
+  using Src = Source<D, MODE, NT>;
+  constexpr int KS = Src::KS, NST = Src::kStages, NG = KS / 16, RT = 8 * NT;
   extern __shared__ __align__(128) uint8_t smem[];
-  __shared__ float sh_m[kRowWarps][kRowTile], sh_l[kRowWarps][kRowTile];
+  __shared__ float sh_m[kRowWarps][RT], sh_l[kRowWarps][RT];
   __shared__ uint32_t sh_nan;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int r = lane >> 2, c = lane & 3;
   const int split = (int)(blockIdx.x % p.splits);
   Tile ti;
-  if (!find_tile(p, blockIdx.x / p.splits, ti)) return;
+  if (!find_tile<RT>(p, blockIdx.x / p.splits, ti)) return;
+  const KeySpan span = tile_span<KS>(p, ti);
+  const int u_lo = split * p.chunk_keys / KS;
+  const int u_hi =
+      split + 1 == p.splits ? span.steps : min(span.steps, (split + 1) * p.chunk_keys / KS);
+  // a sequence without keys still has rows to write
+  if (u_lo >= u_hi && (split > 0 || p.splits > 1)) return;
   if (threadIdx.x == 0) sh_nan = 0u;
 
-  const KeySpan span = MODE == 2 ? KeySpan{0, 0, p.topk, 0, 0, (p.topk + KS - 1) / KS}
-                                 : key_span<KS>(ti.t_min, ti.t_max, ti.len, p.window, p.sinks);
-  const int u_lo = (int)((int64_t)span.steps * split / p.splits);
-  const int u_hi = (int)((int64_t)span.steps * (split + 1) / p.splits);
-
   Src src;
-  int t_row[2];
-  {
-    const uint16_t* qr[2];
+  float f_row[NT][2];  // scale of the thread's score columns
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const int row = r + 8 * h;
-      const bool live = row < ti.rows;
-      qr[h] = live ? p.q + out_row(p, ti, ti.row0 + row) * D : nullptr;
-      t_row[h] = ti.len - ti.q_len + (ti.row0 + min(row, ti.rows - 1)) / p.G;
-    }
-    src.load_q(p, qr, lane);
+  for (int x = 0; x < NT; ++x) {
+    const int row = 8 * x + r;
+    src.load_q(x, row < ti.rows ? p.q + out_row(p, ti, ti.row0 + row) * D : nullptr, lane);
+#pragma unroll
+    for (int e = 0; e < 2; ++e)
+      f_row[x][e] = __shfl_sync(0xFFFFFFFFu, src.row_factor[x], 8 * c + 4 * e) * p.scale_log2;
   }
-  const float f_row[2] = {src.row_factor[0] * p.scale_log2, src.row_factor[1] * p.scale_log2};
 
-  RowState<D> st;
+  RowState<D, NT> st;
 #pragma unroll
-  for (int i = 0; i < D / 8; ++i) st.o[i][0] = st.o[i][1] = st.o[i][2] = st.o[i][3] = 0.0f;
-  st.m[0] = st.m[1] = neg_inf();
-  st.l[0] = st.l[1] = 0.0f;
+  for (int x = 0; x < NT; ++x) {
+#pragma unroll
+    for (int i = 0; i < D / 16; ++i)
+      st.o[x][i][0] = st.o[x][i][1] = st.o[x][i][2] = st.o[x][i][3] = 0.0f;
+    st.m[x][0] = st.m[x][1] = neg_inf();
+    st.l[x][0] = st.l[x][1] = 0.0f;
+  }
 
   const uint32_t ring = smem_u32(smem) + warp * NST * Src::kStageBytes;
   uint32_t vmask[NST];  // keys of a stage that lie in a page
@@ -439,6 +477,106 @@ __global__ void __launch_bounds__(kRowWarps * 32, 3)
     cp_async_commit();
   };
 
+  // One step from a stage: scores, running maximum, weights, values.
+  auto step = [&](auto masked, int u, uint32_t at, uint32_t vm) {
+    constexpr bool MASKED = decltype(masked)::value;
+    float s[NG][NT][4];
+#pragma unroll
+    for (int g = 0; g < NG; ++g) {
+      if constexpr (MODE == 0)
+        src.scores(at, g, lane, s[g]);
+      else
+        src.scores(at + g * 8 * D, at + 2 * Src::kCodes + g * D, lane, s[g]);
+    }
+    uint32_t live = 0xFFFFFFFFu;  // keys whose values may be read
+    const int j0 = MASKED && MODE != 2 ? step_key<KS>(span, u) : 0;
+    if constexpr (MASKED && MODE == 1)
+      live = __ballot_sync(0xFFFFFFFFu,
+                           ((vm >> lane) & 1u) && span_holds(span, u, j0 + lane, p.sinks));
+    if constexpr (MASKED && MODE == 2) live = vm;
+    // scores to log2 units, unseen keys to -inf
+    float mx[NT][2];
+#pragma unroll
+    for (int x = 0; x < NT; ++x) {
+      mx[x][0] = st.m[x][0];
+      mx[x][1] = st.m[x][1];
+      int t_row[2] = {0, 0};
+      if constexpr (MASKED && MODE != 2)
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+          t_row[e] = ti.len - ti.q_len + (ti.row0 + min(8 * x + 2 * c + e, ti.rows - 1)) / p.G;
+#pragma unroll
+      for (int g = 0; g < NG; ++g)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          float v = s[g][x][e] * f_row[x][e & 1];
+          if constexpr (MASKED) {
+            const int key = 16 * g + (MODE == 0 ? 8 * (e >> 1) + r : group_key(e >> 1, r));
+            bool see = (live >> key) & 1u;
+            if constexpr (MODE != 2)
+              see = see && span_holds(span, u, j0 + key, p.sinks) &&
+                    sees(j0 + key, t_row[e & 1], ti.len, p.window, p.sinks);
+            v = see ? v : neg_inf();
+          }
+          s[g][x][e] = v;
+          mx[x][e & 1] = fmaxf(mx[x][e & 1], v);
+        }
+    }
+    bool grown = false;
+#pragma unroll
+    for (int x = 0; x < NT; ++x)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+#pragma unroll
+        for (int o = 4; o < 32; o <<= 1)
+          mx[x][e] = fmaxf(mx[x][e], __shfl_xor_sync(0xFFFFFFFFu, mx[x][e], o));
+        grown |= mx[x][e] > st.m[x][e];
+      }
+    if (__any_sync(0xFFFFFFFFu, grown)) {
+#pragma unroll
+      for (int x = 0; x < NT; ++x) {
+        float a[2];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          a[e] = mx[x][e] > st.m[x][e] ? ex2(st.m[x][e] - mx[x][e]) : 1.0f;
+          st.m[x][e] = mx[x][e];
+          st.l[x][e] *= a[e];
+        }
+#pragma unroll
+        for (int i = 0; i < D / 16; ++i) {
+          st.o[x][i][0] *= a[0];
+          st.o[x][i][1] *= a[1];
+          st.o[x][i][2] *= a[0];
+          st.o[x][i][3] *= a[1];
+        }
+      }
+    }
+    // a row that has seen nothing keeps its maximum at -inf: its weights are 2^-inf
+    const float shift = MODE == 0 ? 0.0f : kProbShift;
+#pragma unroll
+    for (int g = 0; g < NG; ++g) {
+      uint32_t pf[NT][2];
+#pragma unroll
+      for (int x = 0; x < NT; ++x) {
+        const float b0 = (st.m[x][0] == neg_inf() ? 0.0f : st.m[x][0]) - shift;
+        const float b1 = (st.m[x][1] == neg_inf() ? 0.0f : st.m[x][1]) - shift;
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+          const float w0 = ex2(s[g][x][2 * t] - b0), w1 = ex2(s[g][x][2 * t + 1] - b1);
+          st.l[x][0] += w0;
+          st.l[x][1] += w1;
+          pf[x][t] = transpose8x8(MODE == 0 ? pack_bf16x2(w0, w1) : pack_f16x2(w0, w1));
+        }
+      }
+      if constexpr (MODE == 0)
+        src.values(at + Src::kRows, g, lane, pf, st);
+      else
+        src.template values<MASKED>(at + Src::kCodes + g * 8 * D,
+                                    at + 2 * Src::kCodes + Src::kScales + g * D, lane, pf,
+                                    live >> (16 * g), st);
+    }
+  };
+
   const int u0 = u_lo + warp;
   if (MODE) look_ahead(u0);
 #pragma unroll
@@ -452,102 +590,17 @@ __global__ void __launch_bounds__(kRowWarps * 32, 3)
     __syncwarp();
     const uint32_t at = ring + stage * Src::kStageBytes;
     const uint32_t vm = vmask[0];
-    float s[NG][2][4];
-#pragma unroll
-    for (int g = 0; g < NG; ++g) {
-      if constexpr (MODE == 0)
-        src.scores(at, g, lane, s[g]);
-      else
-        src.scores(at + g * 8 * D, at + 2 * Src::kCodes + g * D, lane, s[g]);
+    bool whole = vm == 0xFFFFFFFFu;  // every row sees every key of the step
+    if (MODE != 2) {
+      const int j0 = step_key<KS>(span, u);
+      whole = whole && j0 + KS - 1 <= ti.t_min && j0 + KS <= ti.len &&
+              (j0 > ti.t_max - p.window || j0 + KS <= p.sinks) &&
+              (u >= span.sink_steps || j0 + KS <= span.sink_end);
     }
-    // scores to log2 units, unseen keys to -inf
-    const int j0 = MODE == 2 ? 0 : step_key<KS>(span, u);
-    const bool whole = vm == 0xFFFFFFFFu &&
-                       (MODE == 2 || (j0 + KS - 1 <= ti.t_min && j0 + KS <= ti.len &&
-                                      (j0 > ti.t_max - p.window || j0 + KS <= p.sinks) &&
-                                      (u >= span.sink_steps || j0 + KS <= span.sink_end)));
-    uint32_t live = 0xFFFFFFFFu;  // keys whose values may be read
-    if (whole) {
-#pragma unroll
-      for (int g = 0; g < NG; ++g)
-#pragma unroll
-        for (int t = 0; t < 2; ++t)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) s[g][t][e] *= f_row[e >> 1];
-    } else {
-      if constexpr (MODE == 1) {
-        const int j = j0 + lane;
-        live = __ballot_sync(0xFFFFFFFFu, ((vm >> lane) & 1u) && span_holds(span, u, j, p.sinks));
-      } else if constexpr (MODE == 2) {
-        live = vm;
-      }
-#pragma unroll
-      for (int g = 0; g < NG; ++g)
-#pragma unroll
-        for (int t = 0; t < 2; ++t)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const int n = 2 * c + (e & 1);
-            const int key = 16 * g + (MODE == 0 ? 8 * t + n : group_key(t, n));
-            bool see = (live >> key) & 1u;
-            if constexpr (MODE != 2)
-              see = see && span_holds(span, u, j0 + key, p.sinks) &&
-                    sees(j0 + key, t_row[e >> 1], ti.len, p.window, p.sinks);
-            s[g][t][e] = see ? s[g][t][e] * f_row[e >> 1] : neg_inf();
-          }
-    }
-    // running maximum of the two rows
-    float mx[2] = {st.m[0], st.m[1]};
-#pragma unroll
-    for (int g = 0; g < NG; ++g)
-#pragma unroll
-      for (int t = 0; t < 2; ++t)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) mx[e >> 1] = fmaxf(mx[e >> 1], s[g][t][e]);
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      mx[h] = fmaxf(mx[h], __shfl_xor_sync(0xFFFFFFFFu, mx[h], 1));
-      mx[h] = fmaxf(mx[h], __shfl_xor_sync(0xFFFFFFFFu, mx[h], 2));
-    }
-    if (__any_sync(0xFFFFFFFFu, mx[0] > st.m[0] || mx[1] > st.m[1])) {
-      const float a0 = mx[0] > st.m[0] ? ex2(st.m[0] - mx[0]) : 1.0f;
-      const float a1 = mx[1] > st.m[1] ? ex2(st.m[1] - mx[1]) : 1.0f;
-      st.m[0] = mx[0];
-      st.m[1] = mx[1];
-      st.l[0] *= a0;
-      st.l[1] *= a1;
-#pragma unroll
-      for (int i = 0; i < D / 8; ++i) {
-        st.o[i][0] *= a0;
-        st.o[i][1] *= a0;
-        st.o[i][2] *= a1;
-        st.o[i][3] *= a1;
-      }
-    }
-    // a row that has seen nothing keeps its maximum at -inf: its weights are 2^-inf
-    const float shift = MODE == 0 ? 0.0f : kProbShift;
-    const float b0 = (st.m[0] == neg_inf() ? 0.0f : st.m[0]) - shift;
-    const float b1 = (st.m[1] == neg_inf() ? 0.0f : st.m[1]) - shift;
-#pragma unroll
-    for (int g = 0; g < NG; ++g) {
-      uint32_t pf[4];
-#pragma unroll
-      for (int t = 0; t < 2; ++t) {
-        float w[4];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          w[e] = ex2(s[g][t][e] - (e < 2 ? b0 : b1));
-          st.l[e >> 1] += w[e];
-        }
-        pf[2 * t] = MODE == 0 ? pack_bf16x2(w[0], w[1]) : pack_f16x2(w[0], w[1]);
-        pf[2 * t + 1] = MODE == 0 ? pack_bf16x2(w[2], w[3]) : pack_f16x2(w[2], w[3]);
-      }
-      if constexpr (MODE == 0)
-        src.values(at + Src::kRows, g, lane, pf, st);
-      else
-        src.values(at + Src::kCodes + g * 8 * D, at + 2 * Src::kCodes + Src::kScales + g * D, lane,
-                   pf, live >> (16 * g), st);
-    }
+    if (whole)
+      step(std::false_type{}, u, at, vm);
+    else
+      step(std::true_type{}, u, at, vm);
     __syncwarp();
     // the stage just read takes the step NST - 1 further on
 #pragma unroll
@@ -561,36 +614,41 @@ __global__ void __launch_bounds__(kRowWarps * 32, 3)
 
   // ---------------------------------------------------------------- join the warps
 #pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    st.l[h] += __shfl_xor_sync(0xFFFFFFFFu, st.l[h], 1);
-    st.l[h] += __shfl_xor_sync(0xFFFFFFFFu, st.l[h], 2);
-    if (c == 0) {
-      sh_m[warp][r + 8 * h] = st.m[h];
-      sh_l[warp][r + 8 * h] = st.l[h];
+  for (int x = 0; x < NT; ++x)
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+#pragma unroll
+      for (int o = 4; o < 32; o <<= 1)
+        st.l[x][e] += __shfl_xor_sync(0xFFFFFFFFu, st.l[x][e], o);
+      if (r == 0) {
+        sh_m[warp][8 * x + 2 * c + e] = st.m[x][e];
+        sh_l[warp][8 * x + 2 * c + e] = st.l[x][e];
+      }
     }
-  }
   __syncthreads();  // the ring is free from here on
   constexpr int kPad = D + 4;
   float* sh_o = reinterpret_cast<float*>(smem);
 #pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    const int row = r + 8 * h;
-    float top = neg_inf();
+  for (int x = 0; x < NT; ++x)
 #pragma unroll
-    for (int w = 0; w < kRowWarps; ++w) top = fmaxf(top, sh_m[w][row]);
-    const float f = st.m[h] == neg_inf() ? 0.0f : ex2(st.m[h] - top);
-    float* orow = sh_o + (warp * kRowTile + row) * kPad;
+    for (int e = 0; e < 2; ++e) {
+      const int row = 8 * x + 2 * c + e;
+      float top = neg_inf();
 #pragma unroll
-    for (int i = 0; i < D / 8; ++i) {
-      // a weight of zero times a sum that is NaN stays NaN: found below
-      orow[Src::element(i, c, 0)] = st.o[i][2 * h] * f;
-      orow[Src::element(i, c, 1)] = st.o[i][2 * h + 1] * f;
+      for (int w = 0; w < kRowWarps; ++w) top = fmaxf(top, sh_m[w][row]);
+      const float f = st.m[x][e] == neg_inf() ? 0.0f : ex2(st.m[x][e] - top);
+      float* orow = sh_o + (warp * RT + row) * kPad;
+#pragma unroll
+      for (int i = 0; i < D / 16; ++i) {
+        // a weight of zero times a sum that is NaN stays NaN: found below
+        orow[Src::element(i, r, 0)] = st.o[x][i][e] * f;
+        orow[Src::element(i, r, 1)] = st.o[x][i][2 + e] * f;
+      }
     }
-  }
   __syncthreads();
-  // eight threads a row, D/8 elements each
-  constexpr int kPer = D / 8;
-  const int row = threadIdx.x >> 3, part = threadIdx.x & 7;
+  // 128 / RT threads a row
+  constexpr int kParts = kRowWarps * 32 / RT, kPer = D / kParts;
+  const int row = threadIdx.x / kParts, part = threadIdx.x % kParts;
   float top = neg_inf(), sum = 0.0f;
 #pragma unroll
   for (int w = 0; w < kRowWarps; ++w) top = fmaxf(top, sh_m[w][row]);
@@ -602,8 +660,7 @@ __global__ void __launch_bounds__(kRowWarps * 32, 3)
   for (int i = 0; i < kPer; ++i) {
     o[i] = 0.0f;
 #pragma unroll
-    for (int w = 0; w < kRowWarps; ++w)
-      o[i] += sh_o[(w * kRowTile + row) * kPad + part * kPer + i];
+    for (int w = 0; w < kRowWarps; ++w) o[i] += sh_o[(w * RT + row) * kPad + part * kPer + i];
   }
   if constexpr (MODE == 0) {
     bool bad = false;
@@ -655,86 +712,113 @@ __global__ void __launch_bounds__(kRowWarps * 32, 3)
   }
   const float inv = sum == 0.0f ? 0.0f : p.v_scale / sum;
   const int64_t orow = out_row(p, ti, ti.row0 + row);
-  uint32_t w[kPer / 2];
+  uint32_t* dst = reinterpret_cast<uint32_t*>(p.out + orow * D + part * kPer);
 #pragma unroll
-  for (int i = 0; i < kPer / 2; ++i) w[i] = pack_bf16x2(o[2 * i] * inv, o[2 * i + 1] * inv);
-#pragma unroll
-  for (int i = 0; i < kPer / 8; ++i)
-    reinterpret_cast<uint4*>(p.out + orow * D + part * kPer)[i] =
-        make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+  for (int i = 0; i < kPer / 4; ++i)
+    reinterpret_cast<uint2*>(dst)[i] =
+        make_uint2(pack_bf16x2(o[4 * i] * inv, o[4 * i + 1] * inv),
+                   pack_bf16x2(o[4 * i + 2] * inv, o[4 * i + 3] * inv));
   if (part == 0 && p.lse)
     p.lse[orow] = sum == 0.0f ? neg_inf() : (top + log2f(sum)) * 0.6931471805599453f;
 }
 
-// Joins the splits of a row: one warp per row, D/32 elements per lane.
-template <int D>
+// Joins the chunks of a row: a CTA of four warps per row, D/32 elements a lane.
+template <int D, int KS, int RT>
 __global__ void __launch_bounds__(128) k_attn_join(const __grid_constant__ RowsParams p) {
   constexpr int E = D / 32;
-  const int lane = threadIdx.x & 31;
-  const int64_t at = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 5);
-  const int64_t rows = (int64_t)p.S * p.G;
-  if (at >= (int64_t)p.B * p.Hk * rows) return;
+  __shared__ float sh_o[4][D], sh_l[4], sh_top[4];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int64_t at = blockIdx.x;
+  const int rows = p.S * p.G;
   const int row = (int)(at % rows);
-  const int64_t bh = at / rows;
-  const int b = (int)(bh / p.Hk), hk = (int)(bh % p.Hk);
-  if (row >= seq_len(p.q_lens, b, p.S) * p.G) return;
+  // the row's tile, for the chunks that its keys filled
+  Tile ti;
+  int tile;
+  if (p.idx) {
+    const int per = (p.G + RT - 1) / RT;
+    tile = row / p.G * per + row % p.G / RT;
+  } else {
+    tile = row / RT;
+  }
+  if (!find_tile<RT>(p, at / rows * p.tiles + tile, ti) || row >= ti.row0 + ti.rows) return;
+  const int n = min(p.splits, (tile_span<KS>(p, ti).steps * KS + p.chunk_keys - 1) / p.chunk_keys);
   const float2* ml = p.part_ml + at * p.splits;
   float top = neg_inf();
-  for (int s = lane; s < p.splits; s += 32) top = fmaxf(top, ml[s].x);
+  for (int s = threadIdx.x; s < n; s += 128) top = fmaxf(top, ml[s].x);
 #pragma unroll
   for (int x = 16; x > 0; x >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, x));
+  if (lane == 0) sh_top[warp] = top;
+  __syncthreads();
+  top = fmaxf(fmaxf(sh_top[0], sh_top[1]), fmaxf(sh_top[2], sh_top[3]));
   float o[E], sum = 0.0f;
 #pragma unroll
   for (int e = 0; e < E; ++e) o[e] = 0.0f;
-  for (int s = 0; s < p.splits; ++s) {
+#pragma unroll 4
+  for (int s = warp; s < n; s += 4) {
     const float2 v = ml[s];
-    if (v.y == 0.0f) continue;
-    const float f = ex2(v.x - top);
+    const float f = v.y == 0.0f ? 0.0f : ex2(v.x - top);
     sum = fmaf(v.y, f, sum);
     const float* po = p.part_o + (at * p.splits + s) * D + lane * E;
 #pragma unroll
     for (int e = 0; e < E; ++e) o[e] = fmaf(po[e], f, o[e]);
   }
-  const float inv = sum == 0.0f ? 0.0f : p.v_scale / sum;
-  const int64_t orow = ((int64_t)b * p.S + row / p.G) * p.H + hk * p.G + row % p.G;
-  uint32_t* out = reinterpret_cast<uint32_t*>(p.out + orow * D) + lane * (E / 2);
 #pragma unroll
-  for (int e = 0; e < E / 2; ++e) out[e] = pack_bf16x2(o[2 * e] * inv, o[2 * e + 1] * inv);
-  if (lane == 0 && p.lse)
+  for (int e = 0; e < E; ++e) sh_o[warp][lane * E + e] = o[e];
+  if (lane == 0) sh_l[warp] = sum;
+  __syncthreads();
+  sum = (sh_l[0] + sh_l[1]) + (sh_l[2] + sh_l[3]);
+  const float inv = sum == 0.0f ? 0.0f : p.v_scale / sum;
+  const int64_t orow = out_row(p, ti, row);
+  for (int d = threadIdx.x; d < D / 2; d += 128) {
+    float v[2];
+#pragma unroll
+    for (int e = 0; e < 2; ++e)
+      v[e] = ((sh_o[0][2 * d + e] + sh_o[1][2 * d + e]) + (sh_o[2][2 * d + e] + sh_o[3][2 * d + e])) * inv;
+    reinterpret_cast<uint32_t*>(p.out + orow * D)[d] = pack_bf16x2(v[0], v[1]);
+  }
+  if (threadIdx.x == 0 && p.lse)
     p.lse[orow] = sum == 0.0f ? neg_inf() : (top + log2f(sum)) * 0.6931471805599453f;
 }
 
 namespace {
 
-template <int D, int MODE>
+template <int D, int MODE, int NT>
 cudaError_t launch(const RowsParams& p, cudaStream_t stream) {
-  using Src = typename std::conditional<MODE == 0, Bf16Rows<D>, Cache4<D>>::type;
+  using Src = Source<D, MODE, NT>;
   const size_t ring = (size_t)kRowWarps * Src::kStages * Src::kStageBytes;
-  const size_t join = (size_t)kRowWarps * kRowTile * (D + 4) * sizeof(float);
+  const size_t join = (size_t)kRowWarps * 8 * NT * (D + 4) * sizeof(float);
   const size_t smem = ring > join ? ring : join;
-  cudaError_t e = cudaFuncSetAttribute(k_attn_rows<D, MODE>,
+  cudaError_t e = cudaFuncSetAttribute(k_attn_rows<D, MODE, NT>,
                                        cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;
   const int64_t ctas = (int64_t)p.B * p.Hk * p.tiles * p.splits;
-  k_attn_rows<D, MODE><<<(unsigned)ctas, kRowWarps * 32, smem, stream>>>(p);
+  k_attn_rows<D, MODE, NT><<<(unsigned)ctas, kRowWarps * 32, smem, stream>>>(p);
   if ((e = cudaGetLastError()) != cudaSuccess || p.splits == 1) return e;
-  const int64_t rows = (int64_t)p.B * p.Hk * p.S * p.G;
-  k_attn_join<D><<<(unsigned)((rows + 3) / 4), 128, 0, stream>>>(p);
+  k_attn_join<D, Src::KS, 8 * NT>
+      <<<(unsigned)((int64_t)p.B * p.Hk * p.S * p.G), 128, 0, stream>>>(p);
   return cudaGetLastError();
+}
+
+template <int D, int MODE>
+cudaError_t launch_nt(const RowsParams& p, cudaStream_t stream) {
+  return p.row_tile == 8    ? launch<D, MODE, 1>(p, stream)
+         : p.row_tile == 16 ? launch<D, MODE, 2>(p, stream)
+                            : launch<D, MODE, 4>(p, stream);
 }
 
 }  // namespace
 
+int attn_rows_ctas(int D, bool cache4, int row_tile) { return row_ctas(D, cache4 ? 1 : 0, row_tile / 8); }
 
 cudaError_t launch_attn_rows(const RowsParams& p, int D, cudaStream_t stream) {
   const int mode = !p.pages ? 0 : (p.idx ? 2 : 1);
   if (D == 128)
-    return mode == 0   ? launch<128, 0>(p, stream)
-           : mode == 1 ? launch<128, 1>(p, stream)
-                       : launch<128, 2>(p, stream);
-  return mode == 0   ? launch<64, 0>(p, stream)
-         : mode == 1 ? launch<64, 1>(p, stream)
-                     : launch<64, 2>(p, stream);
+    return mode == 0   ? launch_nt<128, 0>(p, stream)
+           : mode == 1 ? launch_nt<128, 1>(p, stream)
+                       : launch_nt<128, 2>(p, stream);
+  return mode == 0   ? launch_nt<64, 0>(p, stream)
+         : mode == 1 ? launch_nt<64, 1>(p, stream)
+                     : launch_nt<64, 2>(p, stream);
 }
 
 }  // namespace si

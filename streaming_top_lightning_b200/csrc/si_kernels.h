@@ -125,10 +125,14 @@ struct RowsParams {
   int window, sinks;   // window <= 2^30
   float scale_log2;    // softmax scale (and K scale) times log2(e)
   float v_scale;
-  int tiles, splits;   // row tiles per kv head; CTAs that share a tile's keys
+  int row_tile, tiles; // rows of a tile (8, 16 or 32); tiles per kv head
+  int splits;          // CTAs that share a tile's keys, chunk_keys each
+  int chunk_keys;
   float* part_o;       // splits > 1: [B*Hk*S*G, splits, D] partial sums
   float2* part_ml;     //             [B*Hk*S*G, splits] (maximum in log2 units, sum)
 };
+// CTAs of a tile width that an SM holds.
+int attn_rows_ctas(int D, bool cache4, int row_tile);
 cudaError_t launch_attn_rows(const RowsParams& p, int D, cudaStream_t stream);
 
 // Window attention of many rows on the tensor cores (k_window_tiles.cu).
