@@ -27,8 +27,8 @@
 //                the tile's columns, then P = 2^(s - m) in bf16 over the first
 //                half of S's columns (the columns read by then), and the row's
 //                sum.  O is rescaled only when a row's maximum has grown by more
-//                than 2^8 since it was last fixed; P stays below 2^8, and the
-//                sum is over the same P's, so the result does not depend on it.
+//                than 2^16 since it was last fixed: bf16 and fp32 keep their
+//                relative precision up there, and the sum is over the same P's.
 // Keys are taken from the first one that the pair of tiles sees, 128 at a time,
 // the last block and the sinks' block cut to multiples of 32 columns, so a
 // window costs about its own length and not whole tiles of it.  Only columns
@@ -48,7 +48,7 @@ constexpr int kM = 128;        // rows of a tile (MMA M)
 constexpr int kN = 128;        // keys of a block
 constexpr int kWinThreads = 384;
 constexpr int kSoftWarp = 4;   // softmax warps 4-7: tile 0, 8-11: tile 1
-constexpr float kGrow = 8.0f;  // log2 growth of a maximum that rescales O
+constexpr float kGrow = 16.0f; // log2 growth of a maximum that rescales O
 
 template <int D>
 struct WinCfg {
@@ -101,6 +101,17 @@ SI_DEV void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
 }
 SI_DEV void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
+SI_DEV void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+        "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr)
+      : "memory");
+}
+
 // Keeps values read from TMEM behind the wait for them.
 SI_DEV void pin32(float (&v)[32]) {
 #pragma unroll
@@ -109,51 +120,80 @@ SI_DEV void pin32(float (&v)[32]) {
                  "+f"(v[i + 5]), "+f"(v[i + 6]), "+f"(v[i + 7]));
 }
 
+// Transposes the 4 x 4 pieces of four neighbouring lanes: lane q's piece e
+// becomes lane e's piece q.
+SI_DEV uint4 shfl_xor4(uint4 x, int m) {
+  return make_uint4(__shfl_xor_sync(0xFFFFFFFFu, x.x, m), __shfl_xor_sync(0xFFFFFFFFu, x.y, m),
+                    __shfl_xor_sync(0xFFFFFFFFu, x.z, m), __shfl_xor_sync(0xFFFFFFFFu, x.w, m));
+}
+SI_DEV void transpose4(uint4 (&x)[4], int lane) {
+#pragma unroll
+  for (int m = 1; m < 4; m <<= 1) {
+    const bool up = (lane & m) != 0;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      if (e & m) continue;
+      // lanes without the bit give their piece e | m for the others' piece e
+      const uint4 give = up ? x[e] : x[e | m];
+      const uint4 got = shfl_xor4(give, m);
+      if (up)
+        x[e] = got;
+      else
+        x[e | m] = got;
+    }
+  }
+}
+
+// The n lowest bits.
+SI_DEV uint32_t below(int n) { return n >= 32 ? 0xFFFFFFFFu : (n <= 0 ? 0u : (1u << n) - 1u); }
+
 // A pair of tiles: its queries, their positions and the key blocks.
 struct WinItem {
   int b, hk, i0;     // batch, kv head, first query
   int len, q_len;
-  int nq[2];         // live queries of each tile (0: none)
-  int t0[2];         // position of each tile's first query
+  int live, QT;      // live queries of the pair, queries of a full tile
+  int t0;            // position of the first query
   KeySpan span;      // of both tiles
-  int blocks, sink_blocks;
+  int blocks, win_blocks;
+  // live queries of tile i (0: none) and the position of its first
+  SI_DEV int nq(int i) const { return clampi(live - i * QT, 0, QT); }
+  SI_DEV int first(int i) const { return t0 + i * QT; }
 };
 
-SI_DEV bool win_item(const WinParams& p, int64_t id, WinItem& it) {
-  const int pair = (int)(id % p.pairs);
-  const int64_t bh = id / p.pairs;
-  it.b = (int)(bh / p.Hk);
-  it.hk = (int)(bh % p.Hk);
+SI_DEV bool win_item(const WinParams& p, int id, WinItem& it) {
+  const int bh = id / p.pairs, pair = id - bh * p.pairs;
+  it.b = bh / p.Hk;
+  it.hk = bh - it.b * p.Hk;
   it.i0 = pair * 2 * p.QT;
   it.len = seq_len(p.lens, it.b, p.T);
   it.q_len = seq_len(p.q_lens, it.b, p.S);
-  const int live = it.q_len - it.i0;
-  if (live <= 0) return false;
-  it.nq[0] = min(live, p.QT);
-  it.nq[1] = max(0, min(live - p.QT, p.QT));
-  it.t0[0] = it.len - it.q_len + it.i0;
-  it.t0[1] = it.t0[0] + p.QT;
-  it.span = key_span<1>(it.t0[0], it.t0[0] + it.nq[0] + it.nq[1] - 1, it.len, p.window, p.sinks);
-  it.sink_blocks = (it.span.sink_end + kN - 1) / kN;
-  it.blocks = it.sink_blocks + (it.span.end - it.span.base + kN - 1) / kN;
+  it.QT = p.QT;
+  it.live = min(it.q_len - it.i0, 2 * p.QT);
+  if (it.live <= 0) return false;
+  it.t0 = it.len - it.q_len + it.i0;
+  it.span = key_span<1>(it.t0, it.t0 + it.live - 1, it.len, p.window, p.sinks);
+  it.win_blocks = (it.span.end - it.span.base + kN - 1) / kN;
+  it.blocks = it.win_blocks + (it.span.sink_end + kN - 1) / kN;
   return true;
 }
 
 // First key of block n, the keys it holds, and its columns (a multiple of 32).
+// The sinks' blocks come last: the first maximum is then that of many keys.
 SI_DEV int block_key(const WinItem& it, int n) {
-  return n < it.sink_blocks ? n * kN : it.span.base + (n - it.sink_blocks) * kN;
+  return n < it.win_blocks ? it.span.base + n * kN : (n - it.win_blocks) * kN;
 }
 SI_DEV int block_keys(const WinItem& it, int n) {
-  return min(kN, (n < it.sink_blocks ? it.span.sink_end : it.span.end) - block_key(it, n));
+  return min(kN, (n < it.win_blocks ? it.span.end : it.span.sink_end) - block_key(it, n));
 }
 SI_DEV int columns(int keys) { return (keys + 31) & ~31; }
 
 // Whether tile i sees a key of block n.
 SI_DEV bool tile_sees(const WinParams& p, const WinItem& it, int i, int n) {
-  if (it.nq[i] == 0) return false;
+  const int nq = it.nq(i);
+  if (nq == 0) return false;
   const int j0 = block_key(it, n), j1 = j0 + block_keys(it, n) - 1;
-  const int ta = it.t0[i], tb = ta + it.nq[i] - 1;
-  return j0 <= tb && (n < it.sink_blocks || j1 > ta - p.window || j0 < p.sinks);
+  const int ta = it.first(i), tb = ta + nq - 1;
+  return j0 <= tb && (n >= it.win_blocks || j1 > ta - p.window || j0 < p.sinks);
 }
 
 }  // namespace
@@ -198,11 +238,15 @@ __global__ void __launch_bounds__(kWinThreads, 1)
   const uint32_t tmem = cs->tmem_base;
   const Ctl ctl{p.err, &cs->abort, p.timeout_ns, nullptr};
 
+  // 168 registers a thread at launch; the softmax warps, which hold a row of 128
+  // scores each, take most of the others' (128 x 64 + 256 x 216 <= 384 x 168)
+  if (warp < kSoftWarp) {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
   if (warp == 0) {
     // ------------------------------------------------------------ K and V
     uint32_t at = 0, lands = 0;  // blocks issued; blocks mended
     bool ok = true;
-    for (int64_t id = blockIdx.x; ok && id < p.items; id += gridDim.x) {
+    for (int id = blockIdx.x; ok && id < p.items; id += gridDim.x) {
       WinItem it;
       if (!win_item(p, id, it)) continue;
       for (int x = 0; ok && x < 2 * it.blocks; ++x, ++at) {
@@ -260,12 +304,12 @@ __global__ void __launch_bounds__(kWinThreads, 1)
     // ------------------------------------------------------------ Q
     if (lane == 0) {
       uint32_t n = 0;
-      for (int64_t id = blockIdx.x; id < p.items; id += gridDim.x) {
+      for (int id = blockIdx.x; id < p.items; id += gridDim.x) {
         WinItem it;
         if (!win_item(p, id, it) || it.blocks == 0) continue;
         if (!mbar_wait(smem_u32(&cs->q_empty), (n & 1u) ^ 1u, ctl)) break;
         ++n;
-        const int tiles = it.nq[1] > 0 ? 2 : 1;
+        const int tiles = it.live > p.QT ? 2 : 1;
         const uint32_t bar = smem_u32(&cs->q_full);
         mbar_arrive_expect_tx(bar, (uint32_t)(tiles * p.QT * p.G * D * 2));
         for (int i = 0; i < tiles; ++i)
@@ -285,18 +329,21 @@ __global__ void __launch_bounds__(kWinThreads, 1)
     // ------------------------------------------------------------ MMA
     if (lane == 0) {
       constexpr uint32_t idesc_o = idesc_make(1, 1, kM, D) | (1u << 16);  // V is MN-major
-      uint32_t at = 0, items = 0, np[2] = {0, 0};
+      // Q's descriptors; those of a K or V block follow from its slot
+      const uint64_t qd = sdesc_sw128(base), kd0 = sdesc_sw128(ring), vd0 = sdesc_mn(ring, C::kHalf);
+      uint32_t at = 0, items = 0, np0 = 0, np1 = 0;
       bool ok = true;
-      for (int64_t id = blockIdx.x; ok && id < p.items; id += gridDim.x) {
+      for (int id = blockIdx.x; ok && id < p.items; id += gridDim.x) {
         WinItem it;
         if (!win_item(p, id, it) || it.blocks == 0) continue;
         if (!mbar_wait(smem_u32(&cs->q_full), items & 1u, ctl)) break;
         ++items;
-        bool begun[2] = {false, false};
-        int last[2] = {-1, -1};
-        for (int n = 0; n < it.blocks; ++n)
-          for (int i = 0; i < 2; ++i)
-            if (tile_sees(p, it, i, n)) last[i] = n;
+        bool begun0 = false, begun1 = false;
+        int last0 = -1, last1 = -1;
+        for (int n = 0; n < it.blocks; ++n) {
+          if (tile_sees(p, it, 0, n)) last0 = n;
+          if (tile_sees(p, it, 1, n)) last1 = n;
+        }
         for (int n = 0; ok && n <= it.blocks; ++n) {
           const uint32_t kb = at + 2 * n, vb = at + 2 * n - 1;  // this K block, the V before it
           const int ks = (int)(kb % C::kSlots), vs = (int)(vb % C::kSlots);
@@ -305,42 +352,40 @@ __global__ void __launch_bounds__(kWinThreads, 1)
             break;
           }
           bool k_in = false;
-          for (int i = 0; ok && i < 2; ++i) {
+          const uint64_t kd = kd0 + (uint64_t)(ks * (C::kBlock >> 4));
+          const uint64_t vd = vd0 + (uint64_t)(vs * (C::kBlock >> 4));
+          const int v_steps = n > 0 ? columns(block_keys(it, n - 1)) / 16 : 0;
+          const uint32_t idesc_s =
+              n < it.blocks ? idesc_make(1, 1, kM, (uint32_t)columns(block_keys(it, n))) : 0u;
+          // one tile's turn: its P V of the block before, its Q K^T of this one
+          auto turn = [&](int i, uint32_t& np, bool& begun, int last) {
             if (n > 0 && tile_sees(p, it, i, n - 1)) {
-              if (!mbar_wait(smem_u32(&cs->p_ready[i]), np[i] & 1u, ctl)) {
-                ok = false;
-                break;
-              }
-              ++np[i];
+              if (!mbar_wait(smem_u32(&cs->p_ready[i]), np & 1u, ctl)) return false;
+              ++np;
               tc_fence_after();
-              const uint32_t va = ring + vs * C::kBlock;
-              const int steps = columns(block_keys(it, n - 1)) / 16;
-              for (int kk = 0; kk < steps; ++kk)
-                umma_ts_bf16(tmem + 256 + i * 128, tmem + i * 128 + kk * 8,
-                             sdesc_mn(va + kk * 2048, C::kHalf), idesc_o,
-                             (kk > 0 || begun[i]) ? 1u : 0u);
-              begun[i] = true;
-              if (last[i] == n - 1) umma_commit(smem_u32(&cs->o_full[i]));
+#pragma unroll 1
+              for (int kk = 0; kk < v_steps; ++kk)
+                umma_ts_bf16(tmem + 256 + i * 128, tmem + i * 128 + kk * 8, vd + kk * (2048 >> 4),
+                             idesc_o, (kk > 0 || begun) ? 1u : 0u);
+              begun = true;
+              if (last == n - 1) umma_commit(smem_u32(&cs->o_full[i]));
             }
             if (n < it.blocks && tile_sees(p, it, i, n)) {
-              if (!k_in && !mbar_wait(smem_u32(&cs->kv_full[ks]), (kb / C::kSlots) & 1u, ctl)) {
-                ok = false;
-                break;
-              }
+              if (!k_in && !mbar_wait(smem_u32(&cs->kv_full[ks]), (kb / C::kSlots) & 1u, ctl))
+                return false;
               k_in = true;
               tc_fence_after();
-              const uint32_t ka = ring + ks * C::kBlock, qa = base + i * C::kBlock;
-              const uint32_t idesc_s =
-                  idesc_make(1, 1, kM, (uint32_t)columns(block_keys(it, n)));
-#pragma unroll
+              const uint64_t qi = qd + (uint64_t)(i * (C::kBlock >> 4));
+#pragma unroll 1
               for (int kk = 0; kk < D / 16; ++kk) {
-                const uint32_t off = (kk >> 2) * C::kHalf + (kk & 3) * 32;
-                umma_bf16(tmem + i * 128, sdesc_sw128(qa + off), sdesc_sw128(ka + off), idesc_s,
-                          kk > 0 ? 1u : 0u);
+                const uint32_t off = ((kk >> 2) * C::kHalf + (kk & 3) * 32) >> 4;
+                umma_bf16(tmem + i * 128, qi + off, kd + off, idesc_s, kk > 0 ? 1u : 0u);
               }
               umma_commit(smem_u32(&cs->s_full[i]));
             }
-          }
+            return true;
+          };
+          ok = turn(0, np0, begun0, last0) && turn(1, np1, begun1, last1);
           // a slot is given back only once it has been filled
           if (ok && n < it.blocks && !k_in)
             ok = mbar_wait(smem_u32(&cs->kv_full[ks]), (kb / C::kSlots) & 1u, ctl);
@@ -353,7 +398,9 @@ __global__ void __launch_bounds__(kWinThreads, 1)
       }
     }
     __syncwarp();
-  } else if (warp >= kSoftWarp) {
+  }
+  } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
     // ------------------------------------------------------------ softmax
     const int i = (warp - kSoftWarp) >> 2;
     const int row = (warp & 3) * 32 + lane;
@@ -362,12 +409,13 @@ __global__ void __launch_bounds__(kWinThreads, 1)
     const float sl2 = p.scale_log2;
     uint32_t ns = 0, no = 0;
     bool stop = false;
-    for (int64_t id = blockIdx.x; !stop && id < p.items; id += gridDim.x) {
+    for (int id = blockIdx.x; !stop && id < p.items; id += gridDim.x) {
       WinItem it;
-      if (!win_item(p, id, it) || it.nq[i] == 0) continue;
+      if (!win_item(p, id, it) || it.nq(i) == 0) continue;
       const int qi = row / p.G;  // query of the row within the tile
-      const int ta = it.t0[i], tb = ta + it.nq[i] - 1;
-      const int t = ta + min(qi, it.nq[i] - 1);
+      const int nq = it.nq(i);
+      const int ta = it.first(i), tb = ta + nq - 1;
+      const int t = ta + min(qi, nq - 1);
       float m = neg_inf(), l = 0.0f;
       bool any = false;
       for (int n = 0; n < it.blocks; ++n) {
@@ -379,77 +427,84 @@ __global__ void __launch_bounds__(kWinThreads, 1)
         ++ns;
         tc_fence_after();
         const int j0 = block_key(it, n), keys = block_keys(it, n), chunks = columns(keys) / 32;
-        // whether every row of the tile sees all of chunk c
-        auto whole = [&](int c) {
-          const int a = j0 + 32 * c, z = a + 31;
-          return 32 * c + 32 <= keys && z <= ta && (a > tb - p.window || z < p.sinks);
-        };
-        auto mask = [&](int c, float (&v)[32]) {
+        // the tile's columns, 32 at a time, stay in registers from here on
+        float v[4][32];
 #pragma unroll
-          for (int e = 0; e < 32; ++e) {
-            const int j = j0 + 32 * c + e;
-            if (32 * c + e >= keys || !sees(j, t, it.len, p.window, p.sinks)) v[e] = neg_inf();
+        for (int c = 0; c < 4; ++c)
+          if (c < chunks) tmem_ld32(s_col + c * 32, v[c]);
+        tmem_ld_wait();
+        float mx[4] = {neg_inf(), neg_inf(), neg_inf(), neg_inf()};
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          pin32(v[c]);
+          if (c < chunks) {
+            // columns that some row of the tile does not see: the row's own are
+            // an interval of them and the sinks
+            const int a = j0 + 32 * c, z = a + 31;
+            if (!(32 * c + 32 <= keys && z <= ta && (a > tb - p.window || z < p.sinks))) {
+              const uint32_t seen = below(min(t + 1, j0 + keys) - a) &
+                                    (~below(t + 1 - p.window - a) | below(p.sinks - a));
+              asm volatile("" ::"r"(seen));  // a branch, and not 32 selections for every chunk
+#pragma unroll
+              for (int e = 0; e < 32; ++e)
+                if (!((seen >> e) & 1u)) v[c][e] = neg_inf();
+            }
+#pragma unroll
+            for (int e = 0; e < 32; ++e) mx[e & 3] = fmaxf(mx[e & 3], v[c][e]);
           }
-        };
-        float v[32], mx[4] = {neg_inf(), neg_inf(), neg_inf(), neg_inf()};
-#pragma unroll 1
-        for (int c = 0; c < chunks; ++c) {
-          tmem_ld32(s_col + c * 32, v);
-          tmem_ld_wait();
-          pin32(v);
-          if (!whole(c)) mask(c, v);
-#pragma unroll
-          for (int e = 0; e < 32; ++e) mx[e & 3] = fmaxf(mx[e & 3], v[e]);
         }
         const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * sl2;
-        // the first maximum is taken as it is; later ones once they pass it by 2^8
+        // the first maximum is taken as it is; later ones once they pass it by 2^16
         const bool grow = top > (m == neg_inf() ? m : m + kGrow);
         if (__any_sync(0xFFFFFFFFu, grow)) {
           const float a = grow ? ex2(m - top) : 1.0f;
           if (any) {
             l *= a;
 #pragma unroll 1
-            for (int c = 0; c < D / 32; ++c) {
-              tmem_ld32(o_col + c * 32, v);
+            for (int c = 0; c < D / 16; ++c) {
+              uint32_t w[16];
+              tmem_ld16(o_col + c * 16, w);
               tmem_ld_wait();
-              pin32(v);
 #pragma unroll
-              for (int e = 0; e < 32; ++e) v[e] *= a;
-              uint32_t w[2][16];
-#pragma unroll
-              for (int e = 0; e < 32; ++e) w[e >> 4][e & 15] = __float_as_uint(v[e]);
-              tmem_st16(o_col + c * 32, w[0]);
-              tmem_st16(o_col + c * 32 + 16, w[1]);
+              for (int e = 0; e < 16; ++e) {
+                asm volatile("" : "+r"(w[e]));
+                w[e] = __float_as_uint(__uint_as_float(w[e]) * a);
+              }
+              tmem_st16(o_col + c * 16, w);
             }
             tmem_st_wait();
           }
           if (grow) m = top;
         }
         any = true;
-        const float sub = m == neg_inf() ? 0.0f : m;
-        float ls[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll 1
-        for (int c = 0; c < chunks; ++c) {
-          tmem_ld32(s_col + c * 32, v);
-          tmem_ld_wait();
-          pin32(v);
-          if (!whole(c)) mask(c, v);
-          uint32_t w[16];
+        const float sub = m == neg_inf() ? 0.0f : -m;
+        const uint64_t sl22 = pair2(sl2, sl2), sub2 = pair2(sub, sub);
+        uint64_t ls[2] = {0ull, 0ull};
 #pragma unroll
-          for (int e = 0; e < 32; e += 2) {
-            const float x = ex2(fmaf(v[e], sl2, -sub)), y = ex2(fmaf(v[e + 1], sl2, -sub));
-            ls[(e >> 1) & 3] += x + y;
-            w[e >> 1] = pack_bf16x2(x, y);
+        for (int c = 0; c < 4; ++c) {
+          if (c < chunks) {
+            uint32_t w[16];
+#pragma unroll
+            for (int e = 0; e < 32; e += 2) {
+              float x, y;
+              unpair2(fma2(pair2(v[c][e], v[c][e + 1]), sl22, sub2), x, y);
+              x = ex2(x);
+              y = ex2(y);
+              ls[(e >> 1) & 1] = add2(ls[(e >> 1) & 1], pair2(x, y));
+              w[e >> 1] = pack_bf16x2(x, y);
+            }
+            tmem_st16(s_col + c * 16, w);
           }
-          tmem_st16(s_col + c * 16, w);
         }
-        l += (ls[0] + ls[1]) + (ls[2] + ls[3]);
+        float l0, l1;
+        unpair2(add2(ls[0], ls[1]), l0, l1);
+        l += l0 + l1;
         tmem_st_wait();
         tc_fence_before();
         mbar_arrive(smem_u32(&cs->p_ready[i]));
       }
       if (stop) break;
-      const bool live = qi < it.nq[i];
+      const bool live = qi < nq;
       const int64_t orow =
           ((int64_t)it.b * p.S + it.i0 + i * p.QT + qi) * p.H + it.hk * p.G + row % p.G;
       bool bad = false;
@@ -458,6 +513,10 @@ __global__ void __launch_bounds__(kWinThreads, 1)
         ++no;
         tc_fence_after();
         const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+        int64_t row_of[4];  // rows of this lane's group of four, -1: not live
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          row_of[e] = __shfl_sync(0xFFFFFFFFu, live ? orow : -1, (lane & ~3) + e);
         float v[32];
 #pragma unroll 1
         for (int c = 0; c < D / 32; ++c) {
@@ -471,11 +530,18 @@ __global__ void __launch_bounds__(kWinThreads, 1)
             bad |= x != x || y != y;
             w[e >> 1] = pack_bf16x2(x, y);
           }
-          if (live) {
-            uint4* dst = reinterpret_cast<uint4*>(p.out + orow * D + c * 32);
+          // four lanes exchange 16-byte pieces, so that a store writes 64
+          // consecutive bytes of each of eight rows
+          uint4 piece[4];
 #pragma unroll
-            for (int e = 0; e < 4; ++e)
-              dst[e] = make_uint4(w[4 * e], w[4 * e + 1], w[4 * e + 2], w[4 * e + 3]);
+          for (int e = 0; e < 4; ++e)
+            piece[e] = make_uint4(w[4 * e], w[4 * e + 1], w[4 * e + 2], w[4 * e + 3]);
+          transpose4(piece, lane);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const int64_t o = row_of[e];
+            if (o >= 0)
+              reinterpret_cast<uint4*>(p.out + o * D + c * 32)[lane & 3] = piece[e];
           }
         }
         tc_fence_before();
@@ -498,10 +564,11 @@ __global__ void __launch_bounds__(kWinThreads, 1)
         float rm = neg_inf(), rl = 0.0f, ro[D / 32];
 #pragma unroll
         for (int e = 0; e < D / 32; ++e) ro[e] = 0.0f;
-        exact_row_keys<D>(p.q + orr * D, p.k + first, p.v + first, stride, 0, it.span.sink_end, tr,
-                          it.len, p.window, p.sinks, sl2, lane, rm, rl, ro);
-        exact_row_keys<D>(p.q + orr * D, p.k + first, p.v + first, stride, it.span.base,
-                          it.span.end, tr, it.len, p.window, p.sinks, sl2, lane, rm, rl, ro);
+#pragma unroll 1
+        for (int part = 0; part < 2; ++part)
+          exact_row_keys<D>(p.q + orr * D, p.k + first, p.v + first, stride,
+                            part ? it.span.base : 0, part ? it.span.end : it.span.sink_end, tr,
+                            it.len, p.window, p.sinks, sl2, lane, rm, rl, ro);
         const float rinv = rl == 0.0f ? 0.0f : 1.0f / rl;
         uint32_t* dst = reinterpret_cast<uint32_t*>(p.out + orr * D) + lane * (D / 64);
 #pragma unroll
