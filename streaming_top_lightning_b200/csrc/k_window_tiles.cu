@@ -45,22 +45,24 @@ namespace si {
 namespace {
 
 constexpr int kM = 128;        // rows of a tile (MMA M)
-constexpr int kN = 128;        // keys of a block
+constexpr int kN = 64;         // keys of a block
 constexpr int kWinThreads = 384;
 constexpr int kSoftWarp = 4;   // softmax warps 4-7: tile 0, 8-11: tile 1
 constexpr float kGrow = 16.0f; // log2 growth of a maximum that rescales O
 
 template <int D>
 struct WinCfg {
-  static constexpr uint32_t kBlock = kN * D * 2;  // one K, V or Q block
+  static constexpr uint32_t kQ = kM * D * 2;      // one Q tile
+  static constexpr uint32_t kQHalf = kM * 128;    // its 64-column half
+  static constexpr uint32_t kBlock = kN * D * 2;  // one K or V block
   static constexpr uint32_t kHalf = kN * 128;     // its 64-column half
-  static constexpr int kSlots = D == 128 ? 5 : 8;
-  static constexpr size_t kSmem = (2 + kSlots) * (size_t)kBlock + 1024 + 512;
+  static constexpr int kSlots = D == 128 ? 10 : 12;
+  static constexpr size_t kSmem = 2 * (size_t)kQ + kSlots * (size_t)kBlock + 1024 + 512;
 };
 
 struct WinCtl {
-  uint64_t kv_full[8], kv_empty[8], kv_land;
-  uint64_t q_full, q_empty, s_full[2], p_ready[2], o_full[2];
+  uint64_t kv_full[12], kv_empty[12], kv_land;
+  uint64_t q_full, q_empty, s_full[2][2], p_ready[2][2], pv_done[2][2];  // [tile][buffer]
   uint32_t tmem_base;
   uint32_t abort;
 };
@@ -120,6 +122,19 @@ SI_DEV void pin32(float (&v)[32]) {
                  "+f"(v[i + 5]), "+f"(v[i + 6]), "+f"(v[i + 7]));
 }
 
+// The first lane's value, which the compiler then knows to be the warp's.
+template <class T>
+SI_DEV T uniform(T x) {
+  return (T)__shfl_sync(0xFFFFFFFFu, (int)x, 0);
+}
+SI_DEV bool elect_one() {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\telect.sync _|p, 0xFFFFFFFF;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(r));
+  return r != 0u;
+}
+
 // Transposes the 4 x 4 pieces of four neighbouring lanes: lane q's piece e
 // becomes lane e's piece q.
 SI_DEV uint4 shfl_xor4(uint4 x, int m) {
@@ -155,6 +170,7 @@ struct WinItem {
   int t0;            // position of the first query
   KeySpan span;      // of both tiles
   int blocks, win_blocks;
+  int from[2], to[2];  // the window blocks that each tile sees; both see the sinks
   // live queries of tile i (0: none) and the position of its first
   SI_DEV int nq(int i) const { return clampi(live - i * QT, 0, QT); }
   SI_DEV int first(int i) const { return t0 + i * QT; }
@@ -174,6 +190,14 @@ SI_DEV bool win_item(const WinParams& p, int id, WinItem& it) {
   it.span = key_span<1>(it.t0, it.t0 + it.live - 1, it.len, p.window, p.sinks);
   it.win_blocks = (it.span.end - it.span.base + kN - 1) / kN;
   it.blocks = it.win_blocks + (it.span.sink_end + kN - 1) / kN;
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    // first key of the tile's first query, last position of its last
+    const int nq = it.nq(i), lo = max(0, it.first(i) - p.window + 1);
+    const int hi = min(it.span.end, it.first(i) + nq);
+    it.from[i] = max(0, (p.sinks > it.span.base ? 0 : lo - it.span.base) / kN);
+    it.to[i] = nq == 0 || hi <= 0 ? 0 : (hi - it.span.base + kN - 1) / kN;
+  }
   return true;
 }
 
@@ -187,13 +211,28 @@ SI_DEV int block_keys(const WinItem& it, int n) {
 }
 SI_DEV int columns(int keys) { return (keys + 31) & ~31; }
 
-// Whether tile i sees a key of block n.
-SI_DEV bool tile_sees(const WinParams& p, const WinItem& it, int i, int n) {
-  const int nq = it.nq(i);
-  if (nq == 0) return false;
-  const int j0 = block_key(it, n), j1 = j0 + block_keys(it, n) - 1;
-  const int ta = it.first(i), tb = ta + nq - 1;
-  return j0 <= tb && (n >= it.win_blocks || j1 > ta - p.window || j0 < p.sinks);
+// The x-th block of an item's ring, in the order of use: K0 K1 V0 K2 V1 K3 ...
+// (with one block: K0 V0), and where a K or V block stands in that order.
+SI_DEV int ring_block(int blocks, int x, bool& is_v) {
+  if (x < 2 && x < blocks) {
+    is_v = false;
+    return x;
+  }
+  if (x >= 2 * blocks - 2 || blocks < 2) {  // the last two values
+    is_v = true;
+    return x - blocks;
+  }
+  is_v = (x & 1) == 0;
+  return is_v ? (x - 2) >> 1 : (x + 1) >> 1;
+}
+SI_DEV int ring_k(int n) { return n < 2 ? n : 2 * n - 1; }
+SI_DEV int ring_v(int blocks, int n) { return n + 2 < blocks ? 2 * n + 2 : blocks + n; }
+
+// Whether tile i sees a key of block n.  (Where there are sinks' blocks, every
+// query of the pair lies behind them.)
+template <int I>
+SI_DEV bool tile_sees(const WinItem& it, int n) {
+  return (n >= it.from[I] && n < it.to[I]) || (n >= it.win_blocks && n < it.blocks && it.to[I] > 0);
 }
 
 }  // namespace
@@ -208,9 +247,9 @@ __global__ void __launch_bounds__(kWinThreads, 1)
                                              ~uintptr_t(1023));
   // [Q0 | Q1 | ring | ctl]
   const uint32_t base = smem_u32(smem);
-  const uint32_t ring = base + 2 * C::kBlock;
-  WinCtl* cs = reinterpret_cast<WinCtl*>(smem + (2 + C::kSlots) * (size_t)C::kBlock);
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const uint32_t ring = base + 2 * C::kQ;
+  WinCtl* cs = reinterpret_cast<WinCtl*>(smem + 2 * (size_t)C::kQ + C::kSlots * (size_t)C::kBlock);
+  const int tid = threadIdx.x, warp = uniform(tid >> 5), lane = tid & 31;
 
   if (tid == 0) {
     for (int i = 0; i < C::kSlots; ++i) {
@@ -221,9 +260,11 @@ __global__ void __launch_bounds__(kWinThreads, 1)
     mbar_init(smem_u32(&cs->q_full), 1);
     mbar_init(smem_u32(&cs->q_empty), 1);
     for (int i = 0; i < 2; ++i) {
-      mbar_init(smem_u32(&cs->s_full[i]), 1);
-      mbar_init(smem_u32(&cs->p_ready[i]), kM);
-      mbar_init(smem_u32(&cs->o_full[i]), 1);
+      for (int x = 0; x < 2; ++x) {
+        mbar_init(smem_u32(&cs->s_full[i][x]), 1);
+        mbar_init(smem_u32(&cs->p_ready[i][x]), kM);
+        mbar_init(smem_u32(&cs->pv_done[i][x]), 1);
+      }
     }
     cs->abort = 0u;
     mbar_fence_init();
@@ -238,10 +279,6 @@ __global__ void __launch_bounds__(kWinThreads, 1)
   const uint32_t tmem = cs->tmem_base;
   const Ctl ctl{p.err, &cs->abort, p.timeout_ns, nullptr};
 
-  // 168 registers a thread at launch; the softmax warps, which hold a row of 128
-  // scores each, take most of the others' (128 x 64 + 256 x 216 <= 384 x 168)
-  if (warp < kSoftWarp) {
-  asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
   if (warp == 0) {
     // ------------------------------------------------------------ K and V
     uint32_t at = 0, lands = 0;  // blocks issued; blocks mended
@@ -250,8 +287,8 @@ __global__ void __launch_bounds__(kWinThreads, 1)
       WinItem it;
       if (!win_item(p, id, it)) continue;
       for (int x = 0; ok && x < 2 * it.blocks; ++x, ++at) {
-        const int n = x >> 1;
-        const bool is_v = (x & 1) != 0;
+        bool is_v;
+        const int n = ring_block(it.blocks, x, is_v);
         const int slot = (int)(at % C::kSlots);
         if (!mbar_wait_warp(smem_u32(&cs->kv_empty[slot]), ((at / C::kSlots) & 1u) ^ 1u, ctl)) {
           ok = false;
@@ -315,7 +352,7 @@ __global__ void __launch_bounds__(kWinThreads, 1)
         for (int i = 0; i < tiles; ++i)
 #pragma unroll
           for (int h = 0; h < D / 64; ++h)
-            tma_load_4d(base + i * C::kBlock + h * C::kHalf, &tm_q, bar, 64 * h, it.hk * p.G,
+            tma_load_4d(base + i * C::kQ + h * C::kQHalf, &tm_q, bar, 64 * h, it.hk * p.G,
                         it.i0 + i * p.QT, it.b);
       }
       if (*ctl.abort && n > 0) {
@@ -327,87 +364,112 @@ __global__ void __launch_bounds__(kWinThreads, 1)
     __syncwarp();
   } else if (warp == 1) {
     // ------------------------------------------------------------ MMA
-    if (lane == 0) {
-      constexpr uint32_t idesc_o = idesc_make(1, 1, kM, D) | (1u << 16);  // V is MN-major
-      // Q's descriptors; those of a K or V block follow from its slot
-      const uint64_t qd = sdesc_sw128(base), kd0 = sdesc_sw128(ring), vd0 = sdesc_mn(ring, C::kHalf);
-      uint32_t at = 0, items = 0, np0 = 0, np1 = 0;
-      bool ok = true;
-      for (int id = blockIdx.x; ok && id < p.items; id += gridDim.x) {
-        WinItem it;
-        if (!win_item(p, id, it) || it.blocks == 0) continue;
-        if (!mbar_wait(smem_u32(&cs->q_full), items & 1u, ctl)) break;
-        ++items;
-        bool begun0 = false, begun1 = false;
-        int last0 = -1, last1 = -1;
-        for (int n = 0; n < it.blocks; ++n) {
-          if (tile_sees(p, it, 0, n)) last0 = n;
-          if (tile_sees(p, it, 1, n)) last1 = n;
-        }
-        for (int n = 0; ok && n <= it.blocks; ++n) {
-          const uint32_t kb = at + 2 * n, vb = at + 2 * n - 1;  // this K block, the V before it
-          const int ks = (int)(kb % C::kSlots), vs = (int)(vb % C::kSlots);
-          if (n > 0 && !mbar_wait(smem_u32(&cs->kv_full[vs]), (vb / C::kSlots) & 1u, ctl)) {
-            ok = false;
-            break;
-          }
-          bool k_in = false;
-          const uint64_t kd = kd0 + (uint64_t)(ks * (C::kBlock >> 4));
-          const uint64_t vd = vd0 + (uint64_t)(vs * (C::kBlock >> 4));
-          const int v_steps = n > 0 ? columns(block_keys(it, n - 1)) / 16 : 0;
-          const uint32_t idesc_s =
-              n < it.blocks ? idesc_make(1, 1, kM, (uint32_t)columns(block_keys(it, n))) : 0u;
-          // one tile's turn: its P V of the block before, its Q K^T of this one
-          auto turn = [&](int i, uint32_t& np, bool& begun, int last) {
-            if (n > 0 && tile_sees(p, it, i, n - 1)) {
-              if (!mbar_wait(smem_u32(&cs->p_ready[i]), np & 1u, ctl)) return false;
-              ++np;
-              tc_fence_after();
-#pragma unroll 1
-              for (int kk = 0; kk < v_steps; ++kk)
-                umma_ts_bf16(tmem + 256 + i * 128, tmem + i * 128 + kk * 8, vd + kk * (2048 >> 4),
-                             idesc_o, (kk > 0 || begun) ? 1u : 0u);
-              begun = true;
-              if (last == n - 1) umma_commit(smem_u32(&cs->o_full[i]));
-            }
-            if (n < it.blocks && tile_sees(p, it, i, n)) {
-              if (!k_in && !mbar_wait(smem_u32(&cs->kv_full[ks]), (kb / C::kSlots) & 1u, ctl))
-                return false;
-              k_in = true;
-              tc_fence_after();
-              const uint64_t qi = qd + (uint64_t)(i * (C::kBlock >> 4));
-#pragma unroll 1
-              for (int kk = 0; kk < D / 16; ++kk) {
-                const uint32_t off = ((kk >> 2) * C::kHalf + (kk & 3) * 32) >> 4;
-                umma_bf16(tmem + i * 128, qi + off, kd + off, idesc_s, kk > 0 ? 1u : 0u);
-              }
-              umma_commit(smem_u32(&cs->s_full[i]));
-            }
-            return true;
-          };
-          ok = turn(0, np0, begun0, last0) && turn(1, np1, begun1, last1);
-          // a slot is given back only once it has been filled
-          if (ok && n < it.blocks && !k_in)
-            ok = mbar_wait(smem_u32(&cs->kv_full[ks]), (kb / C::kSlots) & 1u, ctl);
-          if (!ok) break;
-          if (n > 0) umma_commit(smem_u32(&cs->kv_empty[vs]));
-          if (n < it.blocks) umma_commit(smem_u32(&cs->kv_empty[ks]));
-          if (n == it.blocks - 1) umma_commit(smem_u32(&cs->q_empty));
-        }
-        at += 2 * it.blocks;
+    // The whole warp goes through the loop with values that are the same in
+    // every lane, and one lane issues: descriptors then stay in uniform
+    // registers.  (Issued from code that one lane alone runs, each of an MMA's
+    // operands is moved there first, about 90 cycles an instruction.)
+    const bool leader = elect_one();
+    constexpr uint32_t idesc_o = idesc_make(1, 1, kM, D) | (1u << 16);  // V is MN-major
+    const uint32_t u_ring = uniform(ring), u_base = uniform(base), u_tmem = uniform(tmem);
+    uint32_t at = 0, items = 0, np0 = 0, np1 = 0;
+    bool ok = true;
+    for (int id = blockIdx.x; ok && id < p.items; id += gridDim.x) {
+      WinItem it;
+      if (!uniform(win_item(p, id, it))) continue;
+      it.blocks = uniform(it.blocks);
+      if (it.blocks == 0) continue;
+      it.win_blocks = uniform(it.win_blocks);
+      it.span.base = uniform(it.span.base);
+      it.span.end = uniform(it.span.end);
+      it.span.sink_end = uniform(it.span.sink_end);
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        it.from[i] = uniform(it.from[i]);
+        it.to[i] = uniform(it.to[i]);
       }
+      if (!mbar_wait_warp(smem_u32(&cs->q_full), items & 1u, ctl)) break;
+      ++items;
+      uint32_t begun0 = 0u, begun1 = 0u;
+      // S_i = Q_i K^T of block n into buffer n % 2
+      auto scores = [&](int i, int n, uint32_t slot) {
+        const uint64_t kd = sdesc_sw128(u_ring + slot * C::kBlock);
+        const uint64_t qi = sdesc_sw128(u_base + i * C::kQ);
+        const uint32_t idesc_s = idesc_make(1, 1, kM, (uint32_t)columns(block_keys(it, n)));
+        const uint32_t d = u_tmem + i * 128 + (n & 1) * kN;
+        if (leader) {
+#pragma unroll
+          for (int kk = 0; kk < D / 16; ++kk)
+            umma_bf16(d, qi + (((kk >> 2) * C::kQHalf + (kk & 3) * 32) >> 4),
+                      kd + (((kk >> 2) * C::kHalf + (kk & 3) * 32) >> 4), idesc_s, kk > 0 ? 1u : 0u);
+          umma_commit(smem_u32(&cs->s_full[i][n & 1]));
+        }
+        __syncwarp();
+      };
+      // O_i += P_i V of block n
+      auto values = [&](int i, int n, uint32_t slot, uint32_t& begun) {
+        const uint64_t vd = sdesc_mn(u_ring + slot * C::kBlock, C::kHalf);
+        const uint32_t a = u_tmem + i * 128 + (n & 1) * kN, d = u_tmem + 256 + i * 128;
+        const int steps = columns(block_keys(it, n)) / 16;
+        if (leader) {
+#pragma unroll
+          for (int kk = 0; kk < kN / 16; ++kk)
+            if (kk < steps)
+              umma_ts_bf16(d, a + kk * 8, vd + kk * (2048 >> 4), idesc_o, kk > 0 ? 1u : begun);
+          umma_commit(smem_u32(&cs->pv_done[i][n & 1]));
+        }
+        __syncwarp();
+        begun = 1u;
+      };
+      auto landed = [&](uint32_t x, uint32_t slot) {
+        return mbar_wait_warp(smem_u32(&cs->kv_full[slot]), (x / C::kSlots) & 1u, ctl);
+      };
+      // the first two blocks' scores, then for each block its values and the
+      // scores of the one two further on
+      for (int n = -2; ok && n < it.blocks; ++n) {
+        const uint32_t xv = at + ring_v(it.blocks, n), xk = at + ring_k(n + 2);
+        const uint32_t sv = xv % C::kSlots, sk = xk % C::kSlots;
+        const bool more = n + 2 < it.blocks;
+        if ((n >= 0 && !landed(xv, sv)) || (more && !landed(xk, sk))) {
+          ok = false;
+          break;
+        }
+        if (n >= 0 && tile_sees<0>(it, n)) {
+          if (!(ok = mbar_wait_warp(smem_u32(&cs->p_ready[0][n & 1]), (np0 >> (n & 1)) & 1u, ctl)))
+            break;
+          np0 ^= 1u << (n & 1);
+          tc_fence_after();
+          values(0, n, sv, begun0);
+        }
+        if (more && tile_sees<0>(it, n + 2)) scores(0, n + 2, sk);
+        if (n >= 0 && tile_sees<1>(it, n)) {
+          if (!(ok = mbar_wait_warp(smem_u32(&cs->p_ready[1][n & 1]), (np1 >> (n & 1)) & 1u, ctl)))
+            break;
+          np1 ^= 1u << (n & 1);
+          tc_fence_after();
+          values(1, n, sv, begun1);
+        }
+        if (more && tile_sees<1>(it, n + 2)) scores(1, n + 2, sk);
+        if (leader) {
+          if (n >= 0) umma_commit(smem_u32(&cs->kv_empty[sv]));
+          if (more) umma_commit(smem_u32(&cs->kv_empty[sk]));
+          if (n + 3 == it.blocks) umma_commit(smem_u32(&cs->q_empty));
+        }
+        __syncwarp();
+      }
+      at += 2 * it.blocks;
     }
-    __syncwarp();
-  }
-  } else {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
+  } else if (warp >= kSoftWarp) {
     // ------------------------------------------------------------ softmax
     const int i = (warp - kSoftWarp) >> 2;
     const int row = (warp & 3) * 32 + lane;
     const uint32_t lane_base = tmem + ((uint32_t)((warp & 3) * 32) << 16);
     const uint32_t s_col = lane_base + i * 128, o_col = lane_base + 256 + i * 128;
     const float sl2 = p.scale_log2;
-    uint32_t ns = 0, no = 0;
+    // parities of each buffer's next scores and next values; the buffer whose
+    // values were the last (a barrier per buffer, because those of the block
+    // before the last are known to be done only where they had the same one)
+    uint32_t ns = 0, npv = 0;
+    int last = 0;
     bool stop = false;
     for (int id = blockIdx.x; !stop && id < p.items; id += gridDim.x) {
       WinItem it;
@@ -419,23 +481,25 @@ __global__ void __launch_bounds__(kWinThreads, 1)
       float m = neg_inf(), l = 0.0f;
       bool any = false;
       for (int n = 0; n < it.blocks; ++n) {
-        if (!tile_sees(p, it, i, n)) continue;
-        if (!mbar_wait_warp(smem_u32(&cs->s_full[i]), ns & 1u, ctl)) {
+        if (!(i ? tile_sees<1>(it, n) : tile_sees<0>(it, n))) continue;
+        const int buf = n & 1;
+        if (!mbar_wait_warp(smem_u32(&cs->s_full[i][buf]), (ns >> buf) & 1u, ctl)) {
           stop = true;
           break;
         }
-        ++ns;
+        ns ^= 1u << buf;
         tc_fence_after();
+        const uint32_t b_col = s_col + buf * kN;
         const int j0 = block_key(it, n), keys = block_keys(it, n), chunks = columns(keys) / 32;
         // the tile's columns, 32 at a time, stay in registers from here on
-        float v[4][32];
+        float v[kN / 32][32];
 #pragma unroll
-        for (int c = 0; c < 4; ++c)
-          if (c < chunks) tmem_ld32(s_col + c * 32, v[c]);
+        for (int c = 0; c < kN / 32; ++c)
+          if (c < chunks) tmem_ld32(b_col + c * 32, v[c]);
         tmem_ld_wait();
         float mx[4] = {neg_inf(), neg_inf(), neg_inf(), neg_inf()};
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
+        for (int c = 0; c < kN / 32; ++c) {
           pin32(v[c]);
           if (c < chunks) {
             // columns that some row of the tile does not see: the row's own are
@@ -459,6 +523,12 @@ __global__ void __launch_bounds__(kWinThreads, 1)
         if (__any_sync(0xFFFFFFFFu, grow)) {
           const float a = grow ? ex2(m - top) : 1.0f;
           if (any) {
+            // nobody writes O once the values of the block before are in it
+            if (!mbar_wait_warp(smem_u32(&cs->pv_done[i][last]), ((npv >> last) & 1u) ^ 1u, ctl)) {
+              stop = true;
+              break;
+            }
+            tc_fence_after();
             l *= a;
 #pragma unroll 1
             for (int c = 0; c < D / 16; ++c) {
@@ -473,6 +543,7 @@ __global__ void __launch_bounds__(kWinThreads, 1)
               tmem_st16(o_col + c * 16, w);
             }
             tmem_st_wait();
+            tc_fence_before();
           }
           if (grow) m = top;
         }
@@ -481,7 +552,7 @@ __global__ void __launch_bounds__(kWinThreads, 1)
         const uint64_t sl22 = pair2(sl2, sl2), sub2 = pair2(sub, sub);
         uint64_t ls[2] = {0ull, 0ull};
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
+        for (int c = 0; c < kN / 32; ++c) {
           if (c < chunks) {
             uint32_t w[16];
 #pragma unroll
@@ -493,7 +564,7 @@ __global__ void __launch_bounds__(kWinThreads, 1)
               ls[(e >> 1) & 1] = add2(ls[(e >> 1) & 1], pair2(x, y));
               w[e >> 1] = pack_bf16x2(x, y);
             }
-            tmem_st16(s_col + c * 16, w);
+            tmem_st16(b_col + c * 16, w);
           }
         }
         float l0, l1;
@@ -501,7 +572,9 @@ __global__ void __launch_bounds__(kWinThreads, 1)
         l += l0 + l1;
         tmem_st_wait();
         tc_fence_before();
-        mbar_arrive(smem_u32(&cs->p_ready[i]));
+        mbar_arrive(smem_u32(&cs->p_ready[i][buf]));
+        npv ^= 1u << buf;
+        last = buf;
       }
       if (stop) break;
       const bool live = qi < nq;
@@ -509,8 +582,7 @@ __global__ void __launch_bounds__(kWinThreads, 1)
           ((int64_t)it.b * p.S + it.i0 + i * p.QT + qi) * p.H + it.hk * p.G + row % p.G;
       bool bad = false;
       if (any) {
-        if (!mbar_wait_warp(smem_u32(&cs->o_full[i]), no & 1u, ctl)) break;
-        ++no;
+        if (!mbar_wait_warp(smem_u32(&cs->pv_done[i][last]), ((npv >> last) & 1u) ^ 1u, ctl)) break;
         tc_fence_after();
         const float inv = l == 0.0f ? 0.0f : 1.0f / l;
         int64_t row_of[4];  // rows of this lane's group of four, -1: not live
