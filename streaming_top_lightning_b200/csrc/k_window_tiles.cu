@@ -48,6 +48,7 @@ constexpr int kM = 128;        // rows of a tile (MMA M)
 constexpr int kN = 64;         // keys of a block
 constexpr int kWinThreads = 384;
 constexpr int kSoftWarp = 4;   // softmax warps 4-7: tile 0, 8-11: tile 1
+constexpr int kPolyEvery = 4;  // every so many pairs of exponentials run as polynomials
 constexpr float kGrow = 16.0f; // log2 growth of a maximum that rescales O
 
 template <int D>
@@ -170,7 +171,9 @@ struct WinItem {
   int t0;            // position of the first query
   KeySpan span;      // of both tiles
   int blocks, win_blocks;
-  int from[2], to[2];  // the window blocks that each tile sees; both see the sinks
+  // the window blocks that each tile sees; both see the sinks (where there are
+  // blocks of them, every query of the pair lies behind them)
+  int from[2], to[2];
   // live queries of tile i (0: none) and the position of its first
   SI_DEV int nq(int i) const { return clampi(live - i * QT, 0, QT); }
   SI_DEV int first(int i) const { return t0 + i * QT; }
@@ -212,7 +215,7 @@ SI_DEV int block_keys(const WinItem& it, int n) {
 SI_DEV int columns(int keys) { return (keys + 31) & ~31; }
 
 // The x-th block of an item's ring, in the order of use: K0 K1 V0 K2 V1 K3 ...
-// (with one block: K0 V0), and where a K or V block stands in that order.
+// (with one block: K0 V0).
 SI_DEV int ring_block(int blocks, int x, bool& is_v) {
   if (x < 2 && x < blocks) {
     is_v = false;
@@ -225,16 +228,6 @@ SI_DEV int ring_block(int blocks, int x, bool& is_v) {
   is_v = (x & 1) == 0;
   return is_v ? (x - 2) >> 1 : (x + 1) >> 1;
 }
-SI_DEV int ring_k(int n) { return n < 2 ? n : 2 * n - 1; }
-SI_DEV int ring_v(int blocks, int n) { return n + 2 < blocks ? 2 * n + 2 : blocks + n; }
-
-// Whether tile i sees a key of block n.  (Where there are sinks' blocks, every
-// query of the pair lies behind them.)
-template <int I>
-SI_DEV bool tile_sees(const WinItem& it, int n) {
-  return (n >= it.from[I] && n < it.to[I]) || (n >= it.win_blocks && n < it.blocks && it.to[I] > 0);
-}
-
 }  // namespace
 
 template <int D>
@@ -254,11 +247,11 @@ __global__ void __launch_bounds__(kWinThreads, 1)
   if (tid == 0) {
     for (int i = 0; i < C::kSlots; ++i) {
       mbar_init(smem_u32(&cs->kv_full[i]), 1);
-      mbar_init(smem_u32(&cs->kv_empty[i]), 1);
+      mbar_init(smem_u32(&cs->kv_empty[i]), 2);  // both MMA warps
     }
     mbar_init(smem_u32(&cs->kv_land), 1);
     mbar_init(smem_u32(&cs->q_full), 1);
-    mbar_init(smem_u32(&cs->q_empty), 1);
+    mbar_init(smem_u32(&cs->q_empty), 2);
     for (int i = 0; i < 2; ++i) {
       for (int x = 0; x < 2; ++x) {
         mbar_init(smem_u32(&cs->s_full[i][x]), 1);
@@ -362,101 +355,97 @@ __global__ void __launch_bounds__(kWinThreads, 1)
       }
     }
     __syncwarp();
-  } else if (warp == 1) {
+  } else if (warp == 1 || warp == 3) {
     // ------------------------------------------------------------ MMA
-    // The whole warp goes through the loop with values that are the same in
-    // every lane, and one lane issues: descriptors then stay in uniform
-    // registers.  (Issued from code that one lane alone runs, each of an MMA's
-    // operands is moved there first, about 90 cycles an instruction.)
+    // Warp 1 for tile 0, warp 3 for tile 1.  The whole warp goes through the
+    // loop with values that are the same in every lane, and one lane issues:
+    // descriptors then stay in uniform registers.  (Issued from code that one
+    // lane alone runs, each of an MMA's operands is moved there first, about 90
+    // cycles an instruction.)
+    const int i = warp >> 1;
     const bool leader = elect_one();
     constexpr uint32_t idesc_o = idesc_make(1, 1, kM, D) | (1u << 16);  // V is MN-major
-    const uint32_t u_ring = uniform(ring), u_base = uniform(base), u_tmem = uniform(tmem);
-    uint32_t at = 0, items = 0, np0 = 0, np1 = 0;
+    const uint32_t u_tmem = uniform(tmem);
+    const uint32_t s_tmem = u_tmem + i * 128, o_tmem = u_tmem + 256 + i * 128;
+    const uint64_t qd = sdesc_sw128(uniform(base) + i * C::kQ);
+    const uint64_t kd0 = sdesc_sw128(uniform(ring)), vd0 = sdesc_mn(uniform(ring), C::kHalf);
+    uint32_t slot = 0, phase = 0;  // of the next block in the ring
+    uint32_t items = 0, np = 0;
     bool ok = true;
     for (int id = blockIdx.x; ok && id < p.items; id += gridDim.x) {
       WinItem it;
       if (!uniform(win_item(p, id, it))) continue;
-      it.blocks = uniform(it.blocks);
-      if (it.blocks == 0) continue;
-      it.win_blocks = uniform(it.win_blocks);
-      it.span.base = uniform(it.span.base);
-      it.span.end = uniform(it.span.end);
-      it.span.sink_end = uniform(it.span.sink_end);
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        it.from[i] = uniform(it.from[i]);
-        it.to[i] = uniform(it.to[i]);
-      }
+      const int blocks = uniform(it.blocks), wins = uniform(it.win_blocks);
+      if (blocks == 0) continue;
+      const int from = uniform(i ? it.from[1] : it.from[0]), to = uniform(i ? it.to[1] : it.to[0]);
+      // columns of the last window block and the last of the sinks
+      const int win_cols = uniform(columns(it.span.end - it.span.base - (it.win_blocks - 1) * kN));
+      const int sink_cols =
+          uniform(columns(it.span.sink_end - (it.blocks - it.win_blocks - 1) * kN));
       if (!mbar_wait_warp(smem_u32(&cs->q_full), items & 1u, ctl)) break;
       ++items;
-      uint32_t begun0 = 0u, begun1 = 0u;
-      // S_i = Q_i K^T of block n into buffer n % 2
-      auto scores = [&](int i, int n, uint32_t slot) {
-        const uint64_t kd = sdesc_sw128(u_ring + slot * C::kBlock);
-        const uint64_t qi = sdesc_sw128(u_base + i * C::kQ);
-        const uint32_t idesc_s = idesc_make(1, 1, kM, (uint32_t)columns(block_keys(it, n)));
-        const uint32_t d = u_tmem + i * 128 + (n & 1) * kN;
-        if (leader) {
+      uint32_t begun = 0u;
+      // The first two blocks' scores, then for each block its values and the
+      // scores of the one two further on, into the buffer of the same parity:
+      // the ring holds them in this order.  see, cols: of blocks n, n + 1, n + 2.
+      uint32_t see = 0u;
+      int cols0 = kN, cols1 = kN, cols2 = kN;
+      for (int n = -2; n < blocks; ++n) {
+        const int m = n + 2;
+        see >>= 1;
+        cols0 = cols1;
+        cols1 = cols2;
+        cols2 = m == wins - 1 ? win_cols : (m == blocks - 1 ? sink_cols : kN);
+        if (m < blocks && ((m >= from && m < to) || (m >= wins && to > 0))) see |= 4u;
+        if (n >= 0) {
+          if (!(ok = mbar_wait_warp(smem_u32(&cs->kv_full[slot]), phase, ctl))) break;
+          if (see & 1u) {  // O += P V
+            const int buf = n & 1;
+            if (!(ok = mbar_wait_warp(smem_u32(&cs->p_ready[i][buf]), (np >> buf) & 1u, ctl))) break;
+            np ^= 1u << buf;
+            tc_fence_after();
+            const uint64_t vd = vd0 + (uint64_t)(slot * (C::kBlock >> 4));
+            const uint32_t a = s_tmem + buf * kN;
+            if (leader) {
 #pragma unroll
-          for (int kk = 0; kk < D / 16; ++kk)
-            umma_bf16(d, qi + (((kk >> 2) * C::kQHalf + (kk & 3) * 32) >> 4),
-                      kd + (((kk >> 2) * C::kHalf + (kk & 3) * 32) >> 4), idesc_s, kk > 0 ? 1u : 0u);
-          umma_commit(smem_u32(&cs->s_full[i][n & 1]));
+              for (int kk = 0; kk < kN / 16; ++kk)
+                if (kk * 16 < cols0)
+                  umma_ts_bf16(o_tmem, a + kk * 8, vd + kk * (2048 >> 4), idesc_o,
+                               kk > 0 ? 1u : begun);
+              umma_commit(smem_u32(&cs->pv_done[i][buf]));
+            }
+            __syncwarp();
+            begun = 1u;
+          }
+          if (leader) umma_commit(smem_u32(&cs->kv_empty[slot]));
+          __syncwarp();
+          if (++slot == (uint32_t)C::kSlots) slot = 0, phase ^= 1u;
         }
-        __syncwarp();
-      };
-      // O_i += P_i V of block n
-      auto values = [&](int i, int n, uint32_t slot, uint32_t& begun) {
-        const uint64_t vd = sdesc_mn(u_ring + slot * C::kBlock, C::kHalf);
-        const uint32_t a = u_tmem + i * 128 + (n & 1) * kN, d = u_tmem + 256 + i * 128;
-        const int steps = columns(block_keys(it, n)) / 16;
-        if (leader) {
+        if (m < blocks) {
+          if (!(ok = mbar_wait_warp(smem_u32(&cs->kv_full[slot]), phase, ctl))) break;
+          if (see & 4u) {  // S = Q K^T
+            tc_fence_after();
+            const uint64_t kd = kd0 + (uint64_t)(slot * (C::kBlock >> 4));
+            const uint32_t idesc_s = idesc_make(1, 1, kM, (uint32_t)cols2);
+            const uint32_t d = s_tmem + (m & 1) * kN;
+            if (leader) {
 #pragma unroll
-          for (int kk = 0; kk < kN / 16; ++kk)
-            if (kk < steps)
-              umma_ts_bf16(d, a + kk * 8, vd + kk * (2048 >> 4), idesc_o, kk > 0 ? 1u : begun);
-          umma_commit(smem_u32(&cs->pv_done[i][n & 1]));
+              for (int kk = 0; kk < D / 16; ++kk)
+                umma_bf16(d, qd + (((kk >> 2) * C::kQHalf + (kk & 3) * 32) >> 4),
+                          kd + (((kk >> 2) * C::kHalf + (kk & 3) * 32) >> 4), idesc_s,
+                          kk > 0 ? 1u : 0u);
+              umma_commit(smem_u32(&cs->s_full[i][m & 1]));
+            }
+            __syncwarp();
+          }
+          if (leader) {
+            umma_commit(smem_u32(&cs->kv_empty[slot]));
+            if (m == blocks - 1) umma_commit(smem_u32(&cs->q_empty));
+          }
+          __syncwarp();
+          if (++slot == (uint32_t)C::kSlots) slot = 0, phase ^= 1u;
         }
-        __syncwarp();
-        begun = 1u;
-      };
-      auto landed = [&](uint32_t x, uint32_t slot) {
-        return mbar_wait_warp(smem_u32(&cs->kv_full[slot]), (x / C::kSlots) & 1u, ctl);
-      };
-      // the first two blocks' scores, then for each block its values and the
-      // scores of the one two further on
-      for (int n = -2; ok && n < it.blocks; ++n) {
-        const uint32_t xv = at + ring_v(it.blocks, n), xk = at + ring_k(n + 2);
-        const uint32_t sv = xv % C::kSlots, sk = xk % C::kSlots;
-        const bool more = n + 2 < it.blocks;
-        if ((n >= 0 && !landed(xv, sv)) || (more && !landed(xk, sk))) {
-          ok = false;
-          break;
-        }
-        if (n >= 0 && tile_sees<0>(it, n)) {
-          if (!(ok = mbar_wait_warp(smem_u32(&cs->p_ready[0][n & 1]), (np0 >> (n & 1)) & 1u, ctl)))
-            break;
-          np0 ^= 1u << (n & 1);
-          tc_fence_after();
-          values(0, n, sv, begun0);
-        }
-        if (more && tile_sees<0>(it, n + 2)) scores(0, n + 2, sk);
-        if (n >= 0 && tile_sees<1>(it, n)) {
-          if (!(ok = mbar_wait_warp(smem_u32(&cs->p_ready[1][n & 1]), (np1 >> (n & 1)) & 1u, ctl)))
-            break;
-          np1 ^= 1u << (n & 1);
-          tc_fence_after();
-          values(1, n, sv, begun1);
-        }
-        if (more && tile_sees<1>(it, n + 2)) scores(1, n + 2, sk);
-        if (leader) {
-          if (n >= 0) umma_commit(smem_u32(&cs->kv_empty[sv]));
-          if (more) umma_commit(smem_u32(&cs->kv_empty[sk]));
-          if (n + 3 == it.blocks) umma_commit(smem_u32(&cs->q_empty));
-        }
-        __syncwarp();
       }
-      at += 2 * it.blocks;
     }
   } else if (warp >= kSoftWarp) {
     // ------------------------------------------------------------ softmax
@@ -478,51 +467,62 @@ __global__ void __launch_bounds__(kWinThreads, 1)
       const int nq = it.nq(i);
       const int ta = it.first(i), tb = ta + nq - 1;
       const int t = ta + min(qi, nq - 1);
-      float m = neg_inf(), l = 0.0f;
-      bool any = false;
-      for (int n = 0; n < it.blocks; ++n) {
-        if (!(i ? tile_sees<1>(it, n) : tile_sees<0>(it, n))) continue;
+      // limit: the maximum that asks for a new m; nothing before the first block
+      float m = neg_inf(), limit = neg_inf(), l = 0.0f;
+      const int from = i ? it.from[1] : it.from[0], to = i ? it.to[1] : it.to[0];
+      const bool any = to > from;
+      for (int n = from; n < it.blocks && any; ++n) {
+        if (n == to) {  // on to the sinks
+          n = it.win_blocks;
+          if (n == it.blocks) break;
+        }
         const int buf = n & 1;
+        const uint32_t b_col = s_col + buf * kN;
+        const int j0 = block_key(it, n), keys = block_keys(it, n), chunks = columns(keys) / 32;
+        // whether every row of the tile sees every key of the block
+        const bool clean = keys == kN && j0 + kN - 1 <= ta &&
+                           (j0 > tb - p.window || j0 + kN - 1 < p.sinks);
         if (!mbar_wait_warp(smem_u32(&cs->s_full[i][buf]), (ns >> buf) & 1u, ctl)) {
           stop = true;
           break;
         }
         ns ^= 1u << buf;
         tc_fence_after();
-        const uint32_t b_col = s_col + buf * kN;
-        const int j0 = block_key(it, n), keys = block_keys(it, n), chunks = columns(keys) / 32;
         // the tile's columns, 32 at a time, stay in registers from here on
         float v[kN / 32][32];
 #pragma unroll
         for (int c = 0; c < kN / 32; ++c)
           if (c < chunks) tmem_ld32(b_col + c * 32, v[c]);
         tmem_ld_wait();
-        float mx[4] = {neg_inf(), neg_inf(), neg_inf(), neg_inf()};
 #pragma unroll
-        for (int c = 0; c < kN / 32; ++c) {
-          pin32(v[c]);
-          if (c < chunks) {
-            // columns that some row of the tile does not see: the row's own are
-            // an interval of them and the sinks
-            const int a = j0 + 32 * c, z = a + 31;
-            if (!(32 * c + 32 <= keys && z <= ta && (a > tb - p.window || z < p.sinks))) {
-              const uint32_t seen = below(min(t + 1, j0 + keys) - a) &
-                                    (~below(t + 1 - p.window - a) | below(p.sinks - a));
-              asm volatile("" ::"r"(seen));  // a branch, and not 32 selections for every chunk
+        for (int c = 0; c < kN / 32; ++c) pin32(v[c]);
+        if (!clean) {
+          // columns that a row does not see: its own are an interval and the sinks
 #pragma unroll
-              for (int e = 0; e < 32; ++e)
-                if (!((seen >> e) & 1u)) v[c][e] = neg_inf();
-            }
+          for (int c = 0; c < kN / 32; ++c) {
+            const int a = j0 + 32 * c;
+            const uint32_t seen = below(min(t + 1, j0 + keys) - a) &
+                                  (~below(t + 1 - p.window - a) | below(p.sinks - a));
+            asm volatile("" ::"r"(seen));  // a branch, and not 64 selections for every block
 #pragma unroll
-            for (int e = 0; e < 32; ++e) mx[e & 3] = fmaxf(mx[e & 3], v[c][e]);
+            for (int e = 0; e < 32; ++e)
+              if (!((seen >> e) & 1u)) v[c][e] = neg_inf();
           }
         }
-        const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * sl2;
+        float mx[4] = {neg_inf(), neg_inf(), neg_inf(), neg_inf()};
+#pragma unroll
+        for (int c = 0; c < kN / 32; ++c)
+#pragma unroll
+          for (int e = 0; e < 32; e += 2)
+            mx[(e >> 1) & 3] = max3_nan(mx[(e >> 1) & 3], v[c][e], v[c][e + 1]);
+        float top = max3_nan(max3_nan(mx[0], mx[1], mx[2]), mx[3], mx[3]) * sl2;
         // the first maximum is taken as it is; later ones once they pass it by 2^16
-        const bool grow = top > (m == neg_inf() ? m : m + kGrow);
+        const bool grow = !(top <= limit);
         if (__any_sync(0xFFFFFFFFu, grow)) {
+          // a score that is infinite or NaN makes the row NaN, as in the formula
+          if (!(top < __int_as_float(0x7F800000))) top = m = __int_as_float(0x7FC00000);
           const float a = grow ? ex2(m - top) : 1.0f;
-          if (any) {
+          if (n != from) {
             // nobody writes O once the values of the block before are in it
             if (!mbar_wait_warp(smem_u32(&cs->pv_done[i][last]), ((npv >> last) & 1u) ^ 1u, ctl)) {
               stop = true;
@@ -545,9 +545,11 @@ __global__ void __launch_bounds__(kWinThreads, 1)
             tmem_st_wait();
             tc_fence_before();
           }
-          if (grow) m = top;
+          if (grow) {
+            m = top;
+            limit = top + kGrow;
+          }
         }
-        any = true;
         const float sub = m == neg_inf() ? 0.0f : -m;
         const uint64_t sl22 = pair2(sl2, sl2), sub2 = pair2(sub, sub);
         uint64_t ls[2] = {0ull, 0ull};
@@ -557,11 +559,19 @@ __global__ void __launch_bounds__(kWinThreads, 1)
             uint32_t w[16];
 #pragma unroll
             for (int e = 0; e < 32; e += 2) {
+              uint64_t xy = fma2(pair2(v[c][e], v[c][e + 1]), sl22, sub2);
               float x, y;
-              unpair2(fma2(pair2(v[c][e], v[c][e + 1]), sl22, sub2), x, y);
-              x = ex2(x);
-              y = ex2(y);
-              ls[(e >> 1) & 1] = add2(ls[(e >> 1) & 1], pair2(x, y));
+              // part of the exponentials go through the FMA units
+              if ((e >> 1) % kPolyEvery == kPolyEvery - 1) {
+                xy = ex2_poly2(xy);
+                unpair2(xy, x, y);
+              } else {
+                unpair2(xy, x, y);
+                x = ex2(x);
+                y = ex2(y);
+                xy = pair2(x, y);
+              }
+              ls[(e >> 1) & 1] = add2(ls[(e >> 1) & 1], xy);
               w[e >> 1] = pack_bf16x2(x, y);
             }
             tmem_st16(b_col + c * 16, w);
