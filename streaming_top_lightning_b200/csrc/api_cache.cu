@@ -31,9 +31,10 @@ int check_attention(int B, int S, int H, int H_k, int d) {
   return SI_OK;
 }
 
-// The rows kernel's plan: the tile width (the narrowest of 8, 16 and 32 rows
-// that holds a kv head's rows, so that keys are read once), the keys of a CTA,
-// and the bytes of partial results.  keys: what one query may see at most.
+// The plan over a tile's keys: the tile width (the narrowest of 8, 16 and 32
+// rows that holds a kv head's rows, so that keys are read once; over a 4-bit
+// cache 128-row tensor-core tiles from 33 rows on), the keys of a CTA, and the
+// bytes of partial results.  keys: what one query may see at most.
 // With fewer tiles than three waves of CTAs the keys are split into chunks, of
 // one length for all sequences, so that they make up three waves at full
 // length (ragged sequences leave some out); a chunk keeps a CTA's four warps at
@@ -42,22 +43,36 @@ int plan_rows(RowsParams* p, int64_t keys, bool cache4, int key_chunk, int sms, 
               size_t* bytes) {
   const bool listed = p->topk > 0;
   const int64_t rows = listed ? p->G : std::min<int64_t>((int64_t)p->S * p->G, 1 << 20);
-  p->row_tile = rows <= 8 ? 8 : rows <= 16 ? 16 : 32;
+  p->row_tile = rows <= 8 ? 8 : rows <= 16 ? 16 : (rows <= 32 || !cache4) ? 32 : 128;
   const int rt = p->row_tile;
   const int64_t per = listed ? (int64_t)p->S * ((p->G + rt - 1) / rt)
                              : ((int64_t)p->S * p->G + rt - 1) / rt;
-  // a tile's queries see a little more than one of them, the sinks and the
-  // window's two ends come in whole steps
+  // a tile's queries see a little more than one of them; the sinks and the
+  // window's two ends come in whole steps (32 keys, 64 in 128-row tiles)
   const int64_t span = listed ? keys : std::min<int64_t>(p->T, keys + rt / p->G + 1);
-  const int64_t steps = (span + 31) / 32 + (listed ? 0 : 3);
+  const int64_t steps = (span + 31) / 32 + (listed ? (rt == 128 ? 1 : 0) : (rt == 128 ? 6 : 3));
   const int64_t tiles = (int64_t)p->B * p->Hk * per;
-  const int64_t room = 3 * (int64_t)sms * attn_rows_ctas(d, cache4, rt);
   int64_t chunk = steps;
   if (key_chunk > 0) {
     chunk = std::max<int64_t>(key_chunk / 32, (steps + 1023) / 1024);
-  } else if (tiles < room) {
-    chunk = std::max<int64_t>(8, std::max((tiles * steps + room - 1) / room, (steps + 127) / 128));
+  } else if (rt == 128) {
+    // one CTA per SM: the number of chunks that makes the rounds of CTAs times
+    // a chunk's cost least, a chunk costing 256 keys besides its own
+    if (tiles < sms) {
+      int64_t best = -1;
+      for (int64_t n = 1; n <= 64; ++n) {
+        const int64_t c = ((steps + n - 1) / n + 3) / 4 * 4;
+        const int64_t cost = (tiles * ((steps + c - 1) / c) + sms - 1) / sms * (c + 8);
+        if (best < 0 || cost < best) best = cost, chunk = c;
+      }
+    }
+  } else {
+    const int64_t room = 3 * (int64_t)sms * attn_rows_ctas(d, cache4, rt);
+    if (tiles < room)
+      chunk =
+          std::max<int64_t>(8, std::max((tiles * steps + room - 1) / room, (steps + 127) / 128));
   }
+  if (rt == 128) chunk = (chunk + 3) / 4 * 4;  // whole pairs of blocks
   p->splits = (int)((steps + chunk - 1) / chunk);
   p->chunk_keys = (int)chunk * 32;
   if (tiles * p->splits >= ((int64_t)1 << 31)) return SI_ERR_DIM;
@@ -380,7 +395,14 @@ int si_cache4_attention(const void* qa, const void* pages, int n_pages, const in
   p.lse = lse;
   p.scale_log2 = scale * k_scale * 1.4426950408889634f;
   p.v_scale = v_scale;
-  return status(launch_attn_rows(p, d, static_cast<cudaStream_t>(stream)));
+  if (p.row_tile < 128)
+    return status(launch_attn_rows(p, d, static_cast<cudaStream_t>(stream)));
+  if (cache4_tiles_smem(d) > (size_t)dev->max_smem) return SI_ERR_UNSUPPORTED;
+  const int64_t items = (int64_t)B * H_k * p.tiles * p.splits;
+  const int most = o.grid_ctas > 0 ? o.grid_ctas : dev->sms;
+  return status(launch_cache4_tiles(p, d, (int)std::min<int64_t>(most, items), dev->err,
+                                    (uint64_t)o.timeout_ms * 1000000ull,
+                                    static_cast<cudaStream_t>(stream)));
 }
 
 // ------------------------------------------------------------ pages

@@ -266,51 +266,6 @@ struct Bf16Rows {
   static SI_DEV int element(int i, int r, int h) { return 16 * i + r + 8 * h; }
 };
 
-// The tile's rows and what its queries see.
-struct Tile {
-  int b, hk, row0, rows;  // rows: live rows of the tile
-  int len, q_len, t_min, t_max;
-  int64_t part;           // index of its first row among all rows
-};
-
-template <int RT>
-SI_DEV bool find_tile(const RowsParams& p, int64_t id, Tile& ti) {
-  const int tile = (int)(id % p.tiles);
-  const int64_t bh = id / p.tiles;
-  ti.b = (int)(bh / p.Hk);
-  ti.hk = (int)(bh % p.Hk);
-  ti.len = seq_len(p.lens, ti.b, p.T);
-  ti.q_len = seq_len(p.q_lens, ti.b, p.S);
-  int last;  // one past the tile's last row
-  if (p.idx) {  // a tile's rows belong to one query
-    const int per = (p.G + RT - 1) / RT;
-    const int i = tile / per;
-    ti.row0 = i * p.G + (tile % per) * RT;
-    last = min((i + 1) * p.G, ti.q_len * p.G);
-  } else {
-    ti.row0 = tile * RT;
-    last = ti.q_len * p.G;
-  }
-  ti.rows = min(RT, last - ti.row0);
-  if (ti.rows <= 0) return false;
-  ti.t_min = ti.len - ti.q_len + ti.row0 / p.G;
-  ti.t_max = ti.len - ti.q_len + (ti.row0 + ti.rows - 1) / p.G;
-  ti.part = bh * p.S * p.G + ti.row0;
-  return true;
-}
-
-// The steps of KS keys that a tile takes.
-template <int KS>
-SI_DEV KeySpan tile_span(const RowsParams& p, const Tile& ti) {
-  if (p.idx) return KeySpan{0, 0, p.topk, 0, 0, (p.topk + KS - 1) / KS};
-  return key_span<KS>(ti.t_min, ti.t_max, ti.len, p.window, p.sinks);
-}
-
-SI_DEV int64_t out_row(const RowsParams& p, const Tile& ti, int row) {
-  const int i = row / p.G;
-  return ((int64_t)ti.b * p.S + i) * p.H + ti.hk * p.G + row % p.G;
-}
-
 // MODE 0: bf16 keys; 1: 4-bit pages; 2: 4-bit pages, listed entries.
 template <int D, int MODE, int NT>
 using Source = typename std::conditional<MODE == 0, Bf16Rows<D, NT>, Cache4<D, NT>>::type;
@@ -807,6 +762,15 @@ cudaError_t launch_nt(const RowsParams& p, cudaStream_t stream) {
 }
 
 }  // namespace
+
+cudaError_t launch_attn_join_tiles(const RowsParams& p, int D, cudaStream_t stream) {
+  const unsigned rows = (unsigned)((int64_t)p.B * p.Hk * p.S * p.G);
+  if (D == 128)
+    k_attn_join<128, 64, 128><<<rows, 128, 0, stream>>>(p);
+  else
+    k_attn_join<64, 64, 128><<<rows, 128, 0, stream>>>(p);
+  return cudaGetLastError();
+}
 
 int attn_rows_ctas(int D, bool cache4, int row_tile) { return row_ctas(D, cache4 ? 1 : 0, row_tile / 8); }
 

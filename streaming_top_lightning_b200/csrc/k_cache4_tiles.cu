@@ -1,0 +1,595 @@
+// Attention of many query rows over a 4-bit paged cache on the tensor cores:
+// 33 and more (query, head) rows of a kv head, as a layer has whose 128 heads
+// share one key row.  Formula, key rule, number formats and roundings are those
+// of k_attn_rows.cu's 4-bit path.
+//
+// What bounds it: per key 4 D operations for each of 128 rows against 4.5 bits
+// per element, so the tensor cores and the exponentials (a 128 x 64 block of
+// scores takes 256 + 256 cycles of MMA at D = 128 and 512 of the SM's 16
+// exponentials a cycle), with the conversion of the codes beside them (16,384
+// fp16 numbers a block into shared memory).
+//
+// One persistent CTA per SM takes (row tile, chunk of keys) items.  The blocks
+// of 64 keys of an item go alternately to two pipelines that share Q and have
+// everything else of their own, the running maximum, sum and O too:
+//   4 producer warps  a thread a key or value row: 64 bytes of codes from the
+//                     page into registers (one block ahead; the page two
+//                     ahead), to fp16 and into the 128-byte swizzled layout;
+//                     keys that are not there become zeros and a cleared mask bit
+//   an MMA warp       S = Q K^T into one of two TMEM buffers, two blocks ahead of
+//                     the softmax, then O += P V with P read from TMEM
+//   4 softmax warps   a thread a row, P = 2^(s - m) in fp16 over S's columns
+// At the end of an item each softmax group writes one half of the row's
+// elements, from both pipelines' O.  O is rescaled when a row's maximum has
+// grown by more than 2^5 since it was last fixed; with the scale of 2^10 a
+// probability then stays below fp16's largest number.
+// Registers: the softmax threads take what the producers and MMA warps leave.
+// Every wait is bounded; a CTA that gives up records the error word and leaves.
+#include "si_attn.cuh"
+
+namespace si {
+namespace {
+
+constexpr int kM = 128;
+constexpr int kN = 64;
+constexpr int kThreads = 640;  // softmax 0, 1; producers 0, 1; MMA warps 16, 17
+constexpr int kSlots = 3;      // K and V blocks of a pipeline
+constexpr int kPolyEvery = 4;  // every so many pairs of exponentials run as polynomials
+constexpr float kShift = 10.0f, kGrow = 5.0f;
+
+template <int D>
+struct TileCfg {
+  static constexpr uint32_t kQ = kM * D * 2, kQHalf = kM * 128;
+  static constexpr uint32_t kBlock = kN * D * 2, kHalf = kN * 128;  // K or V block
+  static constexpr size_t kRing = 2 * kSlots * 2 * (size_t)kBlock;
+};
+
+struct TileCtl {
+  uint64_t kv_full[2][kSlots], kv_empty[2][kSlots];
+  uint64_t s_full[2][2], p_ready[2][2], pv_done[2][2];
+  uint64_t q_full, q_empty, ml_full, o_free;
+  uint64_t mask[2][kSlots];       // keys of a block that are there
+  float factor[kM];               // 2^-x of the rows scaled by 2^x
+  float xm[2][kM], xl[2][kM];     // the pipelines' maxima and sums
+  uint32_t tmem_base;
+  uint32_t abort;
+};
+
+// An item: its tile, its blocks [lo, hi) and its chunk.
+struct TileItem {
+  Tile ti;
+  KeySpan span;
+  int lo, hi, split;
+};
+
+SI_DEV bool tile_item(const RowsParams& p, int id, TileItem& it) {
+  const int tile = id / p.splits;
+  it.split = id - tile * p.splits;
+  if (!find_tile<kM>(p, tile, it.ti)) return false;
+  it.span = tile_span<kN>(p, it.ti);
+  const int per = p.chunk_keys / kN;
+  it.lo = it.split * per;
+  it.hi = it.split + 1 == p.splits ? it.span.steps : min(it.span.steps, it.lo + per);
+  return it.lo < it.hi || p.splits == 1;  // a row without keys is still written
+}
+// Blocks of pipeline i.
+SI_DEV int pipe_blocks(const TileItem& it, int i) { return max(0, it.hi - it.lo + 1 - i) >> 1; }
+
+}  // namespace
+
+template <int D, bool LISTED>
+__global__ void __launch_bounds__(kThreads, 1) k_cache4_tiles(const __grid_constant__ RowsParams p,
+                                                              int items, uint32_t* err,
+                                                              uint64_t timeout_ns) {
+  using C = TileCfg<D>;
+  // [Q | pipeline 0: K V K V K V | pipeline 1 | ctl], with no room to align it by hand
+  extern __shared__ __align__(1024) uint8_t smem[];
+  const uint32_t base = smem_u32(smem), ring = base + C::kQ;
+  TileCtl* cs = reinterpret_cast<TileCtl*>(smem + C::kQ + C::kRing);
+  const int tid = threadIdx.x, warp = uniform(tid >> 5), lane = tid & 31;
+
+  if (base & 1023u) {  // the swizzled layout needs it
+    if (tid == 0) atomicOr(err, SI_DEVERR_BAD_STATE);
+    return;
+  }
+
+  if (tid == 0) {
+    for (int i = 0; i < 2; ++i) {
+      for (int x = 0; x < kSlots; ++x) {
+        mbar_init(smem_u32(&cs->kv_full[i][x]), 128);
+        mbar_init(smem_u32(&cs->kv_empty[i][x]), 1);
+      }
+      for (int x = 0; x < 2; ++x) {
+        mbar_init(smem_u32(&cs->s_full[i][x]), 1);
+        mbar_init(smem_u32(&cs->p_ready[i][x]), kM);
+        mbar_init(smem_u32(&cs->pv_done[i][x]), 1);
+      }
+    }
+    mbar_init(smem_u32(&cs->q_full), kM);
+    mbar_init(smem_u32(&cs->q_empty), 2);
+    mbar_init(smem_u32(&cs->ml_full), 2 * kM);
+    mbar_init(smem_u32(&cs->o_free), 2 * kM);
+    cs->abort = 0u;
+    mbar_fence_init();
+  }
+  if (warp == 16) {
+    tmem_alloc(smem_u32(&cs->tmem_base), 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = cs->tmem_base;
+  const Ctl ctl{err, &cs->abort, timeout_ns, nullptr};
+
+  if (warp >= 16) {
+    // ------------------------------------------------------------ MMA
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 32;");
+    if (warp < 18) {
+      const int i = warp - 16;
+      const bool leader = elect_one();
+      constexpr uint32_t idesc_s = idesc_make(0, 0, kM, kN);               // fp16
+      constexpr uint32_t idesc_o = idesc_make(0, 0, kM, D) | (1u << 16);   // V is MN-major
+      const uint32_t u_tmem = uniform(tmem);
+      const uint32_t s_tmem = u_tmem + i * 128, o_tmem = u_tmem + 256 + i * 128;
+      const uint64_t qd = sdesc_sw128(uniform(base));
+      const uint32_t my_ring = uniform(ring) + i * (kSlots * 2 * C::kBlock);
+      const uint64_t kd0 = sdesc_sw128(my_ring), vd0 = sdesc_mn(my_ring + C::kBlock, C::kHalf);
+      uint32_t kslot = 0, kphase = 0, vslot = 0, n_items = 0, np = 0;
+      bool ok = true;
+      for (int id = blockIdx.x; ok && id < items; id += gridDim.x) {
+        int blocks, any;
+        {
+          TileItem it;
+          if (!uniform(tile_item(p, id, it))) continue;
+          any = uniform(it.hi - it.lo);
+          blocks = uniform(pipe_blocks(it, i));
+        }
+        if (any <= 0) continue;
+        if (!mbar_wait_warp(smem_u32(&cs->q_full), n_items & 1u, ctl)) break;
+        ++n_items;
+        if (blocks == 0 && leader) mbar_arrive(smem_u32(&cs->q_empty));
+        for (int n = -2; n < blocks; ++n) {
+          const int m = n + 2;
+          if (n >= 0) {  // O += P V
+            const int buf = n & 1;
+            if (!(ok = mbar_wait_warp(smem_u32(&cs->p_ready[i][buf]), (np >> buf) & 1u, ctl))) break;
+            np ^= 1u << buf;
+            tc_fence_after();
+            if (leader) {
+              const uint64_t vd = vd0 + (uint64_t)(vslot * (2 * C::kBlock >> 4));
+              const uint32_t a = s_tmem + buf * kN;
+#pragma unroll
+              for (int kk = 0; kk < kN / 16; ++kk)
+                umma_ts(o_tmem, a + kk * 8, vd + kk * (2048 >> 4), idesc_o,
+                        (kk > 0 || n > 0) ? 1u : 0u);
+              umma_commit(smem_u32(&cs->pv_done[i][buf]));
+              umma_commit(smem_u32(&cs->kv_empty[i][vslot]));
+            }
+            __syncwarp();
+            if (++vslot == (uint32_t)kSlots) vslot = 0;
+          }
+          if (m < blocks) {  // S = Q K^T
+            if (!(ok = mbar_wait_warp(smem_u32(&cs->kv_full[i][kslot]), kphase, ctl))) break;
+            tc_fence_after();
+            if (leader) {
+              const uint64_t kd = kd0 + (uint64_t)(kslot * (2 * C::kBlock >> 4));
+              const uint32_t d = s_tmem + (m & 1) * kN;
+#pragma unroll
+              for (int kk = 0; kk < D / 16; ++kk)
+                umma_bf16(d, qd + (((kk >> 2) * C::kQHalf + (kk & 3) * 32) >> 4),
+                          kd + (((kk >> 2) * C::kHalf + (kk & 3) * 32) >> 4), idesc_s,
+                          kk > 0 ? 1u : 0u);
+              umma_commit(smem_u32(&cs->s_full[i][m & 1]));
+              if (m == blocks - 1) umma_commit(smem_u32(&cs->q_empty));
+            }
+            __syncwarp();
+            if (++kslot == (uint32_t)kSlots) kslot = 0, kphase ^= 1u;
+          }
+        }
+      }
+    }
+  } else if (warp >= 8) {
+    // ------------------------------------------------------------ producers
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
+    const int i = (warp - 8) >> 2;
+    const int pt = tid - 256 - i * 128;     // thread of the group
+    const int key = pt & (kN - 1);
+    const bool is_v = pt >= kN;
+    const int page = 1 << p.page_shift;
+    const uint32_t my_ring = ring + i * (kSlots * 2 * C::kBlock) + (is_v ? C::kBlock : 0);
+    uint32_t slot = 0, phase = 0, n_items = 0;
+    bool ok = true;
+    for (int id = blockIdx.x; ok && id < items; id += gridDim.x) {
+      TileItem it;
+      if (!tile_item(p, id, it) || it.hi <= it.lo) continue;
+      if (i == 0) {
+        // Q to fp16, a thread a row, scaled by a power of two (k_attn_rows.cu)
+        if (!mbar_wait(smem_u32(&cs->q_empty), (n_items & 1u) ^ 1u, ctl)) {
+          ok = false;
+        } else {
+          const bool live = pt < it.ti.rows;
+          const uint4* q = reinterpret_cast<const uint4*>(
+              p.q + (live ? out_row(p, it.ti, it.ti.row0 + pt) : 0) * D);
+          float top = 0.0f;
+#pragma unroll 4
+          for (int c = 0; c < D / 8; ++c) {
+            const uint4 x = __ldg(q + c);
+            const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              top = fmaxf(top, fmaxf(fabsf(bf16_lo(w[e])), fabsf(bf16_hi(w[e]))));
+          }
+          const int e = (int)(__float_as_uint(top) >> 23);
+          const int up = (e == 0 || e == 255) ? 0 : max(-126, min(126, 137 - e));
+          const float f = __uint_as_float((uint32_t)(127 + up) << 23);
+          cs->factor[pt] = __uint_as_float((uint32_t)(127 - up) << 23);
+#pragma unroll 4
+          for (int c = 0; c < D / 8; ++c) {
+            const uint4 x = live ? __ldg(q + c) : make_uint4(0, 0, 0, 0);
+            const uint32_t o0 = pack_f16x2(bf16_lo(x.x) * f, bf16_hi(x.x) * f);
+            const uint32_t o1 = pack_f16x2(bf16_lo(x.y) * f, bf16_hi(x.y) * f);
+            const uint32_t o2 = pack_f16x2(bf16_lo(x.z) * f, bf16_hi(x.z) * f);
+            const uint32_t o3 = pack_f16x2(bf16_lo(x.w) * f, bf16_hi(x.w) * f);
+            asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(
+                             base + (c >> 3) * C::kQHalf + pt * 128 + (((c & 7) ^ (pt & 7)) << 4)),
+                         "r"(o0), "r"(o1), "r"(o2), "r"(o3)
+                         : "memory");
+          }
+          fence_async();
+          mbar_arrive(smem_u32(&cs->q_full));
+        }
+      }
+      ++n_items;
+      const int blocks = pipe_blocks(it, i);
+      const int32_t* table = p.table + (int64_t)it.ti.b * p.width;
+      const int32_t* irow =
+          LISTED ? p.idx + ((int64_t)it.ti.b * p.S + it.ti.row0 / p.G) * p.topk : nullptr;
+      const uint8_t* head = p.pages + (int64_t)it.ti.hk * cache4_block<D>(page);
+      // where this thread's row of the pipeline's n-th block lies: the head's
+      // block in the page (null: the row is not there) and the slot
+      auto find = [&](int n, int& at) -> const uint8_t* {
+        at = 0;
+        if (n >= blocks) return nullptr;
+        const int u = it.lo + 2 * n + i;
+        int j;
+        if constexpr (LISTED) {
+          const int e = u * kN + key;
+          j = e < p.topk ? __ldg(irow + e) : -1;
+          if (j < 0 || j >= it.ti.len) return nullptr;
+        } else {
+          j = step_key<kN>(it.span, u) + key;
+          if (!span_holds(it.span, u, j, p.sinks)) return nullptr;
+        }
+        const int pg = __ldg(table + (j >> p.page_shift));
+        if (pg < 0 || pg >= p.n_pages) return nullptr;
+        at = j & (page - 1);
+        return head + (int64_t)pg * p.page_bytes;
+      };
+      // the row's codes and scales
+      uint4 code[D / 32];
+      uint2 sc;
+      auto load = [&](const uint8_t* blk, int at) {
+        if (blk) {
+          const uint4* c = reinterpret_cast<const uint4*>(blk + ((is_v ? page : 0) + at) * (D / 2));
+#pragma unroll
+          for (int x = 0; x < D / 32; ++x) code[x] = __ldg(c + x);
+          const uint8_t* s = blk + page * D + ((is_v ? page : 0) + at) * (D / 16);
+          if constexpr (D == 128)
+            sc = __ldg(reinterpret_cast<const uint2*>(s));
+          else
+            sc = make_uint2(__ldg(reinterpret_cast<const uint32_t*>(s)), 0u);
+        } else {
+#pragma unroll
+          for (int x = 0; x < D / 32; ++x) code[x] = make_uint4(0, 0, 0, 0);
+          sc = make_uint2(0u, 0u);
+        }
+      };
+      int at_here, at_next;
+      const uint8_t* here = find(0, at_here);
+      load(here, at_here);
+      const uint8_t* next = find(1, at_next);
+      for (int n = 0; ok && n < blocks; ++n) {
+        if (!mbar_wait(smem_u32(&cs->kv_empty[i][slot]), phase ^ 1u, ctl)) {
+          ok = false;
+          break;
+        }
+        const uint32_t dst = my_ring + slot * (2 * C::kBlock) + key * 128;
+        uint4 cur[D / 32];
+#pragma unroll
+        for (int x = 0; x < D / 32; ++x) cur[x] = code[x];
+        const uint2 cs2 = sc;
+        const bool there = here != nullptr;
+        here = next;
+        load(here, at_next);
+        next = find(n + 2, at_next);
+#pragma unroll
+        for (int b = 0; b < D / 16; ++b) {
+          const uint32_t sw = b < 4 ? cs2.x : cs2.y;
+          const uint32_t s1 = e4m3x2((sw >> (8 * (b & 3))) & 0xFFu);
+          const uint32_t s = __byte_perm(s1, 0, 0x1010);
+          const uint4 c4 = cur[b >> 1];
+          const uint32_t w0 = (b & 1) ? c4.z : c4.x, w1 = (b & 1) ? c4.w : c4.y;
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const uint32_t w = h ? w1 : w0;
+            const int ch = 2 * b + h;
+            asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(
+                             dst + (ch >> 3) * C::kHalf + (((ch & 7) ^ (key & 7)) << 4)),
+                         "r"(hmul2(e2m1x2<0>(w), s)), "r"(hmul2(e2m1x2<1>(w), s)),
+                         "r"(hmul2(e2m1x2<2>(w), s)), "r"(hmul2(e2m1x2<3>(w), s))
+                         : "memory");
+          }
+        }
+        const uint32_t m = __ballot_sync(0xFFFFFFFFu, there);
+        if (!is_v && lane == 0)
+          reinterpret_cast<uint32_t*>(&cs->mask[i][slot])[(pt >> 5) & 1] = m;
+        fence_async();
+        mbar_arrive(smem_u32(&cs->kv_full[i][slot]));
+        if (++slot == (uint32_t)kSlots) slot = 0, phase ^= 1u;
+      }
+    }
+  } else {
+    // ------------------------------------------------------------ softmax
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 144;");
+    const int i = warp >> 2;
+    const int row = (warp & 3) * 32 + lane;
+    const uint32_t lane_base = tmem + ((uint32_t)((warp & 3) * 32) << 16);
+    const uint32_t s_col = lane_base + i * 128, o_all = lane_base + 256, o_col = o_all + i * 128;
+    // parities: each pipeline's values per buffer, this one's scores per buffer
+    uint32_t mine = 0, theirs = 0, ns = 0, kslot = 0, kphase = 0, n_items = 0, n_ml = 0;
+    bool stop = false;
+    for (int id = blockIdx.x; !stop && id < items; id += gridDim.x) {
+      TileItem it;
+      if (!tile_item(p, id, it)) continue;
+      const Tile& ti = it.ti;
+      const bool live = row < ti.rows;
+      const int t = ti.len - ti.q_len + (ti.row0 + min(row, ti.rows - 1)) / p.G;
+      const int blocks = pipe_blocks(it, i), others = pipe_blocks(it, i ^ 1);
+      float m = neg_inf(), limit = neg_inf(), l = 0.0f, f = 0.0f;
+      if (it.hi > it.lo) {
+        if (!mbar_wait_warp(smem_u32(&cs->q_full), n_items & 1u, ctl)) break;
+        ++n_items;
+        // above zero: times -inf for an unseen key it is not NaN
+        f = fmaxf(cs->factor[row] * p.scale_log2, 1.17549435e-38f);
+      }
+      for (int n = 0; n < blocks; ++n) {
+        const int buf = n & 1;
+        const uint32_t b_col = s_col + buf * kN;
+        const int u = it.lo + 2 * n + i;
+        if (!mbar_wait_warp(smem_u32(&cs->kv_full[i][kslot]), kphase, ctl) ||
+            !mbar_wait_warp(smem_u32(&cs->s_full[i][buf]), (ns >> buf) & 1u, ctl)) {
+          stop = true;
+          break;
+        }
+        const uint64_t there = cs->mask[i][kslot];
+        if (++kslot == (uint32_t)kSlots) kslot = 0, kphase ^= 1u;
+        ns ^= 1u << buf;
+        tc_fence_after();
+        float v[kN / 32][32];
+#pragma unroll
+        for (int c = 0; c < kN / 32; ++c) tmem_ld32(b_col + c * 32, v[c]);
+        tmem_ld_wait();
+#pragma unroll
+        for (int c = 0; c < kN / 32; ++c) pin32(v[c]);
+        bool clean = there == ~0ull;
+        int j0 = 0;
+        if constexpr (!LISTED) {
+          j0 = step_key<kN>(it.span, u);
+          clean = clean && j0 + kN - 1 <= ti.t_min &&
+                  (j0 > ti.t_max - p.window || j0 + kN <= p.sinks);
+        }
+        if (!clean) {
+#pragma unroll
+          for (int c = 0; c < kN / 32; ++c) {
+            uint32_t seen = (uint32_t)(there >> (32 * c));
+            if constexpr (!LISTED) {
+              const int a = j0 + 32 * c;
+              seen &= below(min(t + 1, ti.len) - a) &
+                      (~below(t + 1 - p.window - a) | below(p.sinks - a));
+            }
+            asm volatile("" ::"r"(seen));  // a branch, and not 64 selections for every block
+#pragma unroll
+            for (int e = 0; e < 32; ++e)
+              if (!((seen >> e) & 1u)) v[c][e] = neg_inf();
+          }
+        }
+        float mx[4] = {neg_inf(), neg_inf(), neg_inf(), neg_inf()};
+#pragma unroll
+        for (int c = 0; c < kN / 32; ++c)
+#pragma unroll
+          for (int e = 0; e < 32; e += 2)
+            mx[(e >> 1) & 3] = max3_nan(mx[(e >> 1) & 3], v[c][e], v[c][e + 1]);
+        float top = max3_nan(max3_nan(mx[0], mx[1], mx[2]), mx[3], mx[3]) * f;
+        const bool grow = !(top <= limit);
+        if (__any_sync(0xFFFFFFFFu, grow)) {
+          // a score that is infinite or NaN makes the row NaN, as in the formula
+          if (!(top < __int_as_float(0x7F800000))) top = m = __int_as_float(0x7FC00000);
+          const float a = grow ? ex2(m - top) : 1.0f;
+          if (n > 0) {
+            // nobody writes O once the values of the block before are in it
+            const int last = buf ^ 1;
+            if (!mbar_wait_warp(smem_u32(&cs->pv_done[i][last]), ((mine >> last) & 1u) ^ 1u,
+                                ctl)) {
+              stop = true;
+              break;
+            }
+            tc_fence_after();
+            l *= a;
+#pragma unroll 1
+            for (int c = 0; c < D / 16; ++c) {
+              uint32_t w[16];
+              tmem_ld16(o_col + c * 16, w);
+              tmem_ld_wait();
+#pragma unroll
+              for (int e = 0; e < 16; ++e) {
+                asm volatile("" : "+r"(w[e]));
+                w[e] = __float_as_uint(__uint_as_float(w[e]) * a);
+              }
+              tmem_st16(o_col + c * 16, w);
+            }
+            tmem_st_wait();
+            tc_fence_before();
+          }
+          if (grow) {
+            m = top;
+            limit = top + kGrow;
+          }
+        }
+        // the other group may still read this pipeline's O of the item before
+        if (n == 0 && n_ml > 0 &&
+            !mbar_wait_warp(smem_u32(&cs->o_free), (n_ml - 1) & 1u, ctl)) {
+          stop = true;
+          break;
+        }
+        const float sub = kShift - (m == neg_inf() ? 0.0f : m);
+        const uint64_t f2 = pair2(f, f), sub2 = pair2(sub, sub);
+        uint64_t ls[2] = {0ull, 0ull};
+#pragma unroll
+        for (int c = 0; c < kN / 32; ++c) {
+          uint32_t w[16];
+#pragma unroll
+          for (int e = 0; e < 32; e += 2) {
+            uint64_t xy = fma2(pair2(v[c][e], v[c][e + 1]), f2, sub2);
+            float x, y;
+            if ((e >> 1) % kPolyEvery == kPolyEvery - 1) {
+              xy = ex2_poly2(xy);
+              unpair2(xy, x, y);
+            } else {
+              unpair2(xy, x, y);
+              x = ex2(x);
+              y = ex2(y);
+              xy = pair2(x, y);
+            }
+            ls[(e >> 1) & 1] = add2(ls[(e >> 1) & 1], xy);
+            w[e >> 1] = pack_f16x2(x, y);
+          }
+          tmem_st16(b_col + c * 16, w);
+        }
+        float l0, l1;
+        unpair2(add2(ls[0], ls[1]), l0, l1);
+        l += l0 + l1;
+        tmem_st_wait();
+        tc_fence_before();
+        mbar_arrive(smem_u32(&cs->p_ready[i][buf]));
+        mine ^= 1u << buf;
+      }
+      if (stop) break;
+      // both pipelines' results: this group writes half of the elements
+      // (the other pipeline has used its buffers in turn)
+      theirs ^= ((uint32_t)(others + 1) >> 1 & 1u) | ((uint32_t)others >> 1 & 1u) << 1;
+      // (and this one's maxima and sums)
+      if (blocks == 0 && n_ml > 0 &&
+          !mbar_wait_warp(smem_u32(&cs->o_free), (n_ml - 1) & 1u, ctl))
+        break;
+      cs->xm[i][row] = m;
+      cs->xl[i][row] = l;
+      mbar_arrive(smem_u32(&cs->ml_full));
+      if (!mbar_wait_warp(smem_u32(&cs->ml_full), n_ml & 1u, ctl)) break;
+      bool ready = true;
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        const int nb = x == i ? blocks : others, last = (nb - 1) & 1;
+        if (nb > 0)
+          ready = ready && mbar_wait_warp(smem_u32(&cs->pv_done[x][last]),
+                                          (((x == i ? mine : theirs) >> last) & 1u) ^ 1u, ctl);
+      }
+      if (!ready) break;
+      tc_fence_after();
+      const int b0 = pipe_blocks(it, 0), b1 = pipe_blocks(it, 1);
+      const float m0 = cs->xm[0][row], m1 = cs->xm[1][row];
+      const float top = fmaxf(m0, m1);
+      const float f0 = b0 && m0 != neg_inf() ? ex2(m0 - top) : 0.0f;
+      const float f1 = b1 && m1 != neg_inf() ? ex2(m1 - top) : 0.0f;
+      const float sum = cs->xl[0][row] * f0 + cs->xl[1][row] * f1;
+      const bool final_rows = p.splits == 1;
+      const float inv = sum == 0.0f ? 0.0f : (final_rows ? p.v_scale / sum : 1.0f);
+      const int64_t part = (ti.part + row) * p.splits + it.split;
+      const int64_t orow = live ? out_row(p, ti, ti.row0 + row) : -1;
+#pragma unroll 1
+      for (int c = 0; c < D / 64; ++c) {
+        const int col = i * (D / 2) + c * 32;
+        float a[32];
+#pragma unroll
+        for (int e = 0; e < 32; ++e) a[e] = 0.0f;
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          if ((x ? b1 : b0) == 0) continue;
+          float o[32];
+          tmem_ld32(o_all + x * 128 + col, o);
+          tmem_ld_wait();
+          pin32(o);
+#pragma unroll
+          for (int e = 0; e < 32; ++e) a[e] = fmaf(o[e], x ? f1 : f0, a[e]);
+        }
+        if (final_rows) {
+          uint4 piece[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            piece[e] = make_uint4(pack_bf16x2(a[8 * e] * inv, a[8 * e + 1] * inv),
+                                  pack_bf16x2(a[8 * e + 2] * inv, a[8 * e + 3] * inv),
+                                  pack_bf16x2(a[8 * e + 4] * inv, a[8 * e + 5] * inv),
+                                  pack_bf16x2(a[8 * e + 6] * inv, a[8 * e + 7] * inv));
+          transpose4(piece, lane);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const int64_t o = __shfl_sync(0xFFFFFFFFu, orow, (lane & ~3) + e);
+            if (o >= 0) reinterpret_cast<uint4*>(p.out + o * D + col)[lane & 3] = piece[e];
+          }
+        } else if (live) {
+          float4* po = reinterpret_cast<float4*>(p.part_o + part * D + col);
+#pragma unroll
+          for (int e = 0; e < 8; ++e)
+            po[e] = make_float4(a[4 * e], a[4 * e + 1], a[4 * e + 2], a[4 * e + 3]);
+        }
+      }
+      tc_fence_before();
+      mbar_arrive(smem_u32(&cs->o_free));
+      ++n_ml;
+      if (live && i == 0) {
+        const float lg = top - kShift;
+        if (!final_rows)
+          p.part_ml[part] = make_float2(sum == 0.0f ? neg_inf() : lg, sum);
+        else if (p.lse)
+          p.lse[orow] = sum == 0.0f ? neg_inf() : (lg + log2f(sum)) * 0.6931471805599453f;
+      }
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 16) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+size_t cache4_tiles_smem(int D) {
+  return (D == 128 ? TileCfg<128>::kQ + TileCfg<128>::kRing : TileCfg<64>::kQ + TileCfg<64>::kRing) +
+         sizeof(TileCtl);
+}
+
+template <int D, bool LISTED>
+static cudaError_t launch_tiles(const RowsParams& p, int items, int grid, uint32_t* err,
+                                uint64_t timeout_ns, cudaStream_t stream) {
+  const size_t smem = cache4_tiles_smem(D);
+  const cudaError_t e = cudaFuncSetAttribute(
+      k_cache4_tiles<D, LISTED>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  if (e != cudaSuccess) return e;
+  k_cache4_tiles<D, LISTED><<<grid, kThreads, smem, stream>>>(p, items, err, timeout_ns);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_cache4_tiles(const RowsParams& p, int D, int grid, uint32_t* err,
+                                uint64_t timeout_ns, cudaStream_t stream) {
+  const int items = (int)((int64_t)p.B * p.Hk * p.tiles * p.splits);
+  const cudaError_t e =
+      D == 128 ? (p.idx ? launch_tiles<128, true>(p, items, grid, err, timeout_ns, stream)
+                        : launch_tiles<128, false>(p, items, grid, err, timeout_ns, stream))
+               : (p.idx ? launch_tiles<64, true>(p, items, grid, err, timeout_ns, stream)
+                        : launch_tiles<64, false>(p, items, grid, err, timeout_ns, stream));
+  if (e != cudaSuccess || p.splits == 1) return e;
+  return launch_attn_join_tiles(p, D, stream);
+}
+
+}  // namespace si

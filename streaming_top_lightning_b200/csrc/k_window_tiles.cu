@@ -68,8 +68,6 @@ struct WinCtl {
   uint32_t abort;
 };
 
-SI_DEV void fence_async() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
-
 SI_DEV void tma_load_4d(uint32_t dst, const CUtensorMap* map, uint32_t bar, int c0, int c1, int c2,
                         int c3) {
   asm volatile(
@@ -78,90 +76,6 @@ SI_DEV void tma_load_4d(uint32_t dst, const CUtensorMap* map, uint32_t bar, int 
       "l"(map), "r"(bar), "r"(c0), "r"(c1), "r"(c2), "r"(c3)
       : "memory");
 }
-
-// D[tmem] (+)= A[tmem] * B[smem].
-SI_DEV void umma_ts_bf16(uint32_t d, uint32_t a, uint64_t bdesc, uint32_t idesc, uint32_t acc) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "setp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
-      "r"(a), "l"(bdesc), "r"(idesc), "r"(acc)
-      : "memory");
-}
-
-SI_DEV uint64_t sdesc_mn(uint32_t saddr, uint32_t lbo_bytes) {
-  return (uint64_t)((saddr >> 4) & 0x3FFFu) | ((uint64_t)((lbo_bytes >> 4) & 0x3FFFu) << 16) |
-         ((uint64_t)64u << 32) | ((uint64_t)1u << 46) | ((uint64_t)2u << 61);
-}
-
-SI_DEV void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
-  asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
-      "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
-      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
-      "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
-      : "memory");
-}
-SI_DEV void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
-
-SI_DEV void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
-      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
-        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
-        "=r"(r[14]), "=r"(r[15])
-      : "r"(taddr)
-      : "memory");
-}
-
-// Keeps values read from TMEM behind the wait for them.
-SI_DEV void pin32(float (&v)[32]) {
-#pragma unroll
-  for (int i = 0; i < 32; i += 8)
-    asm volatile("" : "+f"(v[i]), "+f"(v[i + 1]), "+f"(v[i + 2]), "+f"(v[i + 3]), "+f"(v[i + 4]),
-                 "+f"(v[i + 5]), "+f"(v[i + 6]), "+f"(v[i + 7]));
-}
-
-// The first lane's value, which the compiler then knows to be the warp's.
-template <class T>
-SI_DEV T uniform(T x) {
-  return (T)__shfl_sync(0xFFFFFFFFu, (int)x, 0);
-}
-SI_DEV bool elect_one() {
-  uint32_t r;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\telect.sync _|p, 0xFFFFFFFF;\n\tselp.u32 %0, 1, 0, p;\n\t}"
-      : "=r"(r));
-  return r != 0u;
-}
-
-// Transposes the 4 x 4 pieces of four neighbouring lanes: lane q's piece e
-// becomes lane e's piece q.
-SI_DEV uint4 shfl_xor4(uint4 x, int m) {
-  return make_uint4(__shfl_xor_sync(0xFFFFFFFFu, x.x, m), __shfl_xor_sync(0xFFFFFFFFu, x.y, m),
-                    __shfl_xor_sync(0xFFFFFFFFu, x.z, m), __shfl_xor_sync(0xFFFFFFFFu, x.w, m));
-}
-SI_DEV void transpose4(uint4 (&x)[4], int lane) {
-#pragma unroll
-  for (int m = 1; m < 4; m <<= 1) {
-    const bool up = (lane & m) != 0;
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      if (e & m) continue;
-      // lanes without the bit give their piece e | m for the others' piece e
-      const uint4 give = up ? x[e] : x[e | m];
-      const uint4 got = shfl_xor4(give, m);
-      if (up)
-        x[e] = got;
-      else
-        x[e | m] = got;
-    }
-  }
-}
-
-// The n lowest bits.
-SI_DEV uint32_t below(int n) { return n >= 32 ? 0xFFFFFFFFu : (n <= 0 ? 0u : (1u << n) - 1u); }
 
 // A pair of tiles: its queries, their positions and the key blocks.
 struct WinItem {
@@ -410,7 +324,7 @@ __global__ void __launch_bounds__(kWinThreads, 1)
 #pragma unroll
               for (int kk = 0; kk < kN / 16; ++kk)
                 if (kk * 16 < cols0)
-                  umma_ts_bf16(o_tmem, a + kk * 8, vd + kk * (2048 >> 4), idesc_o,
+                  umma_ts(o_tmem, a + kk * 8, vd + kk * (2048 >> 4), idesc_o,
                                kk > 0 ? 1u : begun);
               umma_commit(smem_u32(&cs->pv_done[i][buf]));
             }

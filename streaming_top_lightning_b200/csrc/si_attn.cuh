@@ -203,6 +203,140 @@ SI_DEV int64_t cache4_block(int page) {
   return (int64_t)page * (D + D / 8);
 }
 
+// The tile's rows and what its queries see.
+struct Tile {
+  int b, hk, row0, rows;  // rows: live rows of the tile
+  int len, q_len, t_min, t_max;
+  int64_t part;           // index of its first row among all rows
+};
+
+template <int RT>
+SI_DEV bool find_tile(const RowsParams& p, int64_t id, Tile& ti) {
+  const int tile = (int)(id % p.tiles);
+  const int64_t bh = id / p.tiles;
+  ti.b = (int)(bh / p.Hk);
+  ti.hk = (int)(bh % p.Hk);
+  ti.len = seq_len(p.lens, ti.b, p.T);
+  ti.q_len = seq_len(p.q_lens, ti.b, p.S);
+  int last;  // one past the tile's last row
+  if (p.idx) {  // a tile's rows belong to one query
+    const int per = (p.G + RT - 1) / RT;
+    const int i = tile / per;
+    ti.row0 = i * p.G + (tile % per) * RT;
+    last = min((i + 1) * p.G, ti.q_len * p.G);
+  } else {
+    ti.row0 = tile * RT;
+    last = ti.q_len * p.G;
+  }
+  ti.rows = min(RT, last - ti.row0);
+  if (ti.rows <= 0) return false;
+  ti.t_min = ti.len - ti.q_len + ti.row0 / p.G;
+  ti.t_max = ti.len - ti.q_len + (ti.row0 + ti.rows - 1) / p.G;
+  ti.part = bh * p.S * p.G + ti.row0;
+  return true;
+}
+
+// The steps of KS keys that a tile takes.
+template <int KS>
+SI_DEV KeySpan tile_span(const RowsParams& p, const Tile& ti) {
+  if (p.idx) return KeySpan{0, 0, p.topk, 0, 0, (p.topk + KS - 1) / KS};
+  return key_span<KS>(ti.t_min, ti.t_max, ti.len, p.window, p.sinks);
+}
+
+SI_DEV int64_t out_row(const RowsParams& p, const Tile& ti, int row) {
+  const int i = row / p.G;
+  return ((int64_t)ti.b * p.S + i) * p.H + ti.hk * p.G + row % p.G;
+}
+
+// ------------------------------------------------------------ tensor-core tiles
+// D[tmem] (+)= A[tmem] * B[smem], 16-bit operands (idesc says which).
+SI_DEV void umma_ts(uint32_t d, uint32_t a, uint64_t bdesc, uint32_t idesc, uint32_t acc) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+      "r"(a), "l"(bdesc), "r"(idesc), "r"(acc)
+      : "memory");
+}
+
+// Descriptor of an MN-major operand in the 128-byte swizzle: 64-element blocks
+// along N lie lbo_bytes apart, 8-row groups along K 1024.
+SI_DEV uint64_t sdesc_mn(uint32_t saddr, uint32_t lbo_bytes) {
+  return (uint64_t)((saddr >> 4) & 0x3FFFu) | ((uint64_t)((lbo_bytes >> 4) & 0x3FFFu) << 16) |
+         ((uint64_t)64u << 32) | ((uint64_t)1u << 46) | ((uint64_t)2u << 61);
+}
+
+SI_DEV void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
+      "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
+      "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
+}
+SI_DEV void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+SI_DEV void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+        "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr)
+      : "memory");
+}
+
+// Keeps values read from TMEM behind the wait for them.
+SI_DEV void pin32(float (&v)[32]) {
+#pragma unroll
+  for (int i = 0; i < 32; i += 8)
+    asm volatile("" : "+f"(v[i]), "+f"(v[i + 1]), "+f"(v[i + 2]), "+f"(v[i + 3]), "+f"(v[i + 4]),
+                 "+f"(v[i + 5]), "+f"(v[i + 6]), "+f"(v[i + 7]));
+}
+
+// The first lane's value, which the compiler then knows to be the warp's.
+template <class T>
+SI_DEV T uniform(T x) {
+  return (T)__shfl_sync(0xFFFFFFFFu, (int)x, 0);
+}
+SI_DEV bool elect_one() {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\telect.sync _|p, 0xFFFFFFFF;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(r));
+  return r != 0u;
+}
+
+// Transposes the 4 x 4 pieces of four neighbouring lanes: lane q's piece e
+// becomes lane e's piece q.
+SI_DEV uint4 shfl_xor4(uint4 x, int m) {
+  return make_uint4(__shfl_xor_sync(0xFFFFFFFFu, x.x, m), __shfl_xor_sync(0xFFFFFFFFu, x.y, m),
+                    __shfl_xor_sync(0xFFFFFFFFu, x.z, m), __shfl_xor_sync(0xFFFFFFFFu, x.w, m));
+}
+SI_DEV void transpose4(uint4 (&x)[4], int lane) {
+#pragma unroll
+  for (int m = 1; m < 4; m <<= 1) {
+    const bool up = (lane & m) != 0;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      if (e & m) continue;
+      // lanes without the bit give their piece e | m for the others' piece e
+      const uint4 give = up ? x[e] : x[e | m];
+      const uint4 got = shfl_xor4(give, m);
+      if (up)
+        x[e] = got;
+      else
+        x[e | m] = got;
+    }
+  }
+}
+
+// The n lowest bits.
+SI_DEV uint32_t below(int n) { return n >= 32 ? 0xFFFFFFFFu : (n <= 0 ? 0u : (1u << n) - 1u); }
+
+SI_DEV void fence_async() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+
 // One query row by the formula, by a whole warp: the keys [j_lo, j_hi) of a
 // bf16 source that the row sees, D/32 dims per lane.  Kernels that multiply
 // whole tiles give a row NaN when a key that it does not see holds an infinity

@@ -125,7 +125,7 @@ struct RowsParams {
   int window, sinks;   // window <= 2^30
   float scale_log2;    // softmax scale (and K scale) times log2(e)
   float v_scale;
-  int row_tile, tiles; // rows of a tile (8, 16 or 32); tiles per kv head
+  int row_tile, tiles; // rows of a tile (8, 16, 32 or 128); tiles per kv head
   int splits;          // CTAs that share a tile's keys, chunk_keys each
   int chunk_keys;
   float* part_o;       // splits > 1: [B*Hk*S*G, splits, D] partial sums
@@ -134,6 +134,12 @@ struct RowsParams {
 // CTAs of a tile width that an SM holds.
 int attn_rows_ctas(int D, bool cache4, int row_tile);
 cudaError_t launch_attn_rows(const RowsParams& p, int D, cudaStream_t stream);
+// The same over a 4-bit cache in tiles of 128 rows (k_cache4_tiles.cu), and the
+// join of its chunks (blocks of 64 keys).
+size_t cache4_tiles_smem(int D);
+cudaError_t launch_cache4_tiles(const RowsParams& p, int D, int grid, uint32_t* err,
+                                uint64_t timeout_ns, cudaStream_t stream);
+cudaError_t launch_attn_join_tiles(const RowsParams& p, int D, cudaStream_t stream);
 
 // Window attention of many rows on the tensor cores (k_window_tiles.cu).
 struct WinParams {
