@@ -13,8 +13,9 @@
 // of its own in shared memory (cp.async, no barrier between warps), the running
 // maximum and sum stay in registers, and the warps of a CTA (and several CTAs,
 // each with a chunk of the keys, unless there are tiles enough) share a
-// sequence's keys; their results are joined at the end, by k_attn_join when
-// there are several CTAs.  Chunks have one length for all sequences, so ragged
+// sequence's keys; their results are joined at the end: up to eight CTAs are a
+// cluster and read one another's shared memory, more leave partial results for
+// k_attn_join.  Chunks have one length for all sequences, so ragged
 // ones keep the CTAs equally busy.
 //
 // Keys are the M side of the products, rows the N side (mma.sync m16n8k16):
@@ -38,9 +39,13 @@
 // unrounded.
 //
 // bf16 keys: bf16 products, probabilities rounded to bf16 (2^-8).
+#include <cooperative_groups.h>
+
 #include <type_traits>
 
 #include "si_attn.cuh"
+
+namespace cg = cooperative_groups;
 
 namespace si {
 namespace {
@@ -287,15 +292,17 @@ __global__ void __launch_bounds__(kRowWarps * 32, row_ctas(D, MODE, NT))
   __shared__ uint32_t sh_nan;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int r = lane >> 2, c = lane & 3;
-  const int split = (int)(blockIdx.x % p.splits);
+  const uint32_t tile = blockIdx.x / (uint32_t)p.splits;
+  const int split = (int)(blockIdx.x - tile * (uint32_t)p.splits);
   Tile ti;
-  if (!find_tile<RT>(p, blockIdx.x / p.splits, ti)) return;
+  if (!find_tile<RT>(p, tile, ti)) return;
   const KeySpan span = tile_span<KS>(p, ti);
   const int u_lo = split * p.chunk_keys / KS;
   const int u_hi =
       split + 1 == p.splits ? span.steps : min(span.steps, (split + 1) * p.chunk_keys / KS);
-  // a sequence without keys still has rows to write
-  if (u_lo >= u_hi && (split > 0 || p.splits > 1)) return;
+  // a sequence without keys still has rows to write, and the CTAs of a cluster
+  // stay together
+  if (u_lo >= u_hi && p.splits > 1 && !p.cluster) return;
   if (threadIdx.x == 0) sh_nan = 0u;
 
   Src src;
@@ -324,15 +331,18 @@ __global__ void __launch_bounds__(kRowWarps * 32, row_ctas(D, MODE, NT))
 #pragma unroll
   for (int i = 0; i < NST; ++i) vmask[i] = 0u;
 
-  // What the next step to be loaded needs from memory first (its pages, or its
-  // entries), read one step ahead.
-  int ahead[NG];        // MODE 1: page of each group of 16 keys; -1: none
-  int64_t a_off = 0;    // MODE 2: this lane's entry
-  int a_slot = 0;
-  bool a_ok = false;
+  // What the next step to be loaded needs from memory first, read ahead and not
+  // looked at before the step is loaded: its pages (MODE 1), or its entries'
+  // pages (MODE 2, whose entries are read another step ahead).
+  int ahead[NG];             // MODE 1: page of each group of 16 keys
+  int e_now = -1, e_next = -1, pg_now = -1;  // MODE 2: this lane's entry and page
   const int32_t* table = MODE ? p.table + (int64_t)ti.b * p.width : nullptr;
   const int32_t* irow =
       MODE == 2 ? p.idx + ((int64_t)ti.b * p.S + ti.row0 / p.G) * p.topk : nullptr;
+  auto entry = [&](int u) {
+    const int e = u * KS + lane;
+    return u < u_hi && e < p.topk ? __ldg(irow + e) : -1;
+  };
   auto look_ahead = [&](int u) {
     if constexpr (MODE == 1) {
       const int j0 = step_key<KS>(span, u);
@@ -341,17 +351,12 @@ __global__ void __launch_bounds__(kRowWarps * 32, row_ctas(D, MODE, NT))
         const int j = j0 + 16 * g;
         const bool in = u < u_hi && j < (u < span.sink_steps ? span.sink_end : span.end) &&
                         (j + 16 > span.lo || j < p.sinks);
-        const int pg = in ? __ldg(table + (j >> p.page_shift)) : -1;
-        ahead[g] = pg >= 0 && pg < p.n_pages ? pg : -1;
+        ahead[g] = in ? __ldg(table + (j >> p.page_shift)) : -1;
       }
     } else if constexpr (MODE == 2) {
-      const int e = u * KS + lane;
-      const int j = u < u_hi && e < p.topk ? __ldg(irow + e) : -1;
-      a_ok = j >= 0 && j < ti.len;
-      const int pg = a_ok ? __ldg(table + (j >> p.page_shift)) : -1;
-      a_ok = pg >= 0 && pg < p.n_pages;
-      a_off = (int64_t)(a_ok ? pg : 0) * p.page_bytes;
-      a_slot = a_ok ? j & ((1 << p.page_shift) - 1) : 0;
+      e_now = e_next;
+      e_next = entry(u + kRowWarps);
+      pg_now = e_now >= 0 && e_now < ti.len ? __ldg(table + (e_now >> p.page_shift)) : -1;
     }
   };
   const int page = MODE ? 1 << p.page_shift : 0;
@@ -387,7 +392,7 @@ __global__ void __launch_bounds__(kRowWarps * 32, row_ctas(D, MODE, NT))
 #pragma unroll
           for (int g = 0; g < NG; ++g) {
             const int pg = ahead[g];
-            const bool ok = pg >= 0;
+            const bool ok = pg >= 0 && pg < p.n_pages;
             if (ok) m |= 0xFFFFu << (16 * g);
             const int slot = (j0 + 16 * g) & (page - 1);
             const uint8_t* blk = head_block + (int64_t)(ok ? pg : 0) * p.page_bytes;
@@ -410,6 +415,9 @@ __global__ void __launch_bounds__(kRowWarps * 32, row_ctas(D, MODE, NT))
           }
           vm = m;
         } else {
+          const bool a_ok = pg_now >= 0 && pg_now < p.n_pages;
+          const int64_t a_off = (int64_t)(a_ok ? pg_now : 0) * p.page_bytes;
+          const int a_slot = a_ok ? e_now & (page - 1) : 0;
           vm = __ballot_sync(0xFFFFFFFFu, a_ok);
 #pragma unroll
           for (int x = 0; x < kChunks; ++x) {
@@ -533,6 +541,7 @@ __global__ void __launch_bounds__(kRowWarps * 32, row_ctas(D, MODE, NT))
   };
 
   const int u0 = u_lo + warp;
+  if (MODE == 2) e_next = entry(u0);
   if (MODE) look_ahead(u0);
 #pragma unroll
   for (int i = 0; i < NST - 1; ++i) {
@@ -654,8 +663,47 @@ __global__ void __launch_bounds__(kRowWarps * 32, row_ctas(D, MODE, NT))
       }
     }
   }
-  if (row >= ti.rows) return;
   if (MODE) top -= kProbShift;  // the weights' common factor
+  if (p.cluster) {
+    // the chunks' CTAs are one cluster: each joins the rows that its rank gives
+    cg::cluster_group cl = cg::this_cluster();
+    __syncthreads();  // everyone is done with sh_o
+    float* mine = sh_o + row * D + part * kPer;
+#pragma unroll
+    for (int i = 0; i < kPer; i += 4)
+      *reinterpret_cast<float4*>(mine + i) = make_float4(o[i], o[i + 1], o[i + 2], o[i + 3]);
+    if (part == 0) {
+      sh_m[0][row] = sum == 0.0f ? neg_inf() : top;
+      sh_l[0][row] = sum;
+    }
+    cl.sync();
+    for (int x = split + warp * p.splits; x < ti.rows; x += kRowWarps * p.splits) {
+      float all = neg_inf(), tot = 0.0f, acc[D / 32];
+      for (int s = 0; s < p.splits; ++s) all = fmaxf(all, *cl.map_shared_rank(&sh_m[0][x], s));
+#pragma unroll
+      for (int e = 0; e < D / 32; ++e) acc[e] = 0.0f;
+#pragma unroll 2
+      for (int s = 0; s < p.splits; ++s) {
+        const float l = *cl.map_shared_rank(&sh_l[0][x], s);
+        const float f = l == 0.0f ? 0.0f : ex2(*cl.map_shared_rank(&sh_m[0][x], s) - all);
+        tot = fmaf(l, f, tot);
+        const float* po = cl.map_shared_rank(sh_o + x * D + lane * (D / 32), s);
+#pragma unroll
+        for (int e = 0; e < D / 32; ++e) acc[e] = fmaf(po[e], f, acc[e]);
+      }
+      const float inv = tot == 0.0f ? 0.0f : p.v_scale / tot;
+      const int64_t orow = out_row(p, ti, ti.row0 + x);
+      uint32_t* dst = reinterpret_cast<uint32_t*>(p.out + orow * D) + lane * (D / 64);
+#pragma unroll
+      for (int e = 0; e < D / 64; ++e)
+        dst[e] = pack_bf16x2(acc[2 * e] * inv, acc[2 * e + 1] * inv);
+      if (lane == 0 && p.lse)
+        p.lse[orow] = tot == 0.0f ? neg_inf() : (all + log2f(tot)) * 0.6931471805599453f;
+    }
+    cl.sync();  // nobody leaves while its results are read
+    return;
+  }
+  if (row >= ti.rows) return;
   if (p.splits > 1) {
     const int64_t at = (ti.part + row) * p.splits + split;
     float* po = p.part_o + at * D + part * kPer;
@@ -677,15 +725,18 @@ __global__ void __launch_bounds__(kRowWarps * 32, row_ctas(D, MODE, NT))
     p.lse[orow] = sum == 0.0f ? neg_inf() : (top + log2f(sum)) * 0.6931471805599453f;
 }
 
-// Joins the chunks of a row: a CTA of four warps per row, D/32 elements a lane.
-template <int D, int KS, int RT>
+// Joins the chunks of a row: W warps per row (1 for few chunks, 4 for many),
+// D/32 elements a lane.
+template <int D, int KS, int RT, int W>
 __global__ void __launch_bounds__(128) k_attn_join(const __grid_constant__ RowsParams p) {
   constexpr int E = D / 32;
   __shared__ float sh_o[4][D], sh_l[4], sh_top[4];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int64_t at = blockIdx.x;
-  const int rows = p.S * p.G;
-  const int row = (int)(at % rows);
+  const uint32_t rows = (uint32_t)(p.S * p.G), at32 = W == 1 ? blockIdx.x * 4 + warp : blockIdx.x;
+  if (at32 >= (uint32_t)(p.B * p.Hk) * rows) return;  // B*S*H < 2^31
+  const int64_t at = at32;
+  const uint32_t bh = at32 / rows;
+  const int row = (int)(at32 - bh * rows);
   // the row's tile, for the chunks that its keys filled
   Tile ti;
   int tile;
@@ -695,47 +746,71 @@ __global__ void __launch_bounds__(128) k_attn_join(const __grid_constant__ RowsP
   } else {
     tile = row / RT;
   }
-  if (!find_tile<RT>(p, at / rows * p.tiles + tile, ti) || row >= ti.row0 + ti.rows) return;
+  if (!find_tile<RT>(p, bh * (uint32_t)p.tiles + tile, ti) || row >= ti.row0 + ti.rows) return;
   const int n = min(p.splits, (tile_span<KS>(p, ti).steps * KS + p.chunk_keys - 1) / p.chunk_keys);
   const float2* ml = p.part_ml + at * p.splits;
+  const int s0 = W == 1 ? 0 : warp;
   float top = neg_inf();
-  for (int s = threadIdx.x; s < n; s += 128) top = fmaxf(top, ml[s].x);
+  for (int s = s0 + W * lane; s < n; s += W * 32) top = fmaxf(top, ml[s].x);
 #pragma unroll
   for (int x = 16; x > 0; x >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, x));
-  if (lane == 0) sh_top[warp] = top;
-  __syncthreads();
-  top = fmaxf(fmaxf(sh_top[0], sh_top[1]), fmaxf(sh_top[2], sh_top[3]));
+  if constexpr (W > 1) {
+    if (lane == 0) sh_top[warp] = top;
+    __syncthreads();
+    top = fmaxf(fmaxf(sh_top[0], sh_top[1]), fmaxf(sh_top[2], sh_top[3]));
+  }
   float o[E], sum = 0.0f;
 #pragma unroll
   for (int e = 0; e < E; ++e) o[e] = 0.0f;
 #pragma unroll 4
-  for (int s = warp; s < n; s += 4) {
+  for (int s = s0; s < n; s += W) {
     const float2 v = ml[s];
     const float f = v.y == 0.0f ? 0.0f : ex2(v.x - top);
     sum = fmaf(v.y, f, sum);
     const float* po = p.part_o + (at * p.splits + s) * D + lane * E;
-#pragma unroll
-    for (int e = 0; e < E; ++e) o[e] = fmaf(po[e], f, o[e]);
+    if constexpr (E == 4) {
+      const float4 x = *reinterpret_cast<const float4*>(po);
+      o[0] = fmaf(x.x, f, o[0]), o[1] = fmaf(x.y, f, o[1]);
+      o[2] = fmaf(x.z, f, o[2]), o[3] = fmaf(x.w, f, o[3]);
+    } else {
+      const float2 x = *reinterpret_cast<const float2*>(po);
+      o[0] = fmaf(x.x, f, o[0]), o[1] = fmaf(x.y, f, o[1]);
+    }
   }
+  if constexpr (W > 1) {
 #pragma unroll
-  for (int e = 0; e < E; ++e) sh_o[warp][lane * E + e] = o[e];
-  if (lane == 0) sh_l[warp] = sum;
-  __syncthreads();
-  sum = (sh_l[0] + sh_l[1]) + (sh_l[2] + sh_l[3]);
+    for (int e = 0; e < E; ++e) sh_o[warp][lane * E + e] = o[e];
+    if (lane == 0) sh_l[warp] = sum;
+    __syncthreads();
+    if (warp) return;
+    sum = (sh_l[0] + sh_l[1]) + (sh_l[2] + sh_l[3]);
+#pragma unroll
+    for (int e = 0; e < E; ++e) {
+      const int d = lane * E + e;
+      o[e] = (sh_o[0][d] + sh_o[1][d]) + (sh_o[2][d] + sh_o[3][d]);
+    }
+  }
   const float inv = sum == 0.0f ? 0.0f : p.v_scale / sum;
   const int64_t orow = out_row(p, ti, row);
-  for (int d = threadIdx.x; d < D / 2; d += 128) {
-    float v[2];
+  uint32_t* dst = reinterpret_cast<uint32_t*>(p.out + orow * D) + lane * (E / 2);
 #pragma unroll
-    for (int e = 0; e < 2; ++e)
-      v[e] = ((sh_o[0][2 * d + e] + sh_o[1][2 * d + e]) + (sh_o[2][2 * d + e] + sh_o[3][2 * d + e])) * inv;
-    reinterpret_cast<uint32_t*>(p.out + orow * D)[d] = pack_bf16x2(v[0], v[1]);
-  }
-  if (threadIdx.x == 0 && p.lse)
+  for (int e = 0; e < E / 2; ++e) dst[e] = pack_bf16x2(o[2 * e] * inv, o[2 * e + 1] * inv);
+  if (lane == 0 && p.lse)
     p.lse[orow] = sum == 0.0f ? neg_inf() : (top + log2f(sum)) * 0.6931471805599453f;
 }
 
 namespace {
+
+// Up to 16 chunks a warp takes a row, beyond that four.
+template <int D, int KS, int RT>
+cudaError_t launch_join(const RowsParams& p, cudaStream_t stream) {
+  const int64_t rows = (int64_t)p.B * p.Hk * p.S * p.G;
+  if (p.splits <= 16)
+    k_attn_join<D, KS, RT, 1><<<(unsigned)((rows + 3) / 4), 128, 0, stream>>>(p);
+  else
+    k_attn_join<D, KS, RT, 4><<<(unsigned)rows, 128, 0, stream>>>(p);
+  return cudaGetLastError();
+}
 
 template <int D, int MODE, int NT>
 cudaError_t launch(const RowsParams& p, cudaStream_t stream) {
@@ -747,11 +822,20 @@ cudaError_t launch(const RowsParams& p, cudaStream_t stream) {
                                        cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;
   const int64_t ctas = (int64_t)p.B * p.Hk * p.tiles * p.splits;
-  k_attn_rows<D, MODE, NT><<<(unsigned)ctas, kRowWarps * 32, smem, stream>>>(p);
-  if ((e = cudaGetLastError()) != cudaSuccess || p.splits == 1) return e;
-  k_attn_join<D, Src::KS, 8 * NT>
-      <<<(unsigned)((int64_t)p.B * p.Hk * p.S * p.G), 128, 0, stream>>>(p);
-  return cudaGetLastError();
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3((unsigned)ctas);
+  cfg.blockDim = dim3(kRowWarps * 32);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr{};
+  attr.id = cudaLaunchAttributeClusterDimension;
+  attr.val.clusterDim.x = (unsigned)p.splits;
+  attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = p.cluster ? 1 : 0;
+  e = cudaLaunchKernelEx(&cfg, k_attn_rows<D, MODE, NT>, p);
+  if (e != cudaSuccess || p.splits == 1 || p.cluster) return e;
+  return launch_join<D, Src::KS, 8 * NT>(p, stream);
 }
 
 template <int D, int MODE>
@@ -764,12 +848,7 @@ cudaError_t launch_nt(const RowsParams& p, cudaStream_t stream) {
 }  // namespace
 
 cudaError_t launch_attn_join_tiles(const RowsParams& p, int D, cudaStream_t stream) {
-  const unsigned rows = (unsigned)((int64_t)p.B * p.Hk * p.S * p.G);
-  if (D == 128)
-    k_attn_join<128, 64, 128><<<rows, 128, 0, stream>>>(p);
-  else
-    k_attn_join<64, 64, 128><<<rows, 128, 0, stream>>>(p);
-  return cudaGetLastError();
+  return D == 128 ? launch_join<128, 64, 128>(p, stream) : launch_join<64, 64, 128>(p, stream);
 }
 
 int attn_rows_ctas(int D, bool cache4, int row_tile) { return row_ctas(D, cache4 ? 1 : 0, row_tile / 8); }

@@ -18,7 +18,8 @@
 //                     keys that are not there become zeros and a cleared mask bit
 //   an MMA warp       S = Q K^T into one of two TMEM buffers, two blocks ahead of
 //                     the softmax, then O += P V with P read from TMEM
-//   4 softmax warps   a thread a row, P = 2^(s - m) in fp16 over S's columns
+//   4 softmax warps   a thread a row, P = 2^(s - m) in fp16 over S's columns;
+//                     those of pipeline 0 also bring Q in at the start of an item
 // At the end of an item each softmax group writes one half of the row's
 // elements, from both pipelines' O.  O is rescaled when a row's maximum has
 // grown by more than 2^5 since it was last fixed; with the scale of 2^10 a
@@ -34,7 +35,6 @@ constexpr int kM = 128;
 constexpr int kN = 64;
 constexpr int kThreads = 640;  // softmax 0, 1; producers 0, 1; MMA warps 16, 17
 constexpr int kSlots = 3;      // K and V blocks of a pipeline
-constexpr int kPolyEvery = 4;  // every so many pairs of exponentials run as polynomials
 constexpr float kShift = 10.0f, kGrow = 5.0f;
 
 template <int D>
@@ -198,73 +198,35 @@ __global__ void __launch_bounds__(kThreads, 1) k_cache4_tiles(const __grid_const
     const bool is_v = pt >= kN;
     const int page = 1 << p.page_shift;
     const uint32_t my_ring = ring + i * (kSlots * 2 * C::kBlock) + (is_v ? C::kBlock : 0);
-    uint32_t slot = 0, phase = 0, n_items = 0;
+    uint32_t slot = 0, phase = 0;
     bool ok = true;
     for (int id = blockIdx.x; ok && id < items; id += gridDim.x) {
       TileItem it;
       if (!tile_item(p, id, it) || it.hi <= it.lo) continue;
-      if (i == 0) {
-        // Q to fp16, a thread a row, scaled by a power of two (k_attn_rows.cu)
-        if (!mbar_wait(smem_u32(&cs->q_empty), (n_items & 1u) ^ 1u, ctl)) {
-          ok = false;
-        } else {
-          const bool live = pt < it.ti.rows;
-          const uint4* q = reinterpret_cast<const uint4*>(
-              p.q + (live ? out_row(p, it.ti, it.ti.row0 + pt) : 0) * D);
-          float top = 0.0f;
-#pragma unroll 4
-          for (int c = 0; c < D / 8; ++c) {
-            const uint4 x = __ldg(q + c);
-            const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-              top = fmaxf(top, fmaxf(fabsf(bf16_lo(w[e])), fabsf(bf16_hi(w[e]))));
-          }
-          const int e = (int)(__float_as_uint(top) >> 23);
-          const int up = (e == 0 || e == 255) ? 0 : max(-126, min(126, 137 - e));
-          const float f = __uint_as_float((uint32_t)(127 + up) << 23);
-          cs->factor[pt] = __uint_as_float((uint32_t)(127 - up) << 23);
-#pragma unroll 4
-          for (int c = 0; c < D / 8; ++c) {
-            const uint4 x = live ? __ldg(q + c) : make_uint4(0, 0, 0, 0);
-            const uint32_t o0 = pack_f16x2(bf16_lo(x.x) * f, bf16_hi(x.x) * f);
-            const uint32_t o1 = pack_f16x2(bf16_lo(x.y) * f, bf16_hi(x.y) * f);
-            const uint32_t o2 = pack_f16x2(bf16_lo(x.z) * f, bf16_hi(x.z) * f);
-            const uint32_t o3 = pack_f16x2(bf16_lo(x.w) * f, bf16_hi(x.w) * f);
-            asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(
-                             base + (c >> 3) * C::kQHalf + pt * 128 + (((c & 7) ^ (pt & 7)) << 4)),
-                         "r"(o0), "r"(o1), "r"(o2), "r"(o3)
-                         : "memory");
-          }
-          fence_async();
-          mbar_arrive(smem_u32(&cs->q_full));
-        }
-      }
-      ++n_items;
       const int blocks = pipe_blocks(it, i);
       const int32_t* table = p.table + (int64_t)it.ti.b * p.width;
       const int32_t* irow =
           LISTED ? p.idx + ((int64_t)it.ti.b * p.S + it.ti.row0 / p.G) * p.topk : nullptr;
       const uint8_t* head = p.pages + (int64_t)it.ti.hk * cache4_block<D>(page);
-      // where this thread's row of the pipeline's n-th block lies: the head's
-      // block in the page (null: the row is not there) and the slot
-      auto find = [&](int n, int& at) -> const uint8_t* {
-        at = 0;
-        if (n >= blocks) return nullptr;
+      // The key of this thread's row of the pipeline's n-th block (-1: none), its
+      // page, and the head's block there (null: the row is not there), each
+      // asked for a block before it is looked at.
+      auto key_of = [&](int n) {
+        if (n >= blocks) return -1;
         const int u = it.lo + 2 * n + i;
-        int j;
         if constexpr (LISTED) {
           const int e = u * kN + key;
-          j = e < p.topk ? __ldg(irow + e) : -1;
-          if (j < 0 || j >= it.ti.len) return nullptr;
+          return e < p.topk ? __ldg(irow + e) : -1;
         } else {
-          j = step_key<kN>(it.span, u) + key;
-          if (!span_holds(it.span, u, j, p.sinks)) return nullptr;
+          const int j = step_key<kN>(it.span, u) + key;
+          return span_holds(it.span, u, j, p.sinks) ? j : -1;
         }
-        const int pg = __ldg(table + (j >> p.page_shift));
-        if (pg < 0 || pg >= p.n_pages) return nullptr;
-        at = j & (page - 1);
-        return head + (int64_t)pg * p.page_bytes;
+      };
+      auto page_of = [&](int j) {
+        return j >= 0 && j < it.ti.len ? __ldg(table + (j >> p.page_shift)) : -1;
+      };
+      auto block_of = [&](int pg) -> const uint8_t* {
+        return pg >= 0 && pg < p.n_pages ? head + (int64_t)pg * p.page_bytes : nullptr;
       };
       // the row's codes and scales
       uint4 code[D / 32];
@@ -285,10 +247,10 @@ __global__ void __launch_bounds__(kThreads, 1) k_cache4_tiles(const __grid_const
           sc = make_uint2(0u, 0u);
         }
       };
-      int at_here, at_next;
-      const uint8_t* here = find(0, at_here);
-      load(here, at_here);
-      const uint8_t* next = find(1, at_next);
+      int j0 = key_of(0), j1 = key_of(1), j2 = key_of(2);
+      int pg1 = page_of(j1);
+      const uint8_t* here = block_of(page_of(j0));
+      load(here, j0 & (page - 1));
       for (int n = 0; ok && n < blocks; ++n) {
         if (!mbar_wait(smem_u32(&cs->kv_empty[i][slot]), phase ^ 1u, ctl)) {
           ok = false;
@@ -300,9 +262,11 @@ __global__ void __launch_bounds__(kThreads, 1) k_cache4_tiles(const __grid_const
         for (int x = 0; x < D / 32; ++x) cur[x] = code[x];
         const uint2 cs2 = sc;
         const bool there = here != nullptr;
-        here = next;
-        load(here, at_next);
-        next = find(n + 2, at_next);
+        here = block_of(pg1);
+        load(here, j1 & (page - 1));
+        pg1 = page_of(j2);
+        j1 = j2;
+        j2 = key_of(n + 3);
 #pragma unroll
         for (int b = 0; b < D / 16; ++b) {
           const uint32_t sw = b < 4 ? cs2.x : cs2.y;
@@ -348,6 +312,39 @@ __global__ void __launch_bounds__(kThreads, 1) k_cache4_tiles(const __grid_const
       const int blocks = pipe_blocks(it, i), others = pipe_blocks(it, i ^ 1);
       float m = neg_inf(), limit = neg_inf(), l = 0.0f, f = 0.0f;
       if (it.hi > it.lo) {
+        if (i == 0) {
+          // Q to fp16, a thread a row, scaled by a power of two (k_attn_rows.cu)
+          const uint4* q = reinterpret_cast<const uint4*>(
+              p.q + (live ? out_row(p, ti, ti.row0 + row) : 0) * D);
+          uint4 x[D / 8];
+#pragma unroll
+          for (int c = 0; c < D / 8; ++c) x[c] = live ? __ldg(q + c) : make_uint4(0, 0, 0, 0);
+          float big = 0.0f;
+#pragma unroll
+          for (int c = 0; c < D / 8; ++c) {
+            const uint32_t w[4] = {x[c].x, x[c].y, x[c].z, x[c].w};
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              big = fmaxf(big, fmaxf(fabsf(bf16_lo(w[e])), fabsf(bf16_hi(w[e]))));
+          }
+          const int e = (int)(__float_as_uint(big) >> 23);
+          const int up = (e == 0 || e == 255) ? 0 : max(-126, min(126, 137 - e));
+          const float g = __uint_as_float((uint32_t)(127 + up) << 23);
+          if (!mbar_wait_warp(smem_u32(&cs->q_empty), (n_items & 1u) ^ 1u, ctl)) break;
+          cs->factor[row] = __uint_as_float((uint32_t)(127 - up) << 23);
+#pragma unroll
+          for (int c = 0; c < D / 8; ++c)
+            asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(
+                             base + (c >> 3) * C::kQHalf + row * 128 +
+                             (((c & 7) ^ (row & 7)) << 4)),
+                         "r"(pack_f16x2(bf16_lo(x[c].x) * g, bf16_hi(x[c].x) * g)),
+                         "r"(pack_f16x2(bf16_lo(x[c].y) * g, bf16_hi(x[c].y) * g)),
+                         "r"(pack_f16x2(bf16_lo(x[c].z) * g, bf16_hi(x[c].z) * g)),
+                         "r"(pack_f16x2(bf16_lo(x[c].w) * g, bf16_hi(x[c].w) * g))
+                         : "memory");
+          fence_async();
+          mbar_arrive(smem_u32(&cs->q_full));
+        }
         if (!mbar_wait_warp(smem_u32(&cs->q_full), n_items & 1u, ctl)) break;
         ++n_items;
         // above zero: times -inf for an unseen key it is not NaN
@@ -452,15 +449,10 @@ __global__ void __launch_bounds__(kThreads, 1) k_cache4_tiles(const __grid_const
           for (int e = 0; e < 32; e += 2) {
             uint64_t xy = fma2(pair2(v[c][e], v[c][e + 1]), f2, sub2);
             float x, y;
-            if ((e >> 1) % kPolyEvery == kPolyEvery - 1) {
-              xy = ex2_poly2(xy);
-              unpair2(xy, x, y);
-            } else {
-              unpair2(xy, x, y);
-              x = ex2(x);
-              y = ex2(y);
-              xy = pair2(x, y);
-            }
+            unpair2(xy, x, y);
+            x = ex2(x);
+            y = ex2(y);
+            xy = pair2(x, y);
             ls[(e >> 1) & 1] = add2(ls[(e >> 1) & 1], xy);
             w[e >> 1] = pack_f16x2(x, y);
           }
@@ -536,11 +528,24 @@ __global__ void __launch_bounds__(kThreads, 1) k_cache4_tiles(const __grid_const
             const int64_t o = __shfl_sync(0xFFFFFFFFu, orow, (lane & ~3) + e);
             if (o >= 0) reinterpret_cast<uint4*>(p.out + o * D + col)[lane & 3] = piece[e];
           }
-        } else if (live) {
-          float4* po = reinterpret_cast<float4*>(p.part_o + part * D + col);
+        } else {
 #pragma unroll
-          for (int e = 0; e < 8; ++e)
-            po[e] = make_float4(a[4 * e], a[4 * e + 1], a[4 * e + 2], a[4 * e + 3]);
+          for (int h = 0; h < 2; ++h) {
+            uint4 piece[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const float* v = a + 16 * h + 4 * e;
+              piece[e] = make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]),
+                                    __float_as_uint(v[2]), __float_as_uint(v[3]));
+            }
+            transpose4(piece, lane);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const int64_t o = __shfl_sync(0xFFFFFFFFu, live ? part : -1, (lane & ~3) + e);
+              if (o >= 0)
+                reinterpret_cast<uint4*>(p.part_o + o * D + col + 16 * h)[lane & 3] = piece[e];
+            }
+          }
         }
       }
       tc_fence_before();

@@ -211,11 +211,11 @@ struct Tile {
 };
 
 template <int RT>
-SI_DEV bool find_tile(const RowsParams& p, int64_t id, Tile& ti) {
-  const int tile = (int)(id % p.tiles);
-  const int64_t bh = id / p.tiles;
-  ti.b = (int)(bh / p.Hk);
-  ti.hk = (int)(bh % p.Hk);
+SI_DEV bool find_tile(const RowsParams& p, uint32_t id, Tile& ti) {
+  const uint32_t bh = id / (uint32_t)p.tiles;
+  const int tile = (int)(id - bh * (uint32_t)p.tiles);
+  ti.b = (int)(bh / (uint32_t)p.Hk);
+  ti.hk = (int)(bh - (uint32_t)ti.b * (uint32_t)p.Hk);
   ti.len = seq_len(p.lens, ti.b, p.T);
   ti.q_len = seq_len(p.q_lens, ti.b, p.S);
   int last;  // one past the tile's last row
@@ -232,7 +232,7 @@ SI_DEV bool find_tile(const RowsParams& p, int64_t id, Tile& ti) {
   if (ti.rows <= 0) return false;
   ti.t_min = ti.len - ti.q_len + ti.row0 / p.G;
   ti.t_max = ti.len - ti.q_len + (ti.row0 + ti.rows - 1) / p.G;
-  ti.part = bh * p.S * p.G + ti.row0;
+  ti.part = (int64_t)bh * p.S * p.G + ti.row0;
   return true;
 }
 

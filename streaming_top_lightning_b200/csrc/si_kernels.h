@@ -128,6 +128,7 @@ struct RowsParams {
   int row_tile, tiles; // rows of a tile (8, 16, 32 or 128); tiles per kv head
   int splits;          // CTAs that share a tile's keys, chunk_keys each
   int chunk_keys;
+  int cluster;         // the splits are one cluster, which joins its results itself
   float* part_o;       // splits > 1: [B*Hk*S*G, splits, D] partial sums
   float2* part_ml;     //             [B*Hk*S*G, splits] (maximum in log2 units, sum)
 };
