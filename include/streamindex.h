@@ -361,8 +361,8 @@ int si_sparse_attention(const void* qa, const void* ka, const void* va, const in
  * Limits: B, S, T >= 1; T < 2^30; H a multiple of H_k; B*S*H, B*T*H_k < 2^31;
  * d in {64, 128} (SI_ERR_DIM); window >= 1, sinks >= 0, scale finite and >= 0
  * (SI_ERR_OPTIONS); tensors 16-byte aligned, lens, q_lens and lse 4-byte.
- * Options: key_chunk > 0 fixes the keys that one CTA takes when few rows share
- * many keys (0: the library's choice); timeout_ms; grid_ctas.
+ * Options: key_chunk > 0 makes the CTAs of few rows share the keys, at least
+ * that many each (0: the library's choice); timeout_ms; grid_ctas.
  * Workspace: caller-provided, at least si_window_attention_workspace_size
  * bytes (partial results of rows whose keys several CTAs share; 0 if none).
  */

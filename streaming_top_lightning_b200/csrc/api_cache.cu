@@ -31,15 +31,12 @@ int check_attention(int B, int S, int H, int H_k, int d) {
   return SI_OK;
 }
 
-// The plan over a tile's keys: the tile width (the narrowest of 8, 16 and 32
+// The plan over a call's keys: the tile width (the narrowest of 8, 16 and 32
 // rows that holds a kv head's rows, so that keys are read once; over a 4-bit
-// cache 128-row tensor-core tiles from 33 rows on), the keys of a CTA, and the
-// bytes of partial results.  keys: what one query may see at most.
-// With fewer tiles than three waves of CTAs the keys are split into chunks, of
-// one length for all sequences, so that they make up three waves at full
-// length (ragged sequences leave some out); a chunk keeps a CTA's four warps at
-// two steps of 32 keys, and a row's chunks stay at 128.
-int plan_rows(RowsParams* p, int64_t keys, bool cache4, int key_chunk, int sms, int d,
+// cache 128-row tensor-core tiles from 33 rows on), how the CTAs share the
+// tiles' keys, and the bytes of partial results.  keys: what one query may see
+// at most; even: that all sequences are likely to see as many.
+int plan_rows(RowsParams* p, int64_t keys, bool cache4, bool even, int key_chunk, int sms, int d,
               size_t* bytes) {
   const bool listed = p->topk > 0;
   const int64_t rows = listed ? p->G : std::min<int64_t>((int64_t)p->S * p->G, 1 << 20);
@@ -47,18 +44,22 @@ int plan_rows(RowsParams* p, int64_t keys, bool cache4, int key_chunk, int sms, 
   const int rt = p->row_tile;
   const int64_t per = listed ? (int64_t)p->S * ((p->G + rt - 1) / rt)
                              : ((int64_t)p->S * p->G + rt - 1) / rt;
+  const int64_t tiles = (int64_t)p->B * p->Hk * per;
+  if (tiles >= ((int64_t)1 << 31)) return SI_ERR_DIM;
+  p->tiles = (int)per;
   // a tile's queries see a little more than one of them; the sinks and the
   // window's two ends come in whole steps (32 keys, 64 in 128-row tiles)
   const int64_t span = listed ? keys : std::min<int64_t>(p->T, keys + rt / p->G + 1);
   const int64_t steps = (span + 31) / 32 + (listed ? (rt == 128 ? 1 : 0) : (rt == 128 ? 6 : 3));
-  const int64_t tiles = (int64_t)p->B * p->Hk * per;
+  const int64_t all = (int64_t)p->B * p->S * p->H;
   int64_t chunk = steps;
-  if (key_chunk > 0) {
-    chunk = std::max<int64_t>(key_chunk / 32, (steps + 1023) / 1024);
-  } else if (rt == 128) {
-    // one CTA per SM: the number of chunks that makes the rounds of CTAs times
-    // a chunk's cost least, a chunk costing 256 keys besides its own
-    if (tiles < sms) {
+  *bytes = 0;
+  if (rt == 128) {
+    // a persistent CTA per SM: the number of chunks that makes the rounds of
+    // CTAs times a chunk's cost least, a chunk costing 256 keys besides its own
+    if (key_chunk > 0) {
+      chunk = std::max<int64_t>(key_chunk / 32, (steps + 1023) / 1024);
+    } else if (tiles < sms) {
       int64_t best = -1;
       for (int64_t n = 1; n <= 64; ++n) {
         const int64_t c = ((steps + n - 1) / n + 3) / 4 * 4;
@@ -66,29 +67,38 @@ int plan_rows(RowsParams* p, int64_t keys, bool cache4, int key_chunk, int sms, 
         if (best < 0 || cost < best) best = cost, chunk = c;
       }
     }
+    chunk = (chunk + 3) / 4 * 4;  // whole pairs of blocks
+    p->share = kSplit;
   } else {
-    const int64_t room = 3 * (int64_t)sms * attn_rows_ctas(d, cache4, rt);
-    if (tiles < room)
-      chunk =
-          std::max<int64_t>(8, std::max((tiles * steps + room - 1) / room, (steps + 127) / 128));
+    const int64_t room = (int64_t)sms * attn_rows_ctas(d, cache4, rt);
+    const int64_t least = 8;  // two steps of 32 keys for each of a CTA's warps
+    // clusters of up to eight, as long as the GPU holds all of them at once
+    const int64_t n = std::min<int64_t>(8, std::max<int64_t>(1, room / tiles));
+    if (key_chunk == 0 && steps <= least) {
+      p->share = kSplit;
+    } else if (key_chunk == 0 && even && 2 * tiles > sms && tiles <= room) {
+      p->share = kSplit;  // a CTA a tile fills the GPU
+    } else if (key_chunk == 0 && n > 1 && steps <= n * least * 2) {
+      p->share = kCluster;
+      chunk = std::max<int64_t>(least, (steps + n - 1) / n);
+    } else {
+      // equal shares: a tile falls into at most so many pieces
+      const int64_t pieces = std::min<int64_t>(96, std::max<int64_t>(8, 8 * room / tiles));
+      chunk = std::max<int64_t>(key_chunk > 0 ? key_chunk / 32 : least,
+                                (steps + pieces - 3) / (pieces - 2));
+      p->share = kShared;
+      p->ctas = (int)room;
+      p->splits = (int)std::min<int64_t>(pieces, (steps - 1) / chunk + 2);
+    }
   }
-  if (rt == 128) chunk = (chunk + 3) / 4 * 4;  // whole pairs of blocks
-  p->splits = (int)((steps + chunk - 1) / chunk);
   p->chunk_keys = (int)chunk * 32;
-  // Up to eight chunks' CTAs that the GPU holds all at once are a cluster and
-  // join their results themselves (12 rows of a kv head over 256 keys, 32 tiles:
-  // 13.9 us a call, 19.3 with a join kernel).  Beyond one wave CTAs of short
-  // sequences would wait in their clusters for the long ones (32 ragged
-  // sequences of up to 8,192: 81 us, 58 with a join kernel).
-  p->cluster = rt < 128 && p->splits > 1 && p->splits <= 8 &&
-               tiles * p->splits <= (int64_t)sms * attn_rows_ctas(d, cache4, rt);
+  if (p->share != kShared) p->splits = (int)((steps + chunk - 1) / chunk);
+  if (p->share == kCluster && p->splits == 1) p->share = kSplit;
   if (tiles * p->splits >= ((int64_t)1 << 31)) return SI_ERR_DIM;
-  p->tiles = (int)per;
-  const int64_t all = (int64_t)p->B * p->S * p->H;
-  *bytes = 0;
-  if (p->splits > 1 && !p->cluster)
+  if (p->share != kCluster && p->splits > 1)
     *bytes = align256((size_t)all * p->splits * d * sizeof(float)) +
-             align256((size_t)all * p->splits * sizeof(float2));
+             align256((size_t)all * p->splits * sizeof(float2)) +
+             (p->share == kShared ? align256((size_t)(tiles + 1) * sizeof(int64_t)) : 0);
   return SI_OK;
 }
 
@@ -97,9 +107,13 @@ int place_partials(RowsParams* p, int d, size_t need, void* ws, size_t ws_bytes)
   if (!ws || ws_bytes < need) return SI_ERR_WORKSPACE;
   if (!aligned16(ws)) return SI_ERR_ALIGN;
   const int64_t rows = (int64_t)p->B * p->S * p->H;
-  p->part_o = static_cast<float*>(ws);
-  p->part_ml = reinterpret_cast<float2*>(
-      static_cast<char*>(ws) + align256((size_t)rows * p->splits * d * sizeof(float)));
+  char* at = static_cast<char*>(ws);
+  p->part_o = reinterpret_cast<float*>(at);
+  at += align256((size_t)rows * p->splits * d * sizeof(float));
+  p->part_ml = reinterpret_cast<float2*>(at);
+  at += align256((size_t)rows * p->splits * sizeof(float2));
+  p->share_out = reinterpret_cast<int64_t*>(at);
+  p->tile_start = p->share_out + 1;
   return SI_OK;
 }
 
@@ -125,8 +139,8 @@ int window_problem(int B, int S, int T, int H, int H_k, int d, int window, int s
   if (window_in_tiles(S, p->G, o->key_chunk)) return SI_OK;
   int max_smem = 0, sms = 0;
   plan_limits(&max_smem, &sms);
-  return plan_rows(p, std::min<int64_t>(T, (int64_t)p->window + p->sinks), false, o->key_chunk,
-                   sms, d, bytes);
+  return plan_rows(p, std::min<int64_t>(T, (int64_t)p->window + p->sinks), false, true,
+                   o->key_chunk, sms, d, bytes);
 }
 
 int cache4_problem(int width, int page, int topk, int B, int S, int H, int H_k, int d, int window,
@@ -151,7 +165,7 @@ int cache4_problem(int width, int page, int topk, int B, int S, int H, int H_k, 
   plan_limits(&max_smem, &sms);
   const int64_t keys =
       topk ? topk : std::min<int64_t>(p->T, (int64_t)p->window + p->sinks);
-  return plan_rows(p, keys, true, o->key_chunk, sms, d, bytes);
+  return plan_rows(p, keys, true, topk > 0 || window > 0, o->key_chunk, sms, d, bytes);
 }
 
 // The sizes of a call on the rows of a 4-bit cache.

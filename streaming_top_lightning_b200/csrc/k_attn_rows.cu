@@ -13,10 +13,11 @@
 // of its own in shared memory (cp.async, no barrier between warps), the running
 // maximum and sum stay in registers, and the warps of a CTA (and several CTAs,
 // each with a chunk of the keys, unless there are tiles enough) share a
-// sequence's keys; their results are joined at the end: up to eight CTAs are a
-// cluster and read one another's shared memory, more leave partial results for
-// k_attn_join.  Chunks have one length for all sequences, so ragged
-// ones keep the CTAs equally busy.
+// sequence's keys.  A small call's CTAs, up to eight a tile, are clusters that
+// join their results through one another's shared memory.  A large call's are
+// one wave, each with an equal share of all tiles' steps, however ragged the
+// sequences: a share begins and ends inside tiles, and k_attn_join joins the
+// pieces of those.
 //
 // Keys are the M side of the products, rows the N side (mma.sync m16n8k16):
 //   S^T = K Q^T,   O^T += V^T P^T
@@ -275,6 +276,82 @@ struct Bf16Rows {
 template <int D, int MODE, int NT>
 using Source = typename std::conditional<MODE == 0, Bf16Rows<D, NT>, Cache4<D, NT>>::type;
 
+// Steps of a (batch, tile) pair: the same for each kv head.
+template <int RT, int KS>
+SI_DEV int pair_steps(const RowsParams& p, int pair) {
+  Tile ti;
+  const int b = pair / p.tiles;
+  if (!find_tile<RT>(p, (uint32_t)(b * p.Hk * p.tiles + pair % p.tiles), ti)) return 0;
+  return tile_span<KS>(p, ti).steps;
+}
+
+// A CTA's share of all work, which stands in a row: (batch, tile), kv head,
+// and in a tile first kTileCost for beginning it and joining its warps, then
+// its steps.  at: the next one's place; left: how much; off: its place in its
+// tile.
+template <int KS>
+constexpr int kTileCost = 256 / KS;
+struct Share {
+  int64_t at, share, left;
+  int pair, hk, off;
+};
+
+// Sum and exclusive prefix sum over the CTA's 128 threads.
+SI_DEV int64_t scan128(int64_t v, int64_t* total) {
+  __shared__ int64_t sh[4];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  int64_t x = v;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int64_t y = __shfl_up_sync(0xFFFFFFFFu, x, o);
+    if (lane >= o) x += y;
+  }
+  if (lane == 31) sh[warp] = x;
+  __syncthreads();
+  int64_t before = 0, all = 0;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if (i < warp) before += sh[i];
+    all += sh[i];
+  }
+  *total = all;
+  return before + x - v;
+}
+
+// The share of this CTA (in shared memory): the steps of all tiles in equal
+// parts, found from the lengths by every CTA for itself.  False: there is none.
+template <int RT, int KS>
+SI_DEV bool share_of(const RowsParams& p, Share& job) {
+  const int pairs = p.B * p.tiles, per = (pairs + 127) / 128;
+  const int lo = min(pairs, (int)threadIdx.x * per), hi = min(pairs, lo + per);
+  int64_t mine = 0, total;
+  auto cost = [&](int i) {
+    const int n = pair_steps<RT, KS>(p, i);
+    return n ? n + kTileCost<KS> : 0;
+  };
+  for (int i = lo; i < hi; ++i) mine += cost(i);
+  const int64_t before = scan128(mine, &total) * p.Hk;
+  total *= p.Hk;
+  const int64_t share =
+      max((total + gridDim.x - 1) / gridDim.x, (int64_t)(p.chunk_keys / KS));
+  const int64_t at = blockIdx.x * share;
+  if (blockIdx.x == 0 && threadIdx.x == 0) *p.share_out = share;
+  if (at >= total) return false;
+  if (at >= before && at < before + mine * p.Hk) {  // one thread's tiles hold its beginning
+    int64_t x = before;
+    for (int i = lo; i < hi; ++i) {
+      const int n = cost(i);
+      if (at < x + (int64_t)n * p.Hk) {
+        job = Share{at, share, min(share, total - at), i, (int)((at - x) / n), (int)((at - x) % n)};
+        break;
+      }
+      x += (int64_t)n * p.Hk;
+    }
+  }
+  __syncthreads();
+  return true;
+}
+
 // CTAs that an SM's registers hold.
 constexpr int row_ctas(int D, int MODE, int NT) {
   return NT == 4 ? 2 : (D == 128 && MODE == 0 ? 2 : (NT == 1 ? 4 : 3));
@@ -292,17 +369,35 @@ __global__ void __launch_bounds__(kRowWarps * 32, row_ctas(D, MODE, NT))
   __shared__ uint32_t sh_nan;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int r = lane >> 2, c = lane & 3;
-  const uint32_t tile = blockIdx.x / (uint32_t)p.splits;
-  const int split = (int)(blockIdx.x - tile * (uint32_t)p.splits);
   Tile ti;
-  if (!find_tile<RT>(p, tile, ti)) return;
-  const KeySpan span = tile_span<KS>(p, ti);
-  const int u_lo = split * p.chunk_keys / KS;
-  const int u_hi =
-      split + 1 == p.splits ? span.steps : min(span.steps, (split + 1) * p.chunk_keys / KS);
-  // a sequence without keys still has rows to write, and the CTAs of a cluster
-  // stay together
-  if (u_lo >= u_hi && p.splits > 1 && !p.cluster) return;
+  KeySpan span;
+  int u_lo, u_hi, split;
+  __shared__ Share job;
+  if (p.share == kShared) {
+    if (!share_of<RT, KS>(p, job)) return;
+  } else {
+    const uint32_t tile = blockIdx.x / (uint32_t)p.splits;
+    split = (int)(blockIdx.x - tile * (uint32_t)p.splits);
+    if (!find_tile<RT>(p, tile, ti)) return;
+    // a sequence without keys still has rows to write
+    span = tile_span<KS>(p, ti);
+    u_lo = split * p.chunk_keys / KS;
+    u_hi = split + 1 == p.splits ? span.steps : min(span.steps, (split + 1) * p.chunk_keys / KS);
+  }
+  for (;;) {
+  if (p.share == kShared) {
+    // the next piece of this CTA's steps
+    const int at_tile = job.pair % p.tiles;
+    find_tile<RT>(p, (uint32_t)((job.pair / p.tiles * p.Hk + job.hk) * p.tiles + at_tile), ti);
+    span = tile_span<KS>(p, ti);
+    u_lo = max(0, job.off - kTileCost<KS>);
+    u_hi = (int)min((int64_t)span.steps, job.off - kTileCost<KS> + job.left);
+    const int64_t start = job.at - job.off + kTileCost<KS>;  // where the tile's steps begin
+    split = (int)(blockIdx.x - start / job.share);
+    if (threadIdx.x == 0 && u_lo == 0 && u_hi > 0)
+      p.tile_start[(int64_t)(ti.b * p.Hk + ti.hk) * p.tiles + at_tile] = start;
+    if (u_hi <= u_lo) return;  // the share ends before the tile's first step
+  }
   if (threadIdx.x == 0) sh_nan = 0u;
 
   Src src;
@@ -664,7 +759,7 @@ __global__ void __launch_bounds__(kRowWarps * 32, row_ctas(D, MODE, NT))
     }
   }
   if (MODE) top -= kProbShift;  // the weights' common factor
-  if (p.cluster) {
+  if (p.share == kCluster) {
     // the chunks' CTAs are one cluster: each joins the rows that its rank gives
     cg::cluster_group cl = cg::this_cluster();
     __syncthreads();  // everyone is done with sh_o
@@ -703,31 +798,52 @@ __global__ void __launch_bounds__(kRowWarps * 32, row_ctas(D, MODE, NT))
     cl.sync();  // nobody leaves while its results are read
     return;
   }
-  if (row >= ti.rows) return;
-  if (p.splits > 1) {
-    const int64_t at = (ti.part + row) * p.splits + split;
-    float* po = p.part_o + at * D + part * kPer;
+  if (row < ti.rows) {
+    if (p.share == kShared && (u_lo > 0 || u_hi < span.steps)) {
+      // (a tile has at most p.splits pieces: a share is at least chunk_keys)
+      const int64_t at = (ti.part + row) * p.splits + split;
+      float* po = p.part_o + at * D + part * kPer;
 #pragma unroll
-    for (int i = 0; i < kPer; i += 4)
-      *reinterpret_cast<float4*>(po + i) = make_float4(o[i], o[i + 1], o[i + 2], o[i + 3]);
-    if (part == 0) p.part_ml[at] = make_float2(sum == 0.0f ? neg_inf() : top, sum);
-    return;
+      for (int i = 0; i < kPer; i += 4)
+        *reinterpret_cast<float4*>(po + i) = make_float4(o[i], o[i + 1], o[i + 2], o[i + 3]);
+      if (part == 0) p.part_ml[at] = make_float2(sum == 0.0f ? neg_inf() : top, sum);
+    } else {
+      const float inv = sum == 0.0f ? 0.0f : p.v_scale / sum;
+      const int64_t orow = out_row(p, ti, ti.row0 + row);
+      uint32_t* dst = reinterpret_cast<uint32_t*>(p.out + orow * D + part * kPer);
+#pragma unroll
+      for (int i = 0; i < kPer / 4; ++i)
+        reinterpret_cast<uint2*>(dst)[i] =
+            make_uint2(pack_bf16x2(o[4 * i] * inv, o[4 * i + 1] * inv),
+                       pack_bf16x2(o[4 * i + 2] * inv, o[4 * i + 3] * inv));
+      if (part == 0 && p.lse)
+        p.lse[orow] = sum == 0.0f ? neg_inf() : (top + log2f(sum)) * 0.6931471805599453f;
+    }
   }
-  const float inv = sum == 0.0f ? 0.0f : p.v_scale / sum;
-  const int64_t orow = out_row(p, ti, ti.row0 + row);
-  uint32_t* dst = reinterpret_cast<uint32_t*>(p.out + orow * D + part * kPer);
-#pragma unroll
-  for (int i = 0; i < kPer / 4; ++i)
-    reinterpret_cast<uint2*>(dst)[i] =
-        make_uint2(pack_bf16x2(o[4 * i] * inv, o[4 * i + 1] * inv),
-                   pack_bf16x2(o[4 * i + 2] * inv, o[4 * i + 3] * inv));
-  if (part == 0 && p.lse)
-    p.lse[orow] = sum == 0.0f ? neg_inf() : (top + log2f(sum)) * 0.6931471805599453f;
+  if (p.share != kShared) return;
+  __syncthreads();  // everyone is done with the join's shared memory and this piece
+  if (threadIdx.x == 0) {
+    const int done = u_hi + kTileCost<KS> - job.off;
+    job.left -= done;
+    job.at += done;
+    // on to the next kv head, or the next tile with keys
+    job.off = 0;
+    if (++job.hk == p.Hk) {
+      job.hk = 0;
+      do {
+        ++job.pair;
+      } while (job.pair < p.B * p.tiles && pair_steps<RT, KS>(p, job.pair) == 0);
+      if (job.pair == p.B * p.tiles) job.left = 0;
+    }
+  }
+  __syncthreads();
+  if (job.left <= 0) return;
+  }
 }
 
 // Joins the chunks of a row: W warps per row (1 for few chunks, 4 for many),
 // D/32 elements a lane.
-template <int D, int KS, int RT, int W>
+template <int D, int KS, int RT, int W, bool SHARED>
 __global__ void __launch_bounds__(128) k_attn_join(const __grid_constant__ RowsParams p) {
   constexpr int E = D / 32;
   __shared__ float sh_o[4][D], sh_l[4], sh_top[4];
@@ -747,7 +863,19 @@ __global__ void __launch_bounds__(128) k_attn_join(const __grid_constant__ RowsP
     tile = row / RT;
   }
   if (!find_tile<RT>(p, bh * (uint32_t)p.tiles + tile, ti) || row >= ti.row0 + ti.rows) return;
-  const int n = min(p.splits, (tile_span<KS>(p, ti).steps * KS + p.chunk_keys - 1) / p.chunk_keys);
+  const int steps = tile_span<KS>(p, ti).steps;
+  int n;
+  if constexpr (SHARED) {
+    n = 0;
+    if (steps > 0) {
+      // the CTAs that had a part of the tile; one alone has written the rows
+      const int64_t start = p.tile_start[(int64_t)bh * p.tiles + tile], share = *p.share_out;
+      n = (int)((start + steps - 1) / share - start / share) + 1;
+      if (n == 1) return;
+    }
+  } else {
+    n = min(p.splits, (steps * KS + p.chunk_keys - 1) / p.chunk_keys);
+  }
   const float2* ml = p.part_ml + at * p.splits;
   const int s0 = W == 1 ? 0 : warp;
   float top = neg_inf();
@@ -801,14 +929,14 @@ __global__ void __launch_bounds__(128) k_attn_join(const __grid_constant__ RowsP
 
 namespace {
 
-// Up to 16 chunks a warp takes a row, beyond that four.
-template <int D, int KS, int RT>
+// Up to 24 chunks a warp takes a row, beyond that four.
+template <int D, int KS, int RT, bool SHARED>
 cudaError_t launch_join(const RowsParams& p, cudaStream_t stream) {
   const int64_t rows = (int64_t)p.B * p.Hk * p.S * p.G;
-  if (p.splits <= 16)
-    k_attn_join<D, KS, RT, 1><<<(unsigned)((rows + 3) / 4), 128, 0, stream>>>(p);
+  if (p.splits <= 24)
+    k_attn_join<D, KS, RT, 1, SHARED><<<(unsigned)((rows + 3) / 4), 128, 0, stream>>>(p);
   else
-    k_attn_join<D, KS, RT, 4><<<(unsigned)rows, 128, 0, stream>>>(p);
+    k_attn_join<D, KS, RT, 4, SHARED><<<(unsigned)rows, 128, 0, stream>>>(p);
   return cudaGetLastError();
 }
 
@@ -821,7 +949,8 @@ cudaError_t launch(const RowsParams& p, cudaStream_t stream) {
   cudaError_t e = cudaFuncSetAttribute(k_attn_rows<D, MODE, NT>,
                                        cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;
-  const int64_t ctas = (int64_t)p.B * p.Hk * p.tiles * p.splits;
+  const int64_t ctas =
+      p.share == kShared ? p.ctas : (int64_t)p.B * p.Hk * p.tiles * p.splits;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3((unsigned)ctas);
   cfg.blockDim = dim3(kRowWarps * 32);
@@ -832,10 +961,10 @@ cudaError_t launch(const RowsParams& p, cudaStream_t stream) {
   attr.val.clusterDim.x = (unsigned)p.splits;
   attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
   cfg.attrs = &attr;
-  cfg.numAttrs = p.cluster ? 1 : 0;
+  cfg.numAttrs = p.share == kCluster ? 1 : 0;
   e = cudaLaunchKernelEx(&cfg, k_attn_rows<D, MODE, NT>, p);
-  if (e != cudaSuccess || p.splits == 1 || p.cluster) return e;
-  return launch_join<D, Src::KS, 8 * NT>(p, stream);
+  if (e != cudaSuccess || p.share != kShared) return e;
+  return launch_join<D, Src::KS, 8 * NT, true>(p, stream);
 }
 
 template <int D, int MODE>
@@ -848,7 +977,8 @@ cudaError_t launch_nt(const RowsParams& p, cudaStream_t stream) {
 }  // namespace
 
 cudaError_t launch_attn_join_tiles(const RowsParams& p, int D, cudaStream_t stream) {
-  return D == 128 ? launch_join<128, 64, 128>(p, stream) : launch_join<64, 64, 128>(p, stream);
+  return D == 128 ? launch_join<128, 64, 128, false>(p, stream)
+                  : launch_join<64, 64, 128, false>(p, stream);
 }
 
 int attn_rows_ctas(int D, bool cache4, int row_tile) { return row_ctas(D, cache4 ? 1 : 0, row_tile / 8); }

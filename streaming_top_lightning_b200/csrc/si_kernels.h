@@ -107,6 +107,10 @@ cudaError_t launch_sort_rows(int32_t* idx, float* score, int64_t rows, int K, in
 cudaError_t launch_quantize_fp8(const uint16_t* x, int64_t rows, int cols, uint8_t* x8,
                                 float* scale, cudaStream_t stream);
 
+// How the CTAs of a call over a key/value cache share its tiles' keys: a CTA a
+// tile or a fixed chunk of one, a cluster a tile, or equal parts of all of them.
+enum { kSplit = 0, kCluster = 1, kShared = 2 };
+
 // Attention of few query rows over a key/value cache (k_attn_rows.cu).
 struct RowsParams {
   const uint16_t* q;   // [B,S,H,D] bf16
@@ -126,11 +130,14 @@ struct RowsParams {
   float scale_log2;    // softmax scale (and K scale) times log2(e)
   float v_scale;
   int row_tile, tiles; // rows of a tile (8, 16, 32 or 128); tiles per kv head
-  int splits;          // CTAs that share a tile's keys, chunk_keys each
-  int chunk_keys;
-  int cluster;         // the splits are one cluster, which joins its results itself
-  float* part_o;       // splits > 1: [B*Hk*S*G, splits, D] partial sums
-  float2* part_ml;     //             [B*Hk*S*G, splits] (maximum in log2 units, sum)
+  int share;           // how the CTAs share the tiles' keys
+  int splits;          // kSplit, kCluster: CTAs of a tile, chunk_keys each;
+  int chunk_keys;      // kShared: pieces of a tile at most; the least keys of a CTA
+  int ctas;            // kShared
+  float* part_o;       // kSplit, kShared: [B*Hk*S*G, splits, D] partial sums
+  float2* part_ml;     // [B*Hk*S*G, splits] (maximum in log2 units, sum)
+  int64_t* tile_start; // kShared: [B*Hk*tiles] where a tile's steps begin
+  int64_t* share_out;  // kShared: steps of a CTA
 };
 // CTAs of a tile width that an SM holds.
 int attn_rows_ctas(int D, bool cache4, int row_tile);
