@@ -14,7 +14,6 @@ device.  idx [B,S,topk] int32 (-1 padding), score [B,S,topk] fp32 (-inf padding)
 from __future__ import annotations
 
 import ctypes
-import functools
 
 from . import _lib
 from ._lib import SiOptions, SiPlanInfo, StreamIndexError  # noqa: F401
@@ -334,17 +333,8 @@ def device_error(stream=None) -> int:
 
 # ---- key/value cache: window attention, 4-bit pages, the pages' life
 #
-# A decode step makes several of these calls per layer, so their checks are
-# kept short: one comparison per tensor, plain integers to ctypes, and the
-# device and stream contexts only where the call needs them.
-
-
-def _elsewhere(t, stream) -> bool:
-    """Whether a call on t has to change the current device or stream first."""
-    torch = _torch()
-    if not isinstance(t, torch.Tensor) or not t.is_cuda:
-        raise ValueError("the call's tensors must be CUDA tensors")
-    return stream is not None or t.get_device() != torch.cuda.current_device()
+# Arguments of these calls are checked and marshalled by the compiled part of
+# this binding (csrc/bind.cpp): a decode step makes several of them per layer.
 
 
 class _at:
@@ -353,6 +343,8 @@ class _at:
 
     def __init__(self, t, stream):
         torch = _torch()
+        if not isinstance(t, torch.Tensor) or not t.is_cuda:
+            raise ValueError("the call's tensors must be CUDA tensors")
         if stream is not None and stream.device != t.device:
             raise ValueError("the stream is on another device than the tensors")
         self.guards = [torch.cuda.device(t.device)]
@@ -368,87 +360,22 @@ class _at:
             g.__exit__(*exc)
 
 
-def _raw_stream(index: int) -> int:
-    return _torch()._C._cuda_getCurrentRawStream(index)
+def _run(name, t, stream, *args):
+    """One call of the compiled binding on the device of t.  A whole number is
+    the library's status, None that another device is current."""
+    if stream is None:
+        r = getattr(_lib.bind(), name)(*args)
+        if r.__class__ is int:
+            _lib.check("si_" + name, r)
+            return None
+        if r is not None:
+            return r
+    with _at(t, stream):
+        return _run(name, t, None, *args)
 
 
-def _check(index, t, dtype, shape, name):
-    """t is a contiguous tensor of this type and shape on device ``index``."""
-    torch = _torch()
-    if not isinstance(t, torch.Tensor):
-        raise ValueError(f"{name} must be a CUDA tensor")
-    if (t.get_device() != index or t.dtype != dtype or t.shape != shape
-            or not t.is_contiguous()):
-        if t.get_device() != index:
-            raise ValueError(f"{name} is on {t.device}, the call's tensors are on cuda:{index}")
-        raise ValueError(f"{name} must be a contiguous {dtype} tensor {list(shape)}, got {t.dtype} "
-                         f"{list(t.shape)} with strides {list(t.stride())}")
-
-
-def _dims(t, n, name):
-    if not isinstance(t, _torch().Tensor) or t.dim() != n:
-        raise ValueError(f"{name} must be a {n}-d tensor")
-    return t.shape
-
-
-@functools.lru_cache(maxsize=4096)
-def _sizes(name: str, *args) -> int:
-    """A size that the library answers from whole numbers alone."""
-    n = ctypes.c_size_t(0)
-    _lib.check(name, getattr(_lib.load(), name)(*args, ctypes.byref(n)))
-    return n.value
-
-
-@functools.lru_cache(maxsize=4096)
-def _plan_size(index: int, name: str, *args) -> int:
-    """A workspace size of device ``index``, the current one."""
-    return _sizes.__wrapped__(name, *args)
-
-
-def _planned(index, name, args, opts):
-    """Workspace bytes of a call with options, which the caller may change from
-    one call to the next; without them they depend on the sizes and the device."""
-    if opts is None:
-        return _plan_size(index, name, *args, None)
-    n = ctypes.c_size_t(0)
-    _lib.check(name, getattr(_lib.load(), name)(*args, ctypes.byref(opts), ctypes.byref(n)))
-    return n.value
-
-
-def _scratch(need, workspace, t):
-    """The call's workspace as (tensor or None, address, bytes): the caller's,
-    or one of its own."""
-    if workspace is None:
-        if need == 0:
-            return None, None, 0
-        torch = _torch()
-        workspace = torch.empty(need, dtype=torch.uint8, device=t.device)
-    elif workspace.dtype != _torch().uint8 or workspace.get_device() != t.get_device() \
-            or not workspace.is_contiguous():
-        raise ValueError("workspace must be a contiguous uint8 tensor on the call's device")
-    return workspace, workspace.data_ptr(), workspace.numel()
-
-
-def _attention_out(index, qa, out, lse):
-    torch = _torch()
-    B, S, H, D = qa.shape
-    if out is None:
-        out = torch.empty((B, S, H, D), dtype=torch.bfloat16, device=qa.device)
-    else:
-        _check(index, out, torch.bfloat16, (B, S, H, D), "out")
-    if lse is None:
-        lse = torch.empty((B, S, H), dtype=torch.float32, device=qa.device)
-    else:
-        _check(index, lse, torch.float32, (B, S, H), "lse")
-    return out, lse
-
-
-def _address(index, t, B, name):
-    """Address of an optional int32 [B] tensor."""
-    if t is None:
-        return None
-    _check(index, t, _torch().int32, (B,), name)
-    return t.data_ptr()
+def _opts_address(opts):
+    return None if opts is None else ctypes.addressof(opts)
 
 
 def window_attention(qa, ka, va, window: int, sinks: int = 0, *, lens=None, q_lens=None,
@@ -462,46 +389,17 @@ def window_attention(qa, ka, va, window: int, sinks: int = 0, *, lens=None, q_le
     defaults to 1/sqrt(D).  Returns (out [B,S,H,D] bf16, lse [B,S,H] fp32: the
     logarithm of each row's sum of exponentials, which joins this result with
     another over other keys); rows past q_lens are left as they were."""
-    if _elsewhere(qa, stream):
-        with _at(qa, stream):
-            return window_attention(qa, ka, va, window, sinks, lens=lens, q_lens=q_lens,
-                                    scale=scale, out=out, lse=lse, opts=opts, workspace=workspace)
-    bf16 = _torch().bfloat16
-    at = qa.get_device()
-    B, S, H, D = _dims(qa, 4, "qa")
-    _, T, Hk, _ = _dims(ka, 4, "ka")
-    _check(at, qa, bf16, (B, S, H, D), "qa")
-    _check(at, ka, bf16, (B, T, Hk, D), "ka")
-    _check(at, va, bf16, (B, T, Hk, D), "va")
-    # the arguments stay referenced: a temporary's memory must not become the workspace's
-    lens_at, q_lens_at = _address(at, lens, B, "lens"), _address(at, q_lens, B, "q_lens")
-    need = _planned(at, "si_window_attention_workspace_size", (B, S, T, H, Hk, D, window, sinks), opts)
-    out, lse = _attention_out(at, qa, out, lse)
-    _keep, ws, ws_bytes = _scratch(need, workspace, qa)
-    rc = _lib.load().si_window_attention(
-        qa.data_ptr(), ka.data_ptr(), va.data_ptr(), lens_at, q_lens_at, B, S, T, H, Hk, D, window,
-        sinks, D ** -0.5 if scale is None else scale, out.data_ptr(), lse.data_ptr(),
-        None if opts is None else ctypes.byref(opts), ws, ws_bytes, _raw_stream(at))
-    if rc:
-        _lib.check("si_window_attention", rc)
-    return out, lse
+    return _run("window_attention", qa, stream, qa, ka, va, window, sinks, lens, q_lens, scale, out,
+                lse, _opts_address(opts), workspace)
 
 
 def cache4_page_bytes(heads: int, dim: int, page: int) -> int:
     """Bytes of one page of a 4-bit cache (si_cache4_page_bytes): ``page`` tokens
     of ``heads`` kv heads of ``dim`` elements."""
-    return _sizes("si_cache4_page_bytes", heads, dim, page)
-
-
-def _cache4(at, pages, table, lens, B, heads, dim, page):
-    """Checks a cache; its number of pages and its table's width."""
-    torch = _torch()
-    n = _dims(pages, 2, "pages")[0]
-    width = _dims(table, 2, "table")[1]
-    _check(at, pages, torch.uint8, (n, cache4_page_bytes(heads, dim, page)), "pages")
-    _check(at, table, torch.int32, (B, width), "table")
-    _check(at, lens, torch.int32, (B,), "lens")
-    return n, width
+    n = ctypes.c_size_t(0)
+    _lib.check("si_cache4_page_bytes",
+               _lib.load().si_cache4_page_bytes(heads, dim, page, ctypes.byref(n)))
+    return n.value
 
 
 def cache4_append(k, v, pages, table, lens, page: int, *, q_lens=None, k_scale: float = 1.0,
@@ -509,24 +407,9 @@ def cache4_append(k, v, pages, table, lens, page: int, *, q_lens=None, k_scale: 
     """Round the newest tokens' key and value rows (k, v [B,S,H_k,D] bf16) into
     the 4-bit pages (si_cache4_append): row i < q_lens[b] is token
     lens[b] - q_lens[b] + i.  ``pages`` [n_pages, cache4_page_bytes] uint8,
-    ``table`` [B,width] int32, ``lens`` [B] int32 with the new tokens counted."""
-    if _elsewhere(k, stream):
-        with _at(k, stream):
-            return cache4_append(k, v, pages, table, lens, page, q_lens=q_lens, k_scale=k_scale,
-                                 v_scale=v_scale)
-    bf16 = _torch().bfloat16
-    at = k.get_device()
-    B, S, Hk, D = _dims(k, 4, "k")
-    n, width = _cache4(at, pages, table, lens, B, Hk, D, page)
-    _check(at, k, bf16, (B, S, Hk, D), "k")
-    _check(at, v, bf16, (B, S, Hk, D), "v")
-    rc = _lib.load().si_cache4_append(k.data_ptr(), v.data_ptr(), B, S, Hk, D, pages.data_ptr(), n,
-                                      table.data_ptr(), width, page, lens.data_ptr(),
-                                      _address(at, q_lens, B, "q_lens"), k_scale, v_scale,
-                                      _raw_stream(at))
-    if rc:
-        _lib.check("si_cache4_append", rc)
-    return pages
+    ``table`` [B,width] int32, ``lens`` [B] int32 with the new tokens counted.
+    Returns ``pages``."""
+    return _run("cache4_append", k, stream, k, v, pages, table, lens, q_lens, page, k_scale, v_scale)
 
 
 def cache4_read(pages, table, lens, S: int, heads: int, dim: int, page: int, *, q_lens=None,
@@ -534,27 +417,9 @@ def cache4_read(pages, table, lens, S: int, heads: int, dim: int, page: int, *, 
     """The newest tokens' rows back as bf16 (si_cache4_read): (k, v), each
     [B,S,heads,dim]; rows of tokens that are not in the cache are left as they
     were in ``out``."""
-    if _elsewhere(pages, stream):
-        with _at(pages, stream):
-            return cache4_read(pages, table, lens, S, heads, dim, page, q_lens=q_lens,
-                               k_scale=k_scale, v_scale=v_scale, out=out)
-    torch = _torch()
-    at = pages.get_device()
-    B = _dims(table, 2, "table")[0]
-    n, width = _cache4(at, pages, table, lens, B, heads, dim, page)
-    if out is None:
-        out = tuple(torch.empty((B, S, heads, dim), dtype=torch.bfloat16, device=pages.device)
-                    for _ in range(2))
-    k, v = out
-    _check(at, k, torch.bfloat16, (B, S, heads, dim), "out[0]")
-    _check(at, v, torch.bfloat16, (B, S, heads, dim), "out[1]")
-    rc = _lib.load().si_cache4_read(k.data_ptr(), v.data_ptr(), B, S, heads, dim, pages.data_ptr(),
-                                    n, table.data_ptr(), width, page, lens.data_ptr(),
-                                    _address(at, q_lens, B, "q_lens"), k_scale, v_scale,
-                                    _raw_stream(at))
-    if rc:
-        _lib.check("si_cache4_read", rc)
-    return k, v
+    k, v = (None, None) if out is None else out
+    return _run("cache4_read", pages, stream, pages, table, lens, q_lens, S, heads, dim, page,
+                k_scale, v_scale, k, v)
 
 
 def cache4_attention(qa, pages, table, lens, heads: int, page: int, window: int = 0,
@@ -567,47 +432,8 @@ def cache4_attention(qa, pages, table, lens, heads: int, page: int, window: int 
     over the entries that ``idx`` [B,S,topk] int32 lists (the rows of
     ``indexer_topk`` and ``indexer_decode``).  Returns (out, lse) as
     ``window_attention``."""
-    if _elsewhere(qa, stream):
-        with _at(qa, stream):
-            return cache4_attention(qa, pages, table, lens, heads, page, window, sinks,
-                                    q_lens=q_lens, idx=idx, scale=scale, k_scale=k_scale,
-                                    v_scale=v_scale, out=out, lse=lse, opts=opts,
-                                    workspace=workspace)
-    torch = _torch()
-    at = qa.get_device()
-    B, S, H, D = _dims(qa, 4, "qa")
-    n, width = _cache4(at, pages, table, lens, B, heads, D, page)
-    _check(at, qa, torch.bfloat16, (B, S, H, D), "qa")
-    topk, entries = 0, None
-    if idx is not None:
-        topk = _dims(idx, 3, "idx")[2]
-        _check(at, idx, torch.int32, (B, S, topk), "idx")
-        entries = idx.data_ptr()
-    need = _planned(at, "si_cache4_attention_workspace_size",
-                    (width, page, topk, B, S, H, heads, D, window, sinks), opts)
-    out, lse = _attention_out(at, qa, out, lse)
-    _keep, ws, ws_bytes = _scratch(need, workspace, qa)
-    rc = _lib.load().si_cache4_attention(
-        qa.data_ptr(), pages.data_ptr(), n, table.data_ptr(), width, page, lens.data_ptr(),
-        _address(at, q_lens, B, "q_lens"), entries, topk, B, S, H, heads, D, window, sinks,
-        D ** -0.5 if scale is None else scale, k_scale, v_scale, out.data_ptr(), lse.data_ptr(),
-        None if opts is None else ctypes.byref(opts), ws, ws_bytes, _raw_stream(at))
-    if rc:
-        _lib.check("si_cache4_attention", rc)
-    return out, lse
-
-
-def _pool(refs, table, lens):
-    """Checks a pool's state; its device, pages, rows and width."""
-    int32 = _torch().int32
-    at = refs.get_device()
-    n, = _dims(refs, 1, "refs")
-    B, width = _dims(table, 2, "table")
-    _check(at, refs, int32, (n,), "refs")
-    _check(at, table, int32, (B, width), "table")
-    if lens is not None:
-        _check(at, lens, int32, (B,), "lens")
-    return at, n, B, width
+    return _run("cache4_attention", qa, stream, qa, pages, table, lens, q_lens, idx, heads, page,
+                window, sinks, scale, k_scale, v_scale, out, lse, _opts_address(opts), workspace)
 
 
 def cache_extend(refs, table, lens, page: int, *, workspace=None, stream=None):
@@ -615,56 +441,19 @@ def cache_extend(refs, table, lens, page: int, *, workspace=None, stream=None):
     tokens, the lowest free ones first (si_cache_extend); ``refs`` [n_pages]
     counts each page's holders.  Returns an int32 [1] tensor: entries for which
     no page was free."""
-    if _elsewhere(refs, stream):
-        with _at(refs, stream):
-            return cache_extend(refs, table, lens, page, workspace=workspace)
-    at, n, B, width = _pool(refs, table, lens)
-    missing = refs.new_empty(1)
-    _keep, ws, ws_bytes = _scratch(_sizes("si_cache_workspace_size", n, B, 0), workspace, refs)
-    rc = _lib.load().si_cache_extend(refs.data_ptr(), n, table.data_ptr(), B, width,
-                                     lens.data_ptr(), page, missing.data_ptr(), ws, ws_bytes,
-                                     _raw_stream(at))
-    if rc:
-        _lib.check("si_cache_extend", rc)
-    return missing
+    return _run("cache_extend", refs, stream, refs, table, lens, page, workspace)
 
 
 def cache_fork(pages, refs, table, lens, src, dst, page: int, *, workspace=None, stream=None):
     """Make each row dst[i] a copy of row src[i] (si_cache_fork): whole pages are
     shared, a partly filled last one is copied.  The rows dst must be empty
     (``cache_free``).  Returns an int32 [1] tensor: children not made."""
-    if _elsewhere(refs, stream):
-        with _at(refs, stream):
-            return cache_fork(pages, refs, table, lens, src, dst, page, workspace=workspace)
-    torch = _torch()
-    at, n, B, width = _pool(refs, table, lens)
-    size = _dims(pages, 2, "pages")[1]
-    _check(at, pages, torch.uint8, (n, size), "pages")
-    count, = _dims(src, 1, "src")
-    _check(at, src, torch.int32, (count,), "src")
-    _check(at, dst, torch.int32, (count,), "dst")
-    missing = refs.new_empty(1)
-    _keep, ws, ws_bytes = _scratch(_sizes("si_cache_workspace_size", n, B, count), workspace, refs)
-    rc = _lib.load().si_cache_fork(pages.data_ptr(), size, refs.data_ptr(), n, table.data_ptr(), B,
-                                   width, lens.data_ptr(), src.data_ptr(), dst.data_ptr(), count,
-                                   page, missing.data_ptr(), ws, ws_bytes, _raw_stream(at))
-    if rc:
-        _lib.check("si_cache_fork", rc)
-    return missing
+    return _run("cache_fork", refs, stream, pages, refs, table, lens, src, dst, page, workspace)
 
 
 def cache_free(refs, table, lens, rows, *, stream=None):
     """Empty the listed rows: their pages lose a holder (si_cache_free)."""
-    if _elsewhere(refs, stream):
-        with _at(refs, stream):
-            return cache_free(refs, table, lens, rows)
-    at, n, B, width = _pool(refs, table, lens)
-    count, = _dims(rows, 1, "rows")
-    _check(at, rows, _torch().int32, (count,), "rows")
-    rc = _lib.load().si_cache_free(refs.data_ptr(), n, table.data_ptr(), B, width, lens.data_ptr(),
-                                   rows.data_ptr(), count, _raw_stream(at))
-    if rc:
-        _lib.check("si_cache_free", rc)
+    _run("cache_free", refs, stream, refs, table, lens, rows)
 
 
 def cache_compact(pages, refs, table, *, out=None, workspace=None, stream=None):
@@ -672,23 +461,5 @@ def cache_compact(pages, refs, table, *, out=None, workspace=None, stream=None):
     Returns (table, refs, live): the new table and counts (``out`` = (table,
     refs) to write them in place, else new tensors) and an int32 [1] tensor with
     the number of pages in use."""
-    if _elsewhere(refs, stream):
-        with _at(refs, stream):
-            return cache_compact(pages, refs, table, out=out, workspace=workspace)
-    torch = _torch()
-    at, n, B, width = _pool(refs, table, None)
-    size = _dims(pages, 2, "pages")[1]
-    _check(at, pages, torch.uint8, (n, size), "pages")
-    if out is None:
-        out = (torch.empty_like(table), torch.empty_like(refs))
-    new_table, new_refs = out
-    _check(at, new_table, torch.int32, (B, width), "out[0]")
-    _check(at, new_refs, torch.int32, (n,), "out[1]")
-    live = refs.new_empty(1)
-    _keep, ws, ws_bytes = _scratch(_sizes("si_cache_workspace_size", n, B, 0), workspace, refs)
-    rc = _lib.load().si_cache_compact(pages.data_ptr(), size, refs.data_ptr(), n, table.data_ptr(),
-                                      B, width, new_refs.data_ptr(), new_table.data_ptr(),
-                                      live.data_ptr(), ws, ws_bytes, _raw_stream(at))
-    if rc:
-        _lib.check("si_cache_compact", rc)
-    return new_table, new_refs, live
+    new_table, new_refs = (None, None) if out is None else out
+    return _run("cache_compact", refs, stream, pages, refs, table, new_table, new_refs, workspace)

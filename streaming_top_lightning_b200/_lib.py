@@ -1,4 +1,5 @@
-"""ctypes loader for libstreamindex.so: declares the C ABI of include/streamindex.h.
+"""ctypes loader for libstreamindex.so: declares the C ABI of include/streamindex.h,
+and loads the compiled part of the binding (csrc/bind.cpp).
 
 There is no fallback: if the library is missing or cannot be loaded, importing
 the calls raises.  Build it with ``python -m streaming_top_lightning_b200.build``.
@@ -125,3 +126,23 @@ def load(path: str | None = None) -> ctypes.CDLL:
 def check(fn: str, status: int) -> None:
     if status != SI_OK:
         raise StreamIndexError(fn, status, load().si_status_string(status).decode())
+
+
+_bind = None
+
+
+def bind():
+    """The compiled part of the binding, attached to the loaded library."""
+    global _bind
+    if _bind is None:
+        import torch  # noqa: F401  (its libraries have to be loaded first)
+
+        lib = load()
+        try:
+            from . import _bind as module
+        except ImportError as e:
+            raise ImportError(f"the compiled binding is not built or does not fit this torch ({e}); run "
+                              "python -m streaming_top_lightning_b200.build") from e
+        module.attach(os.path.abspath(lib._name))
+        _bind = module
+    return _bind

@@ -1,4 +1,5 @@
-"""Build the CUDA library libstreamindex.so in-tree with nvcc for sm_100a.
+"""Build the CUDA library libstreamindex.so in-tree with nvcc for sm_100a, and
+the compiled part of the Python binding (_bind.so) with g++.
 
     python -m streaming_top_lightning_b200.build [--force] [--debug]
 
@@ -22,6 +23,10 @@ INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libstreamindex.so")
 # profiling build: the same sources with per-role cycle counters (SI_ROLE_CLOCKS)
 LIB_ROLES = os.path.join(PKG, "libstreamindex_roles.so")
+
+# compiled part of the Python binding, against the installed torch's headers
+BIND_SRC = os.path.join(CSRC, "bind.cpp")
+BIND = os.path.join(PKG, "_bind.so")
 
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 
@@ -68,6 +73,33 @@ def build(force: bool = False, debug: bool = False, verbose: bool = False,
     return lib
 
 
+def build_bind(force: bool = False) -> str:
+    """Compile the binding (skipped when up to date)."""
+    import sysconfig
+
+    import torch
+
+    header = os.path.join(INCLUDE, "streamindex.h")
+    if not force and os.path.exists(BIND) and os.path.getmtime(BIND) > max(
+            os.path.getmtime(BIND_SRC), os.path.getmtime(header), os.path.getmtime(torch.__file__)):
+        return BIND
+    root = os.path.dirname(torch.__file__)
+    cuda = os.path.dirname(os.path.dirname(_nvcc()))
+    tmp = BIND + f".tmp{os.getpid()}"
+    includes = [INCLUDE, os.path.join(root, "include"),
+                os.path.join(root, "include", "torch", "csrc", "api", "include"),
+                sysconfig.get_paths()["include"], os.path.join(cuda, "include")]
+    abi = int(torch._C._GLIBCXX_USE_CXX11_ABI)
+    cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared",
+           f"-D_GLIBCXX_USE_CXX11_ABI={abi}", *[f for i in includes for f in ("-I", i)], BIND_SRC,
+           "-o", tmp, "-L", os.path.join(root, "lib"), "-lc10", "-lc10_cuda", "-ltorch_cpu",
+           "-ltorch_python"]
+    subprocess.check_call(cmd)
+    os.replace(tmp, BIND)
+    return BIND
+
+
 if __name__ == "__main__":
+    print(build_bind(force="--force" in sys.argv))
     print(build(force="--force" in sys.argv, debug="--debug" in sys.argv,
                 verbose="-v" in sys.argv, roles="--roles" in sys.argv))
