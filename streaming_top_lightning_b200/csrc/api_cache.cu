@@ -92,6 +92,7 @@ int plan_rows(RowsParams* p, int64_t keys, bool cache4, bool even, int key_chunk
     }
   }
   p->chunk_keys = (int)chunk * 32;
+  if (rt == 128 && (steps + chunk - 1) / chunk <= 8) p->share = kCluster;
   if (p->share != kShared) p->splits = (int)((steps + chunk - 1) / chunk);
   if (p->share == kCluster && p->splits == 1) p->share = kSplit;
   if (tiles * p->splits >= ((int64_t)1 << 31)) return SI_ERR_DIM;

@@ -12,21 +12,27 @@
 // One persistent CTA per SM takes (row tile, chunk of keys) items.  The blocks
 // of 64 keys of an item go alternately to two pipelines that share Q and have
 // everything else of their own, the running maximum, sum and O too:
-//   4 producer warps  a thread a key or value row: 64 bytes of codes from the
-//                     page into registers (one block ahead; the page two
-//                     ahead), to fp16 and into the 128-byte swizzled layout;
-//                     keys that are not there become zeros and a cleared mask bit
+//   4 producer warps  codes from the pages into registers (one block ahead; the
+//                     page two ahead, the listed entry three), to fp16 and into
+//                     the 128-byte swizzled layout; keys that are not there
+//                     become zeros and a cleared mask bit
 //   an MMA warp       S = Q K^T into one of two TMEM buffers, two blocks ahead of
 //                     the softmax, then O += P V with P read from TMEM
 //   4 softmax warps   a thread a row, P = 2^(s - m) in fp16 over S's columns;
-//                     those of pipeline 0 also bring Q in at the start of an item
+//                     at the start of an item they bring Q in
 // At the end of an item each softmax group writes one half of the row's
-// elements, from both pipelines' O.  O is rescaled when a row's maximum has
+// elements, from both pipelines' O.  The CTAs of a tile whose keys are split are
+// a cluster (of up to eight): each joins a part of the rows, which the others
+// write into its ring.  O is rescaled when a row's maximum has
 // grown by more than 2^5 since it was last fixed; with the scale of 2^10 a
 // probability then stays below fp16's largest number.
 // Registers: the softmax threads take what the producers and MMA warps leave.
 // Every wait is bounded; a CTA that gives up records the error word and leaves.
+#include <cooperative_groups.h>
+
 #include "si_attn.cuh"
+
+namespace cg = cooperative_groups;
 
 namespace si {
 namespace {
@@ -36,6 +42,8 @@ constexpr int kN = 64;
 constexpr int kThreads = 640;  // softmax 0, 1; producers 0, 1; MMA warps 16, 17
 constexpr int kSlots = 3;      // K and V blocks of a pipeline
 constexpr float kShift = 10.0f, kGrow = 5.0f;
+template <int D>
+constexpr int kRowPad = D + 4;  // floats of a row in a cluster's join: O, maximum, sum
 
 template <int D>
 struct TileCfg {
@@ -70,8 +78,23 @@ SI_DEV bool tile_item(const RowsParams& p, int id, TileItem& it) {
   const int per = p.chunk_keys / kN;
   it.lo = it.split * per;
   it.hi = it.split + 1 == p.splits ? it.span.steps : min(it.span.steps, it.lo + per);
-  return it.lo < it.hi || p.splits == 1;  // a row without keys is still written
+  // a row without keys is still written, and the CTAs of a cluster stay together
+  return it.lo < it.hi || p.splits == 1 || p.share == kCluster;
 }
+// All threads of the cluster's CTAs.
+SI_DEV void cluster_sync() {
+  __syncwarp();
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::
+                   : "memory");
+}
+// The two meetings of a cluster's join, for warps with no part in it.
+SI_DEV void stand_by(const RowsParams& p) {
+  Tile ti;
+  if (p.share != kCluster || !find_tile<kM>(p, blockIdx.x / p.splits, ti)) return;
+  cluster_sync();
+  cluster_sync();
+}
+
 // Blocks of pipeline i.
 SI_DEV int pipe_blocks(const TileItem& it, int i) { return max(0, it.hi - it.lo + 1 - i) >> 1; }
 
@@ -105,7 +128,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_cache4_tiles(const __grid_const
         mbar_init(smem_u32(&cs->pv_done[i][x]), 1);
       }
     }
-    mbar_init(smem_u32(&cs->q_full), kM);
+    mbar_init(smem_u32(&cs->q_full), 2 * kM);
     mbar_init(smem_u32(&cs->q_empty), 2);
     mbar_init(smem_u32(&cs->ml_full), 2 * kM);
     mbar_init(smem_u32(&cs->o_free), 2 * kM);
@@ -189,13 +212,19 @@ __global__ void __launch_bounds__(kThreads, 1) k_cache4_tiles(const __grid_const
         }
       }
     }
+    stand_by(p);
   } else if (warp >= 8) {
     // ------------------------------------------------------------ producers
     asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
+    // A warp takes 32 rows: keys 0-31 or 32-63 of a block, as K or as V rows.
+    // Its lanes look up a row each; L lanes then share a row, 16 bytes of codes
+    // (32 elements) each, 32 / L rows at a time, so that a load instruction
+    // touches few lines.
+    constexpr int L = D / 32, R = 32 / L;
     const int i = (warp - 8) >> 2;
-    const int pt = tid - 256 - i * 128;     // thread of the group
-    const int key = pt & (kN - 1);
-    const bool is_v = pt >= kN;
+    const bool is_v = (warp & 2) != 0;
+    const int key0 = (warp & 1) * 32, key = key0 + lane;
+    const int c = lane % L, sub = lane / L;
     const int page = 1 << p.page_shift;
     const uint32_t my_ring = ring + i * (kSlots * 2 * C::kBlock) + (is_v ? C::kBlock : 0);
     uint32_t slot = 0, phase = 0;
@@ -225,74 +254,75 @@ __global__ void __launch_bounds__(kThreads, 1) k_cache4_tiles(const __grid_const
       auto page_of = [&](int j) {
         return j >= 0 && j < it.ti.len ? __ldg(table + (j >> p.page_shift)) : -1;
       };
-      auto block_of = [&](int pg) -> const uint8_t* {
-        return pg >= 0 && pg < p.n_pages ? head + (int64_t)pg * p.page_bytes : nullptr;
+      // A row's place in the pool, its page's offset plus its slot (page_bytes
+      // is a multiple of the page's tokens), or -1: it is not there.
+      auto place = [&](int j, int pg) -> int64_t {
+        return pg >= 0 && pg < p.n_pages ? (int64_t)pg * p.page_bytes + (j & (page - 1)) : -1;
       };
-      // the row's codes and scales
-      uint4 code[D / 32];
-      uint2 sc;
-      auto load = [&](const uint8_t* blk, int at) {
-        if (blk) {
-          const uint4* c = reinterpret_cast<const uint4*>(blk + ((is_v ? page : 0) + at) * (D / 2));
+      // codes and scales of this lane's part of L rows; at: its own row's place
+      uint4 code[L];
+      uint32_t sc[L];
+      auto load = [&](int64_t at) {
 #pragma unroll
-          for (int x = 0; x < D / 32; ++x) code[x] = __ldg(c + x);
-          const uint8_t* s = blk + page * D + ((is_v ? page : 0) + at) * (D / 16);
-          if constexpr (D == 128)
-            sc = __ldg(reinterpret_cast<const uint2*>(s));
-          else
-            sc = make_uint2(__ldg(reinterpret_cast<const uint32_t*>(s)), 0u);
-        } else {
-#pragma unroll
-          for (int x = 0; x < D / 32; ++x) code[x] = make_uint4(0, 0, 0, 0);
-          sc = make_uint2(0u, 0u);
+        for (int x = 0; x < L; ++x) {
+          const int64_t o = __shfl_sync(0xFFFFFFFFu, at, x * R + sub);
+          const int sl = (int)o & (page - 1);
+          const uint8_t* blk = head + (o - sl);
+          const int row = (is_v ? page : 0) + sl;
+          code[x] = o >= 0 ? __ldg(reinterpret_cast<const uint4*>(blk + row * (D / 2)) + c)
+                           : make_uint4(0, 0, 0, 0);
+          sc[x] = o >= 0 ? __ldg(reinterpret_cast<const uint16_t*>(blk + page * D + row * (D / 16)) + c)
+                         : 0u;
         }
       };
       int j0 = key_of(0), j1 = key_of(1), j2 = key_of(2);
       int pg1 = page_of(j1);
-      const uint8_t* here = block_of(page_of(j0));
-      load(here, j0 & (page - 1));
+      int64_t here = place(j0, page_of(j0));
+      load(here);
       for (int n = 0; ok && n < blocks; ++n) {
-        if (!mbar_wait(smem_u32(&cs->kv_empty[i][slot]), phase ^ 1u, ctl)) {
+        if (!mbar_wait_warp(smem_u32(&cs->kv_empty[i][slot]), phase ^ 1u, ctl)) {
           ok = false;
           break;
         }
-        const uint32_t dst = my_ring + slot * (2 * C::kBlock) + key * 128;
-        uint4 cur[D / 32];
+        const uint32_t dst = my_ring + slot * (2 * C::kBlock);
+        uint4 cur[L];
+        uint32_t cur_s[L];
 #pragma unroll
-        for (int x = 0; x < D / 32; ++x) cur[x] = code[x];
-        const uint2 cs2 = sc;
-        const bool there = here != nullptr;
-        here = block_of(pg1);
-        load(here, j1 & (page - 1));
+        for (int x = 0; x < L; ++x) cur[x] = code[x], cur_s[x] = sc[x];
+        const uint32_t m = __ballot_sync(0xFFFFFFFFu, here >= 0);
+        here = place(j1, pg1);
+        load(here);
         pg1 = page_of(j2);
         j1 = j2;
         j2 = key_of(n + 3);
 #pragma unroll
-        for (int b = 0; b < D / 16; ++b) {
-          const uint32_t sw = b < 4 ? cs2.x : cs2.y;
-          const uint32_t s1 = e4m3x2((sw >> (8 * (b & 3))) & 0xFFu);
-          const uint32_t s = __byte_perm(s1, 0, 0x1010);
-          const uint4 c4 = cur[b >> 1];
-          const uint32_t w0 = (b & 1) ? c4.z : c4.x, w1 = (b & 1) ? c4.w : c4.y;
+        for (int x = 0; x < L; ++x) {
+          const int row = key0 + x * R + sub;
+          const uint32_t s2 = e4m3x2(cur_s[x]);
+          const uint32_t f[2] = {__byte_perm(s2, 0, 0x1010), __byte_perm(s2, 0, 0x3232)};
+          const uint32_t w[4] = {cur[x].x, cur[x].y, cur[x].z, cur[x].w};
+          const uint32_t to = dst + row * 128 + (c >> 1) * C::kHalf;
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const uint32_t w = h ? w1 : w0;
-            const int ch = 2 * b + h;
+          for (int k = 0; k < 4; ++k) {
+            // the upper half's lanes store in another order: no bank twice
+            const int q = k ^ (c & 2);
+            const uint32_t ww = (c & 2) ? w[k ^ 2] : w[k];
+            const uint32_t s = (c & 2) ? f[(k ^ 2) >> 1] : f[k >> 1];
             asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(
-                             dst + (ch >> 3) * C::kHalf + (((ch & 7) ^ (key & 7)) << 4)),
-                         "r"(hmul2(e2m1x2<0>(w), s)), "r"(hmul2(e2m1x2<1>(w), s)),
-                         "r"(hmul2(e2m1x2<2>(w), s)), "r"(hmul2(e2m1x2<3>(w), s))
+                             to + (((4 * (c & 1) + q) ^ (row & 7)) << 4)),
+                         "r"(hmul2(e2m1x2<0>(ww), s)), "r"(hmul2(e2m1x2<1>(ww), s)),
+                         "r"(hmul2(e2m1x2<2>(ww), s)), "r"(hmul2(e2m1x2<3>(ww), s))
                          : "memory");
           }
         }
-        const uint32_t m = __ballot_sync(0xFFFFFFFFu, there);
         if (!is_v && lane == 0)
-          reinterpret_cast<uint32_t*>(&cs->mask[i][slot])[(pt >> 5) & 1] = m;
+          reinterpret_cast<uint32_t*>(&cs->mask[i][slot])[warp & 1] = m;
         fence_async();
         mbar_arrive(smem_u32(&cs->kv_full[i][slot]));
         if (++slot == (uint32_t)kSlots) slot = 0, phase ^= 1u;
       }
     }
+    stand_by(p);
   } else {
     // ------------------------------------------------------------ softmax
     asm volatile("setmaxnreg.inc.sync.aligned.u32 144;");
@@ -302,7 +332,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_cache4_tiles(const __grid_const
     const uint32_t s_col = lane_base + i * 128, o_all = lane_base + 256, o_col = o_all + i * 128;
     // parities: each pipeline's values per buffer, this one's scores per buffer
     uint32_t mine = 0, theirs = 0, ns = 0, kslot = 0, kphase = 0, n_items = 0, n_ml = 0;
-    bool stop = false;
+    bool stop = false, met = false;
     for (int id = blockIdx.x; !stop && id < items; id += gridDim.x) {
       TileItem it;
       if (!tile_item(p, id, it)) continue;
@@ -312,39 +342,44 @@ __global__ void __launch_bounds__(kThreads, 1) k_cache4_tiles(const __grid_const
       const int blocks = pipe_blocks(it, i), others = pipe_blocks(it, i ^ 1);
       float m = neg_inf(), limit = neg_inf(), l = 0.0f, f = 0.0f;
       if (it.hi > it.lo) {
-        if (i == 0) {
-          // Q to fp16, a thread a row, scaled by a power of two (k_attn_rows.cu)
-          const uint4* q = reinterpret_cast<const uint4*>(
-              p.q + (live ? out_row(p, ti, ti.row0 + row) : 0) * D);
-          uint4 x[D / 8];
+        // Q to fp16, scaled by a power of two a row (k_attn_rows.cu): 16 rows a
+        // warp, D/8 lanes a row
+        constexpr int LQ = D / 8, RQ = 32 / LQ;
+        uint4 x[16 / RQ];
 #pragma unroll
-          for (int c = 0; c < D / 8; ++c) x[c] = live ? __ldg(q + c) : make_uint4(0, 0, 0, 0);
+        for (int y = 0; y < 16 / RQ; ++y) {
+          const int r = warp * 16 + y * RQ + lane / LQ;
+          x[y] = r < ti.rows ? __ldg(reinterpret_cast<const uint4*>(
+                                         p.q + out_row(p, ti, ti.row0 + r) * D) +
+                                     lane % LQ)
+                             : make_uint4(0, 0, 0, 0);
+        }
+        if (!mbar_wait_warp(smem_u32(&cs->q_empty), (n_items & 1u) ^ 1u, ctl)) break;
+#pragma unroll
+        for (int y = 0; y < 16 / RQ; ++y) {
+          const int r = warp * 16 + y * RQ + lane / LQ, c = lane % LQ;
+          const uint32_t w[4] = {x[y].x, x[y].y, x[y].z, x[y].w};
           float big = 0.0f;
 #pragma unroll
-          for (int c = 0; c < D / 8; ++c) {
-            const uint32_t w[4] = {x[c].x, x[c].y, x[c].z, x[c].w};
+          for (int e = 0; e < 4; ++e)
+            big = fmaxf(big, fmaxf(fabsf(bf16_lo(w[e])), fabsf(bf16_hi(w[e]))));
 #pragma unroll
-            for (int e = 0; e < 4; ++e)
-              big = fmaxf(big, fmaxf(fabsf(bf16_lo(w[e])), fabsf(bf16_hi(w[e]))));
-          }
+          for (int o = 1; o < LQ; o <<= 1)
+            big = fmaxf(big, __shfl_xor_sync(0xFFFFFFFFu, big, o));
           const int e = (int)(__float_as_uint(big) >> 23);
           const int up = (e == 0 || e == 255) ? 0 : max(-126, min(126, 137 - e));
           const float g = __uint_as_float((uint32_t)(127 + up) << 23);
-          if (!mbar_wait_warp(smem_u32(&cs->q_empty), (n_items & 1u) ^ 1u, ctl)) break;
-          cs->factor[row] = __uint_as_float((uint32_t)(127 - up) << 23);
-#pragma unroll
-          for (int c = 0; c < D / 8; ++c)
-            asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(
-                             base + (c >> 3) * C::kQHalf + row * 128 +
-                             (((c & 7) ^ (row & 7)) << 4)),
-                         "r"(pack_f16x2(bf16_lo(x[c].x) * g, bf16_hi(x[c].x) * g)),
-                         "r"(pack_f16x2(bf16_lo(x[c].y) * g, bf16_hi(x[c].y) * g)),
-                         "r"(pack_f16x2(bf16_lo(x[c].z) * g, bf16_hi(x[c].z) * g)),
-                         "r"(pack_f16x2(bf16_lo(x[c].w) * g, bf16_hi(x[c].w) * g))
-                         : "memory");
-          fence_async();
-          mbar_arrive(smem_u32(&cs->q_full));
+          if (c == 0) cs->factor[r] = __uint_as_float((uint32_t)(127 - up) << 23);
+          asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(
+                           base + (c >> 3) * C::kQHalf + r * 128 + (((c & 7) ^ (r & 7)) << 4)),
+                       "r"(pack_f16x2(bf16_lo(w[0]) * g, bf16_hi(w[0]) * g)),
+                       "r"(pack_f16x2(bf16_lo(w[1]) * g, bf16_hi(w[1]) * g)),
+                       "r"(pack_f16x2(bf16_lo(w[2]) * g, bf16_hi(w[2]) * g)),
+                       "r"(pack_f16x2(bf16_lo(w[3]) * g, bf16_hi(w[3]) * g))
+                       : "memory");
         }
+        fence_async();
+        mbar_arrive(smem_u32(&cs->q_full));
         if (!mbar_wait_warp(smem_u32(&cs->q_full), n_items & 1u, ctl)) break;
         ++n_items;
         // above zero: times -inf for an unseen key it is not NaN
@@ -498,6 +533,17 @@ __global__ void __launch_bounds__(kThreads, 1) k_cache4_tiles(const __grid_const
       const float inv = sum == 0.0f ? 0.0f : (final_rows ? p.v_scale / sum : 1.0f);
       const int64_t part = (ti.part + row) * p.splits + it.split;
       const int64_t orow = live ? out_row(p, ti, ti.row0 + row) : -1;
+      // in a cluster, the CTA that joins this row, and the row's place there
+      const int per = (kM + p.splits - 1) / p.splits, rank = row / per;
+      float* there = nullptr;
+      if (p.share == kCluster) {
+        cluster_sync();  // every CTA is done with its ring
+        cg::cluster_group cl = cg::this_cluster();
+        float* mine = reinterpret_cast<float*>(smem + C::kQ);
+        there = cl.map_shared_rank(mine, rank) + (it.split * per + row - rank * per) * kRowPad<D>;
+        if (i == 0)
+          *reinterpret_cast<float2*>(there + D) = make_float2(sum == 0.0f ? neg_inf() : top, sum);
+      }
 #pragma unroll 1
       for (int c = 0; c < D / 64; ++c) {
         const int col = i * (D / 2) + c * 32;
@@ -528,6 +574,11 @@ __global__ void __launch_bounds__(kThreads, 1) k_cache4_tiles(const __grid_const
             const int64_t o = __shfl_sync(0xFFFFFFFFu, orow, (lane & ~3) + e);
             if (o >= 0) reinterpret_cast<uint4*>(p.out + o * D + col)[lane & 3] = piece[e];
           }
+        } else if (p.share == kCluster) {
+#pragma unroll
+          for (int e = 0; e < 8; ++e)
+            *reinterpret_cast<float4*>(there + col + 4 * e) =
+                make_float4(a[4 * e], a[4 * e + 1], a[4 * e + 2], a[4 * e + 3]);
         } else {
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
@@ -551,7 +602,35 @@ __global__ void __launch_bounds__(kThreads, 1) k_cache4_tiles(const __grid_const
       tc_fence_before();
       mbar_arrive(smem_u32(&cs->o_free));
       ++n_ml;
-      if (live && i == 0) {
+      if (p.share == kCluster) {
+        cluster_sync();  // all of this CTA's rows are here
+        const float* mine = reinterpret_cast<const float*>(smem + C::kQ);
+        const int r0 = it.split * per;  // the split is the CTA's rank
+        for (int x = warp; x < per && r0 + x < ti.rows; x += 8) {
+          float big = neg_inf(), tot = 0.0f, acc[D / 32];
+#pragma unroll
+          for (int e = 0; e < D / 32; ++e) acc[e] = 0.0f;
+          for (int y = 0; y < p.splits; ++y)
+            big = fmaxf(big, mine[(y * per + x) * kRowPad<D> + D]);
+          for (int y = 0; y < p.splits; ++y) {
+            const float* from = mine + (y * per + x) * kRowPad<D>;
+            const float w = from[D + 1] == 0.0f ? 0.0f : ex2(from[D] - big);
+            tot = fmaf(from[D + 1], w, tot);
+#pragma unroll
+            for (int e = 0; e < D / 32; ++e)
+              acc[e] = fmaf(from[lane * (D / 32) + e], w, acc[e]);
+          }
+          const float fin = tot == 0.0f ? 0.0f : p.v_scale / tot;
+          const int64_t to = out_row(p, ti, ti.row0 + r0 + x);
+          uint32_t* dst = reinterpret_cast<uint32_t*>(p.out + to * D) + lane * (D / 64);
+#pragma unroll
+          for (int e = 0; e < D / 64; ++e)
+            dst[e] = pack_bf16x2(acc[2 * e] * fin, acc[2 * e + 1] * fin);
+          if (lane == 0 && p.lse)
+            p.lse[to] = tot == 0.0f ? neg_inf() : (big - kShift + log2f(tot)) * 0.6931471805599453f;
+        }
+        met = true;
+      } else if (live && i == 0) {
         const float lg = top - kShift;
         if (!final_rows)
           p.part_ml[part] = make_float2(sum == 0.0f ? neg_inf() : lg, sum);
@@ -559,6 +638,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_cache4_tiles(const __grid_const
           p.lse[orow] = sum == 0.0f ? neg_inf() : (lg + log2f(sum)) * 0.6931471805599453f;
       }
     }
+    if (!met) stand_by(p);  // gave up before the join: the others still meet
   }
 
   tc_fence_before();
@@ -581,19 +661,30 @@ static cudaError_t launch_tiles(const RowsParams& p, int items, int grid, uint32
   const cudaError_t e = cudaFuncSetAttribute(
       k_cache4_tiles<D, LISTED>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;
-  k_cache4_tiles<D, LISTED><<<grid, kThreads, smem, stream>>>(p, items, err, timeout_ns);
-  return cudaGetLastError();
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3((unsigned)grid);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr{};
+  attr.id = cudaLaunchAttributeClusterDimension;
+  attr.val.clusterDim.x = (unsigned)p.splits;
+  attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = p.share == kCluster ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, k_cache4_tiles<D, LISTED>, p, items, err, timeout_ns);
 }
 
 cudaError_t launch_cache4_tiles(const RowsParams& p, int D, int grid, uint32_t* err,
                                 uint64_t timeout_ns, cudaStream_t stream) {
   const int items = (int)((int64_t)p.B * p.Hk * p.tiles * p.splits);
+  if (p.share == kCluster) grid = items;  // an item a CTA
   const cudaError_t e =
       D == 128 ? (p.idx ? launch_tiles<128, true>(p, items, grid, err, timeout_ns, stream)
                         : launch_tiles<128, false>(p, items, grid, err, timeout_ns, stream))
                : (p.idx ? launch_tiles<64, true>(p, items, grid, err, timeout_ns, stream)
                         : launch_tiles<64, false>(p, items, grid, err, timeout_ns, stream));
-  if (e != cudaSuccess || p.splits == 1) return e;
+  if (e != cudaSuccess || p.splits == 1 || p.share == kCluster) return e;
   return launch_attn_join_tiles(p, D, stream);
 }
 
