@@ -606,10 +606,14 @@ __global__ void __launch_bounds__(kThreads, 1) k_cache4_tiles(const __grid_const
         cluster_sync();  // all of this CTA's rows are here
         const float* mine = reinterpret_cast<const float*>(smem + C::kQ);
         const int r0 = it.split * per;  // the split is the CTA's rank
-        for (int x = warp; x < per && r0 + x < ti.rows; x += 8) {
-          float big = neg_inf(), tot = 0.0f, acc[D / 32];
+        // D/32 threads a row, 32 elements each, in an order that spreads the banks
+        constexpr int TR = D / 32;
+        const int q = tid % TR;
+        for (int x = tid / TR; x < per && r0 + x < ti.rows; x += 2 * kM / TR) {
+          float big = neg_inf(), tot = 0.0f;
+          float4 acc[8];
 #pragma unroll
-          for (int e = 0; e < D / 32; ++e) acc[e] = 0.0f;
+          for (int e = 0; e < 8; ++e) acc[e] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
           for (int y = 0; y < p.splits; ++y)
             big = fmaxf(big, mine[(y * per + x) * kRowPad<D> + D]);
           for (int y = 0; y < p.splits; ++y) {
@@ -617,16 +621,21 @@ __global__ void __launch_bounds__(kThreads, 1) k_cache4_tiles(const __grid_const
             const float w = from[D + 1] == 0.0f ? 0.0f : ex2(from[D] - big);
             tot = fmaf(from[D + 1], w, tot);
 #pragma unroll
-            for (int e = 0; e < D / 32; ++e)
-              acc[e] = fmaf(from[lane * (D / 32) + e], w, acc[e]);
+            for (int e = 0; e < 8; ++e) {
+              const float4 v =
+                  *reinterpret_cast<const float4*>(from + 32 * q + 4 * ((e + 2 * q) & 7));
+              acc[e].x = fmaf(v.x, w, acc[e].x), acc[e].y = fmaf(v.y, w, acc[e].y);
+              acc[e].z = fmaf(v.z, w, acc[e].z), acc[e].w = fmaf(v.w, w, acc[e].w);
+            }
           }
           const float fin = tot == 0.0f ? 0.0f : p.v_scale / tot;
           const int64_t to = out_row(p, ti, ti.row0 + r0 + x);
-          uint32_t* dst = reinterpret_cast<uint32_t*>(p.out + to * D) + lane * (D / 64);
 #pragma unroll
-          for (int e = 0; e < D / 64; ++e)
-            dst[e] = pack_bf16x2(acc[2 * e] * fin, acc[2 * e + 1] * fin);
-          if (lane == 0 && p.lse)
+          for (int e = 0; e < 8; ++e)
+            *reinterpret_cast<uint2*>(p.out + to * D + 32 * q + 4 * ((e + 2 * q) & 7)) =
+                make_uint2(pack_bf16x2(acc[e].x * fin, acc[e].y * fin),
+                           pack_bf16x2(acc[e].z * fin, acc[e].w * fin));
+          if (q == 0 && p.lse)
             p.lse[to] = tot == 0.0f ? neg_inf() : (big - kShift + log2f(tot)) * 0.6931471805599453f;
         }
         met = true;
