@@ -28,17 +28,19 @@ struct Block {
 };
 
 template <int D>
-SI_DEV Block<D> find_block(const Cache4Params& p, int64_t id) {
+SI_DEV Block<D> find_block(const Cache4Params& p, uint32_t block, int thread) {
   constexpr int NB = D / 16;
   Block<D> r;
-  const int blk = (int)(id % NB);
-  int64_t x = id / NB;
-  const int hk = (int)(x % p.Hk);
-  x /= p.Hk;
-  r.is_v = (x & 1) != 0;  // all of a row's key blocks, then its value blocks
-  x >>= 1;
-  const int i = (int)(x % p.S);
-  const int b = (int)(x / p.S);
+  // (row, key or value, kv head, block): `block` counts rows of blocks, and
+  // B * S * Hk < 2^31
+  const int blk = thread % NB;
+  const uint32_t x = block * (kThreads / NB) + thread / NB;
+  const uint32_t row2 = x / (uint32_t)p.Hk;
+  const int hk = (int)(x - row2 * (uint32_t)p.Hk);
+  r.is_v = (row2 & 1u) != 0;  // all of a row's key blocks, then its value blocks
+  const uint32_t row = row2 >> 1;
+  const int b = (int)(row / (uint32_t)p.S);
+  const int i = (int)(row - (uint32_t)b * (uint32_t)p.S);
   r.live = false;
   if (b >= p.B) return r;
   const int page = 1 << p.page_shift;
@@ -70,7 +72,7 @@ SI_DEV uint32_t e2m1_byte(float lo, float hi) {
 
 template <int D>
 __global__ void __launch_bounds__(kThreads) k_cache4_append(const Cache4Params p) {
-  const Block<D> bl = find_block<D>(p, (int64_t)blockIdx.x * kThreads + threadIdx.x);
+  const Block<D> bl = find_block<D>(p, blockIdx.x, threadIdx.x);
   if (!bl.live) return;
   const uint4* src = reinterpret_cast<const uint4*>((bl.is_v ? p.v : p.k) + bl.src);
   const uint4 a = __ldcs(src), b = __ldcs(src + 1);
@@ -114,7 +116,7 @@ __global__ void __launch_bounds__(kThreads) k_cache4_append(const Cache4Params p
 // The rows back as bf16: code x (g s), rounded once.
 template <int D>
 __global__ void __launch_bounds__(kThreads) k_cache4_read(const Cache4Params p) {
-  const Block<D> bl = find_block<D>(p, (int64_t)blockIdx.x * kThreads + threadIdx.x);
+  const Block<D> bl = find_block<D>(p, blockIdx.x, threadIdx.x);
   if (!bl.live) return;
   const uint2 c = *reinterpret_cast<const uint2*>(p.pages + bl.codes);
   const float gs = (bl.is_v ? p.v_scale : p.k_scale) *

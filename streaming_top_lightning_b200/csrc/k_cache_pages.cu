@@ -6,9 +6,10 @@
 // of its rows, so a result depends on nothing but the inputs.
 //
 // The counting parts read the counts and tables twice and decide with prefix
-// sums over them: one cluster of eight CTAs, each with a contiguous share,
-// that exchange their shares' sums through distributed shared memory (one
-// launch; a grid-wide scan would take two or three).  They are bound by latency.
+// sums over them: one CTA where a few rounds of its threads are enough, else a
+// cluster of eight, each with a contiguous share, that exchange their shares'
+// sums through distributed shared memory (one launch; a grid-wide scan would
+// take two or three).  They are bound by latency: of a load, a barrier, a round.
 // Copies of pages run in a second launch over the whole GPU, HBM-bound.
 #include <cooperative_groups.h>
 
@@ -19,7 +20,7 @@ namespace cg = cooperative_groups;
 namespace si {
 namespace {
 
-constexpr int kClu = 8;         // CTAs of the counting kernels' cluster
+constexpr int kClu = 8;         // CTAs of a counting kernel's cluster, or one
 constexpr int kThreads = 1024;  // threads of each
 constexpr int kSlice = 16384;   // bytes of a page that one CTA copies at a time
 
@@ -56,28 +57,71 @@ SI_DEV int cta_scan(int v, int* sh, int* total) {
   return x - v + (warp > 0 ? before : 0);
 }
 
-// The sums of all CTAs' `mine`: those before this CTA, and all of them.
-SI_DEV void cluster_sums(cg::cluster_group& cl, int* slot, int mine, int* before, int* all) {
-  if (threadIdx.x == 0) *slot = mine;
-  cl.sync();
-  int b = 0, t = 0;
-  const unsigned rank = cl.block_rank();
-#pragma unroll
-  for (unsigned i = 0; i < kClu; ++i) {
-    const int v = *cl.map_shared_rank(slot, i);
-    if (i < rank) b += v;
-    t += v;
+// The CTAs of a counting kernel: C = 1 or a cluster.
+template <int C>
+struct Team {
+  unsigned rank;
+  SI_DEV Team() : rank(C == 1 ? 0u : cg::this_cluster().block_rank()) {}
+  // Everyone's writes, to global memory too, are seen by everyone.
+  SI_DEV void sync() const {
+    if constexpr (C == 1) {
+      __syncthreads();
+    } else {
+      __threadfence();
+      cg::this_cluster().sync();
+    }
   }
-  *before = b;
-  *all = t;
-}
+  // Two sums of each CTA (the same in all its threads): those of the CTAs
+  // before this one, and of all.  slot: two numbers in shared memory.
+  SI_DEV void sums(int* slot, int a, int b, int (&before)[2], int (&all)[2]) const {
+    if constexpr (C == 1) {
+      before[0] = before[1] = 0;
+      all[0] = a, all[1] = b;
+    } else {
+      if (threadIdx.x == 0) slot[0] = a, slot[1] = b;
+      sync();
+      cg::cluster_group cl = cg::this_cluster();
+#pragma unroll
+      for (int i = 0; i < 2; ++i) before[i] = all[i] = 0;
+#pragma unroll
+      for (unsigned r = 0; r < C; ++r) {
+        const int* o = cl.map_shared_rank(slot, r);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const int v = o[i];
+          if (r < rank) before[i] += v;
+          all[i] += v;
+        }
+      }
+    }
+  }
+  // This CTA's share of n things, in whole fours.
+  SI_DEV int64_t from(int64_t n) const { return C == 1 ? 0 : n * rank / C / 4 * 4; }
+  SI_DEV int64_t to(int64_t n) const {
+    return C == 1 || rank == C - 1 ? n : n * (rank + 1) / C / 4 * 4;
+  }
+};
 
-SI_DEV int64_t share(int64_t n, unsigned rank) { return n * rank / kClu; }
+// Four counts from i on (a multiple of four; the array 16-byte aligned or not),
+// those past the end as `none`.
+SI_DEV int4 four(const int32_t* a, int64_t i, int64_t end, int none) {
+  if (i + 4 <= end && (reinterpret_cast<uintptr_t>(a) & 15u) == 0)
+    return *reinterpret_cast<const int4*>(a + i);
+  int4 v = make_int4(none, none, none, none);
+  if (i < end) v.x = a[i];
+  if (i + 1 < end) v.y = a[i + 1];
+  if (i + 2 < end) v.z = a[i + 2];
+  if (i + 3 < end) v.w = a[i + 3];
+  return v;
+}
 
 // Free pages among refs [lo, hi).
 SI_DEV int count_free(const int32_t* refs, int64_t lo, int64_t hi, int* sh) {
   int c = 0;
-  for (int64_t i = lo + threadIdx.x; i < hi; i += kThreads) c += refs[i] == 0;
+  for (int64_t i = lo + 4 * threadIdx.x; i < hi; i += 4 * kThreads) {
+    const int4 v = four(refs, i, hi, 1);
+    c += (v.x == 0) + (v.y == 0) + (v.z == 0) + (v.w == 0);
+  }
   return cta_sum(c, sh);
 }
 
@@ -85,15 +129,20 @@ SI_DEV int count_free(const int32_t* refs, int64_t lo, int64_t hi, int* sh) {
 // below `need` go to order[rank] and get one holder.
 SI_DEV void take_free(int32_t* refs, int64_t lo, int64_t hi, int rank, int need, int32_t* order,
                       int* sh) {
-  for (int64_t at = lo; at < hi && rank < need; at += kThreads) {
-    const int64_t i = at + threadIdx.x;
-    const int f = i < hi && refs[i] == 0;
-    int n;
-    const int r = rank + cta_scan(f, sh, &n);
-    if (f && r < need) {
-      order[r] = (int32_t)i;
-      refs[i] = 1;
-    }
+  for (int64_t at = lo; at < hi && rank < need; at += 4 * kThreads) {
+    const int64_t i = at + 4 * threadIdx.x;
+    const int4 v = four(refs, i, hi, 1);
+    const int f[4] = {v.x == 0, v.y == 0, v.z == 0, v.w == 0};
+    int n, r = rank + cta_scan(f[0] + f[1] + f[2] + f[3], sh, &n);
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      if (f[e]) {
+        if (r < need) {
+          order[r] = (int32_t)(i + e);
+          refs[i + e] = 1;
+        }
+        ++r;
+      }
     rank += n;
   }
 }
@@ -108,14 +157,11 @@ SI_DEV int pages_of(int len, int page_shift, int width) {
 
 // ---------------------------------------------------------------- extend
 // Entries of the first ceil(len / page) of each row that hold no page get one.
-__global__ void __cluster_dims__(kClu, 1, 1) __launch_bounds__(kThreads)
-    k_pages_extend(const PagesParams p) {
-  __shared__ int sh[32];
-  __shared__ int x_want, x_free;
-  cg::cluster_group cl = cg::this_cluster();
-  const unsigned rank = cl.block_rank();
-  const int64_t r_lo = share(p.B, rank), r_hi = share(p.B, rank + 1);
-  const int64_t f_lo = share(p.n_pages, rank), f_hi = share(p.n_pages, rank + 1);
+template <int C>
+__global__ void __launch_bounds__(kThreads) k_pages_extend(const PagesParams p) {
+  __shared__ int sh[32], slot[2];
+  const Team<C> team;
+  const int64_t r_lo = team.from(p.B), r_hi = team.to(p.B);
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   // what this CTA's rows want: a warp a row
   int c = 0;
@@ -123,41 +169,42 @@ __global__ void __cluster_dims__(kClu, 1, 1) __launch_bounds__(kThreads)
     const int n = pages_of(p.lens[r], p.page_shift, p.width);
     for (int e = lane; e < n; e += 32) c += p.table[r * p.width + e] < 0;
   }
-  const int want = cta_sum(c, sh);
+  const int64_t f_lo = team.from(p.n_pages), f_hi = team.to(p.n_pages);
   const int nfree = count_free(p.refs, f_lo, f_hi, sh);
-  int want_before, want_all, free_before, free_all;
-  cluster_sums(cl, &x_want, want, &want_before, &want_all);
-  cluster_sums(cl, &x_free, nfree, &free_before, &free_all);
-  take_free(p.refs, f_lo, f_hi, free_before, want_all, p.order, sh);
-  __threadfence();
-  cl.sync();
-  // rows in order: each row's wants are a prefix sum over the CTA's rows
-  int at = want_before;
-  for (int64_t r0 = r_lo; r0 < r_hi; r0 += kThreads / 32) {
-    const int64_t r = r0 + warp;
-    int n = 0, cnt = 0;
-    if (r < r_hi) {
-      n = pages_of(p.lens[r], p.page_shift, p.width);
-      for (int e = lane; e < n; e += 32) cnt += p.table[r * p.width + e] < 0;
-    }
-    cnt = __reduce_add_sync(0xFFFFFFFFu, cnt);
-    int all;
-    int mine = at + cta_scan(lane == 0 ? cnt : 0, sh, &all);
-    mine = __shfl_sync(0xFFFFFFFFu, mine, 0);
-    if (cnt) {
-      for (int e0 = 0; e0 < n; e0 += 32) {
-        const int e = e0 + lane;
-        const bool w = e < n && p.table[r * p.width + e] < 0;
-        const uint32_t m = __ballot_sync(0xFFFFFFFFu, w);
-        const int k = mine + __popc(m & ((1u << lane) - 1u));
-        if (w && k < free_all) p.table[r * p.width + e] = __ldcg(p.order + k);
-        mine += __popc(m);
+  const int want = cta_sum(c, sh);
+  int before[2], all[2];
+  team.sums(slot, want, nfree, before, all);
+  if (team.rank == 0 && threadIdx.x == 0) *p.missing = max(0, all[0] - all[1]);
+  if (all[0] > 0) {
+    take_free(p.refs, f_lo, f_hi, before[1], all[0], p.order, sh);
+    team.sync();
+    // rows in order: each row's wants are a prefix sum over the CTA's rows
+    int at = before[0];
+    for (int64_t r0 = r_lo; r0 < r_hi; r0 += kThreads / 32) {
+      const int64_t r = r0 + warp;
+      int n = 0, cnt = 0;
+      if (r < r_hi) {
+        n = pages_of(p.lens[r], p.page_shift, p.width);
+        for (int e = lane; e < n; e += 32) cnt += p.table[r * p.width + e] < 0;
       }
+      cnt = __reduce_add_sync(0xFFFFFFFFu, cnt);
+      int sum;
+      int mine = at + cta_scan(lane == 0 ? cnt : 0, sh, &sum);
+      mine = __shfl_sync(0xFFFFFFFFu, mine, 0);
+      if (cnt) {
+        for (int e0 = 0; e0 < n; e0 += 32) {
+          const int e = e0 + lane;
+          const bool w = e < n && p.table[r * p.width + e] < 0;
+          const uint32_t m = __ballot_sync(0xFFFFFFFFu, w);
+          const int k = mine + __popc(m & ((1u << lane) - 1u));
+          if (w && k < all[1]) p.table[r * p.width + e] = __ldcg(p.order + k);
+          mine += __popc(m);
+        }
+      }
+      at += sum;
     }
-    at += all;
   }
-  if (rank == 0 && threadIdx.x == 0) *p.missing = want_all > free_all ? want_all - free_all : 0;
-  cl.sync();  // no CTA leaves while another reads its shared memory
+  if constexpr (C > 1) team.sync();  // no CTA leaves while another reads its shared memory
 }
 
 // ---------------------------------------------------------------- free
@@ -178,66 +225,63 @@ __global__ void __launch_bounds__(128) k_pages_free(const PagesParams p) {
 
 // ---------------------------------------------------------------- fork
 // Per child: pages shared with its parent, the page copied (or -1) and where to.
-__global__ void __cluster_dims__(kClu, 1, 1) __launch_bounds__(kThreads)
-    k_pages_fork_plan(const PagesParams p) {
-  __shared__ int sh[32];
-  __shared__ int x_need, x_free, x_bad;
-  cg::cluster_group cl = cg::this_cluster();
-  const unsigned rank = cl.block_rank();
-  const int64_t c_lo = share(p.n, rank), c_hi = share(p.n, rank + 1);
-  const int64_t f_lo = share(p.n_pages, rank), f_hi = share(p.n_pages, rank + 1);
+template <int C>
+__global__ void __launch_bounds__(kThreads) k_pages_fork_plan(const PagesParams p) {
+  __shared__ int sh[32], slot[4];
+  const Team<C> team;
+  const int64_t c_lo = team.from(p.n), c_hi = team.to(p.n);
+  const int64_t f_lo = team.from(p.n_pages), f_hi = team.to(p.n_pages);
   const int page = 1 << p.page_shift;
   // of several children on one row the first is made
   for (int64_t i = c_lo + threadIdx.x; i < c_hi; i += kThreads) {
     const int d = p.dst[i];
     if (d >= 0 && d < p.B) p.claim[d] = 0x7FFFFFFF;
   }
-  __threadfence();
-  cl.sync();
+  team.sync();
   for (int64_t i = c_lo + threadIdx.x; i < c_hi; i += kThreads) {
     const int d = p.dst[i];
     if (d >= 0 && d < p.B) atomicMin(p.claim + d, (int)i);
   }
   const int nfree = count_free(p.refs, f_lo, f_hi, sh);
-  __threadfence();
-  cl.sync();
+  team.sync();
   int need = 0;
   for (int64_t i = c_lo + threadIdx.x; i < c_hi; i += kThreads) {
     const int s = p.src[i], d = p.dst[i];
     ForkChild ch{-1, 0, -1, -1};
-    if (s >= 0 && s < p.B && d >= 0 && d < p.B && s != d && __ldcg(p.claim + d) == (int)i &&
-        p.lens[d] == 0 && p.table[(int64_t)d * p.width] < 0) {
-      const int len = p.lens[s];
-      const int full = len > 0 ? len >> p.page_shift : 0;
-      const bool part = len > 0 && (len & (page - 1)) != 0;
-      if (len >= 0 && full + (part ? 1 : 0) <= p.width) {
-        const int last = part ? p.table[(int64_t)s * p.width + full] : -1;
-        if (!part || (last >= 0 && last < p.n_pages)) {
-          ch = ForkChild{len, full, last, -1};
-          need += part;
+    if (s >= 0 && s < p.B && d >= 0 && d < p.B && s != d) {
+      // (asked for together)
+      const int claim = __ldcg(p.claim + d), d_len = p.lens[d], len = p.lens[s];
+      const int first = p.table[(int64_t)d * p.width];
+      if (claim == (int)i && d_len == 0 && first < 0 && len >= 0) {
+        const int full = len >> p.page_shift;
+        const bool part = (len & (page - 1)) != 0;
+        if (full + (part ? 1 : 0) <= p.width) {
+          const int last = part ? p.table[(int64_t)s * p.width + full] : -1;
+          if (!part || (last >= 0 && last < p.n_pages)) {
+            ch = ForkChild{len, full, last, -1};
+            need += part;
+          }
         }
       }
     }
     p.child[i] = ch;
   }
   need = cta_sum(need, sh);
-  int need_before, need_all, free_before, free_all;
-  cluster_sums(cl, &x_need, need, &need_before, &need_all);
-  cluster_sums(cl, &x_free, nfree, &free_before, &free_all);
-  take_free(p.refs, f_lo, f_hi, free_before, need_all, p.order, sh);
-  __threadfence();
-  cl.sync();
-  int bad = 0, at = need_before;
+  int before[2], all[2];
+  team.sums(slot, need, nfree, before, all);
+  take_free(p.refs, f_lo, f_hi, before[1], all[0], p.order, sh);
+  team.sync();
+  int bad = 0, at = before[0];
   for (int64_t i0 = c_lo; i0 < c_hi; i0 += kThreads) {
     const int64_t i = i0 + threadIdx.x;
     ForkChild ch{-1, 0, -1, -1};
     if (i < c_hi) ch = p.child[i];
-    int all;
-    const int k = at + cta_scan(ch.last >= 0, sh, &all);
-    at += all;
+    int sum;
+    const int k = at + cta_scan(ch.last >= 0, sh, &sum);
+    at += sum;
     if (i < c_hi) {
       if (ch.last >= 0) {
-        if (k < free_all)
+        if (k < all[1])
           ch.fresh = __ldcg(p.order + k);
         else
           ch = ForkChild{-1, 0, -1, -1};
@@ -247,10 +291,9 @@ __global__ void __cluster_dims__(kClu, 1, 1) __launch_bounds__(kThreads)
     }
   }
   bad = cta_sum(bad, sh);
-  int bad_before, bad_all;
-  cluster_sums(cl, &x_bad, bad, &bad_before, &bad_all);
-  if (rank == 0 && threadIdx.x == 0) *p.missing = bad_all;
-  cl.sync();
+  team.sums(slot + 2, bad, 0, before, all);
+  if (team.rank == 0 && threadIdx.x == 0) *p.missing = all[0];
+  if constexpr (C > 1) team.sync();
 }
 
 // One CTA per child and slice of the copied page; slice 0 writes the table row.
@@ -292,46 +335,49 @@ __global__ void __launch_bounds__(256) k_pages_fork_apply(const PagesParams p, i
 // pages from L on (movers, ascending).  lr[p]: live pages before p, as ~lr for
 // a free page; hole[h]: the h-th hole; mover[r], mref[r]: the page that r live
 // pages precede, and its count, for pages from L on.
-__global__ void __cluster_dims__(kClu, 1, 1) __launch_bounds__(kThreads)
-    k_pages_compact_plan(const PagesParams p) {
-  __shared__ int sh[32];
-  __shared__ int x_live, x_hole;
-  cg::cluster_group cl = cg::this_cluster();
-  const unsigned rank = cl.block_rank();
-  const int64_t lo = share(p.n_pages, rank), hi = share(p.n_pages, rank + 1);
+template <int C>
+__global__ void __launch_bounds__(kThreads) k_pages_compact_plan(const PagesParams p) {
+  __shared__ int sh[32], slot[4];
+  const Team<C> team;
+  const int64_t lo = team.from(p.n_pages), hi = team.to(p.n_pages);
   int c = 0;
-  for (int64_t i = lo + threadIdx.x; i < hi; i += kThreads) c += p.refs[i] > 0;
-  const int live = cta_sum(c, sh);
-  int before, L;
-  cluster_sums(cl, &x_live, live, &before, &L);
-  int holes = 0;
-  for (int64_t at = lo; at < hi; at += kThreads) {
-    const int64_t i = at + threadIdx.x;
-    const int ref = i < hi ? p.refs[i] : 0;
-    const int f = ref > 0;
-    int n;
-    const int r = before + cta_scan(f, sh, &n);
-    before += n;
-    if (i < hi) {
-      p.lr[i] = f ? r : ~r;
-      if (i < L && !f) {
-        p.hole[i - r] = (int32_t)i;
+  for (int64_t i = lo + 4 * threadIdx.x; i < hi; i += 4 * kThreads) {
+    const int4 v = four(p.refs, i, hi, 0);
+    c += (v.x > 0) + (v.y > 0) + (v.z > 0) + (v.w > 0);
+  }
+  int before[2], all[2];
+  team.sums(slot, cta_sum(c, sh), 0, before, all);
+  const int L = all[0];
+  int rank = before[0], holes = 0;
+  for (int64_t at = lo; at < hi; at += 4 * kThreads) {
+    const int64_t i = at + 4 * threadIdx.x;
+    const int4 v = four(p.refs, i, hi, 0);
+    const int ref[4] = {v.x, v.y, v.z, v.w};
+    int n, r = rank + cta_scan((v.x > 0) + (v.y > 0) + (v.z > 0) + (v.w > 0), sh, &n);
+    rank += n;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const int64_t pg = i + e;
+      if (pg >= hi) break;
+      const bool f = ref[e] > 0;
+      p.lr[pg] = f ? r : ~r;
+      if (pg < L && !f) {
+        p.hole[pg - r] = (int32_t)pg;
         ++holes;
       }
-      if (i >= L && f) {
-        p.mover[r] = (int32_t)i;
-        p.mref[r] = ref;
+      if (pg >= L && f) {
+        p.mover[r] = (int32_t)pg;
+        p.mref[r] = ref[e];
       }
+      r += f;
     }
   }
-  holes = cta_sum(holes, sh);
-  int b, M;
-  cluster_sums(cl, &x_hole, holes, &b, &M);
-  if (rank == 0 && threadIdx.x == 0) {
+  team.sums(slot + 2, cta_sum(holes, sh), 0, before, all);
+  if (team.rank == 0 && threadIdx.x == 0) {
     p.missing[0] = L;
-    p.moves[0] = M;
+    p.moves[0] = all[0];
   }
-  cl.sync();
+  if constexpr (C > 1) team.sync();
 }
 
 // Copies the movers, writes the new counts and renames the table's pages.
@@ -371,9 +417,29 @@ __global__ void __launch_bounds__(256) k_pages_compact_apply(const PagesParams p
 }
 
 // ---------------------------------------------------------------- launches
+// One CTA for up to so many pages (and four times as many table entries): four
+// rounds of its threads.  A cluster's barriers cost about a microsecond each.
+constexpr int kOneCta = 4 * 4 * kThreads;
+
+template <class K>
+static cudaError_t launch_team(K one, K many, bool small, const PagesParams& p,
+                               cudaStream_t stream) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(small ? 1 : kClu);
+  cfg.blockDim = dim3(kThreads);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr{};
+  attr.id = cudaLaunchAttributeClusterDimension;
+  attr.val.clusterDim.x = kClu;
+  attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = small ? 0 : 1;
+  return cudaLaunchKernelEx(&cfg, small ? one : many, p);
+}
+
 cudaError_t launch_pages_extend(const PagesParams& p, cudaStream_t stream) {
-  k_pages_extend<<<kClu, kThreads, 0, stream>>>(p);
-  return cudaGetLastError();
+  const bool small = p.n_pages <= kOneCta && (int64_t)p.B * p.width <= 4 * kOneCta;
+  return launch_team(k_pages_extend<1>, k_pages_extend<kClu>, small, p, stream);
 }
 
 cudaError_t launch_pages_free(const PagesParams& p, cudaStream_t stream) {
@@ -383,8 +449,9 @@ cudaError_t launch_pages_free(const PagesParams& p, cudaStream_t stream) {
 }
 
 cudaError_t launch_pages_fork(const PagesParams& p, cudaStream_t stream) {
-  k_pages_fork_plan<<<kClu, kThreads, 0, stream>>>(p);
-  cudaError_t e = cudaGetLastError();
+  const bool small = p.n_pages <= kOneCta && p.n <= 4 * kThreads;
+  const cudaError_t e =
+      launch_team(k_pages_fork_plan<1>, k_pages_fork_plan<kClu>, small, p, stream);
   if (e != cudaSuccess || p.n == 0) return e;
   const int slices = (int)((p.page_bytes + kSlice - 1) / kSlice);
   k_pages_fork_apply<<<(unsigned)((int64_t)p.n * slices), 256, 0, stream>>>(p, slices);
@@ -392,8 +459,8 @@ cudaError_t launch_pages_fork(const PagesParams& p, cudaStream_t stream) {
 }
 
 cudaError_t launch_pages_compact(const PagesParams& p, int sms, cudaStream_t stream) {
-  k_pages_compact_plan<<<kClu, kThreads, 0, stream>>>(p);
-  const cudaError_t e = cudaGetLastError();
+  const cudaError_t e = launch_team(k_pages_compact_plan<1>, k_pages_compact_plan<kClu>,
+                                    p.n_pages <= kOneCta, p, stream);
   if (e != cudaSuccess) return e;
   const int slices = (int)((p.page_bytes + kSlice - 1) / kSlice);
   k_pages_compact_apply<<<sms * 8, 256, 0, stream>>>(p, slices);
