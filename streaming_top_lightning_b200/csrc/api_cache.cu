@@ -76,8 +76,8 @@ int plan_rows(RowsParams* p, int64_t keys, bool cache4, bool even, int key_chunk
     const int64_t n = std::min<int64_t>(8, std::max<int64_t>(1, room / tiles));
     if (key_chunk == 0 && steps <= least) {
       p->share = kSplit;
-    } else if (key_chunk == 0 && even && 2 * tiles > sms && tiles <= room) {
-      p->share = kSplit;  // a CTA a tile fills the GPU
+    } else if (key_chunk == 0 && ((even && 2 * tiles > sms && tiles <= room) || tiles > 8 * room)) {
+      p->share = kSplit;  // a CTA a tile fills the GPU evenly, or many times over
     } else if (key_chunk == 0 && n > 1 && steps <= n * least * 2) {
       p->share = kCluster;
       chunk = std::max<int64_t>(least, (steps + n - 1) / n);

@@ -264,3 +264,150 @@ def test_a_layer_step():
             o, aw, _, _ = _cache.attend(qa.double().cpu().numpy()[r, 0, h], kk, vv, 128 ** -0.5)
             # two results of 2^-8 each for the probabilities and the rounding, joined in fp32
             assert np.all(np.abs(got[r, 0, h] - o) <= 2.0 ** -7 * aw * 1.01 + 1e-5)
+
+
+TILE_CASES = [
+    # B, S, T, H, Hk, D, page, window, sinks, topk
+    (1, 1, 40, 128, 1, 128, 16, 0, 0, 0),      # fewer keys than a block
+    (3, 1, 700, 64, 1, 64, 32, 0, 0, 0),       # a cluster joins the chunks
+    (2, 1, 1500, 200, 1, 128, 64, 0, 0, 0),    # two row tiles of a query
+    (1, 9, 600, 24, 3, 128, 16, 100, 61, 0),   # 72 rows, a window with sinks
+    (2, 50, 130, 8, 8, 64, 16, 0, 0, 0),       # a chunk of 50 queries, one head a group
+    (2, 2, 500, 128, 1, 128, 64, 0, 0, 300),   # listed entries
+]
+
+
+@pytest.mark.parametrize("B,S,T,H,Hk,D,page,window,sinks,topk", TILE_CASES)
+@pytest.mark.parametrize("chunk", [0, 128])
+def test_tiles_against_formula(B, S, T, H, Hk, D, page, window, sinks, topk, chunk):
+    """33 rows of a kv head and more: the 128-row tiles, with few and with many chunks of a tile's keys."""
+    c = Filled(B, T, Hk, D, page, seed=T, k_scale=2.0, v_scale=0.5)
+    q = queries(B, S, H, D, seed=T + 1)
+    g = np.random.default_rng(T)
+    lens = [T] + [int(x) for x in g.integers(0, T, B - 1)]
+    q_lens = [S] + [max(1, S - 1)] * (B - 1)
+    idx = see = None
+    if topk:
+        idx = g.integers(-1, T, (B, S, topk)).astype(np.int32)
+        see = lambda b, i: np.array([j for j in idx[b, i] if 0 <= j < lens[b]], int)  # noqa: E731
+    out, lse = attend(c, q, lens, q_lens, window, sinks, idx=idx, opts=stl.options(key_chunk=chunk) if chunk else None)
+    rows = {(b, i) for b in range(B) for i in {0, 1, S // 2, S - 1}}
+    check(c, q, window, sinks, lens, q_lens, out, lse, rows=rows, see=see)
+
+
+def test_tiles_one_cta():
+    """A single persistent CTA goes through every item."""
+    c = Filled(3, 200, 2, 128, 16, seed=21)
+    q = queries(3, 1, 80, 128, seed=22)
+    out, lse = attend(c, q, [200, 0, 131], [1, 1, 1], opts=stl.options(grid_ctas=1))
+    check(c, q, 0, 0, [200, 0, 131], [1, 1, 1], out, lse)
+
+
+@pytest.mark.parametrize("H,S", [(8, 1), (8, 4), (24, 1)])
+def test_many_ragged_sequences(H, S):
+    """Equal shares of the steps of many sequences, most of them short, some without a token."""
+    B, T, Hk, D, page = 90, 400, 2, 64, 16
+    c = Filled(B, T, Hk, D, page, seed=H)
+    q = queries(B, S, H, D, seed=S)
+    g = np.random.default_rng(5)
+    lens = [int(x) for x in g.choice([0, 1, 5, 33, 64, 399, 400], B)]
+    q_lens = [int(x) for x in g.integers(0, S + 1, B)]
+    for chunk in (0, 128):
+        out, lse = attend(c, q, lens, q_lens, opts=stl.options(key_chunk=chunk) if chunk else None)
+        check(c, q, 0, 0, lens, q_lens, out, lse)
+
+
+def test_same_bits_again():
+    c = Filled(5, 900, 2, 128, 32, seed=31)
+    lens = [900, 20, 555, 0, 431]
+    for H in (8, 80):
+        q = queries(5, 1, H, 128, seed=32)
+        first = attend(c, q, lens, [1] * 5)
+        for _ in range(3):
+            again = attend(c, q, lens, [1] * 5)
+            assert torch.equal(first[0], again[0]) and torch.equal(first[1], again[1])
+
+
+def test_two_streams_and_a_graph():
+    """Calls that overlap on two streams, and a captured decode step whose lengths grow in place."""
+    c = Filled(4, 640, 2, 128, 16, seed=41)
+    pages, table = c.on_gpu()
+    sets = []
+    for H in (8, 80):
+        q = queries(4, 1, H, 128, seed=H)
+        want = stl.cache4_attention(q, pages, table, dev([640, 100, 333, 1]), 2, 16)
+        sets.append((q, want))
+    streams = [torch.cuda.Stream() for _ in sets]
+    lens = dev([640, 100, 333, 1])
+    torch.cuda.synchronize()
+    for _ in range(5):
+        got = [stl.cache4_attention(q, pages, table, lens, 2, 16, stream=s) for (q, _), s in zip(sets, streams)]
+        torch.cuda.synchronize()
+        for (_, want), have in zip(sets, got):
+            assert torch.equal(want[0], have[0]) and torch.equal(want[1], have[1])
+    for q, _ in sets:
+        n = dev([639, 99, 332, 1])
+        out, lse = torch.zeros_like(q), torch.zeros(q.shape[:3], device="cuda")
+        stl.cache4_attention(q, pages, table, n, 2, 16, out=out, lse=lse)
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            stl.cache4_attention(q, pages, table, n, 2, 16, out=out, lse=lse)
+        for lens_now in ([640, 100, 333, 1], [17, 640, 0, 500]):
+            n.copy_(dev(lens_now))
+            graph.replay()
+            want = stl.cache4_attention(q, pages, table, dev(lens_now), 2, 16)
+            torch.cuda.synchronize()
+            assert torch.equal(out, want[0]) and torch.equal(lse, want[1])
+
+
+def test_pools_beyond_four_gigabytes():
+    """Pages whose offsets pass 32 bits: written, read back and attended to like the first ones."""
+    heads, dim, page = 8, 128, 64
+    n = (5 << 30) // stl.cache4_page_bytes(heads, dim, page)
+    pages = torch.zeros((n, stl.cache4_page_bytes(heads, dim, page)), dtype=torch.uint8, device="cuda")
+    g = torch.Generator().manual_seed(50)
+    k, v = (torch.randn((1, 100, heads, dim), generator=g).to(torch.bfloat16).cuda() for _ in range(2))
+    results = []
+    for table in ([[3, 1]], [[n - 1, n - 7]]):
+        t, lens = dev(table), dev([100])
+        stl.cache4_append(k, v, pages, t, lens, page)
+        back = stl.cache4_read(pages, t, lens, 100, heads, dim, page)
+        att = [stl.cache4_attention(queries(1, 1, H, dim, seed=H), pages, t, lens, heads, page) for H in (16, 320)]
+        results.append([*back, *[x for a in att for x in a]])
+    for a, b in zip(*results):
+        assert torch.equal(a, b)
+    refs = torch.zeros(n, dtype=torch.int32, device="cuda")
+    refs[[n - 1, n - 7]] = 1
+    table, refs2, live = stl.cache_compact(pages, refs, dev([[n - 1, n - 7]]))
+    assert live.item() == 2 and table.tolist() == [[1, 0]] and refs2[:2].tolist() == [1, 1]
+    assert torch.equal(pages[0], pages[n - 7]) and torch.equal(pages[1], pages[n - 1])
+
+
+def test_python_refusals():
+    c = Filled(2, 64, 2, 64, 16, seed=60)
+    pages, table = c.on_gpu()
+    lens = dev([64, 64])
+    q = queries(2, 1, 8, 64, seed=61)
+    ok = dict(qa=q, pages=pages, table=table, lens=lens, heads=2, page=16)
+    stl.cache4_attention(**ok)
+    for bad in (dict(qa=q.float()), dict(qa=q[0]), dict(qa=q.cpu()), dict(qa=None), dict(qa=torch.stack([q, q], -1)[..., 0]), dict(pages=pages[:, :-16]),
+                dict(pages=pages.int()), dict(table=table.long()), dict(table=table[:1]), dict(lens=lens.cpu()), dict(lens=lens[:1]),
+                dict(heads=4), dict(page=17), dict(q_lens=lens.float()), dict(idx=table), dict(out=q.float()), dict(lse=q),
+                dict(workspace=lens)):
+        with pytest.raises(ValueError):
+            stl.cache4_attention(**{**ok, **bad})
+    for bad in (dict(window=-1), dict(sinks=2), dict(k_scale=0.0), dict(scale=float("nan")), dict(idx=torch.zeros((2, 1, 2049), dtype=torch.int32,
+                                                                                                                 device="cuda"))):
+        with pytest.raises(stl.StreamIndexError):
+            stl.cache4_attention(**{**ok, **bad})
+    with pytest.raises(TypeError):
+        stl.cache4_attention(**{**ok, "heads": 2.5})
+    k = queries(2, 3, 2, 64, seed=62)
+    for bad in (dict(v=k[:1]), dict(k=k.half()), dict(table=table[0]), dict(page=3)):
+        with pytest.raises(ValueError):
+            stl.cache4_append(**{**dict(k=k, v=k, pages=pages, table=table, lens=lens, page=16), **bad})
+    with pytest.raises(ValueError):
+        stl.cache_fork(pages[:-1], torch.zeros(pages.shape[0], dtype=torch.int32, device="cuda"), table, lens, lens, lens, 16)
+    with pytest.raises(ValueError):
+        stl.cache_extend(torch.zeros(4, device="cuda"), table, lens, 16)

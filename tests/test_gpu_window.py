@@ -244,3 +244,49 @@ def test_tiles_agree_with_rows():
     assert (a[0].float() - b[0].float()).abs().max() <= 2.0 ** -6 * v.abs().max()
     assert (a[1] - b[1]).abs().max() <= 1e-4
     check(q, k, v, 333, 3, [600, 411], [90, 77], *b, rows={(0, 0), (0, 89), (1, 40), (1, 76)}, fill=None)
+
+
+def test_caches_beyond_four_gigabytes():
+    """Keys whose offsets pass 32 bits (elements and bytes), by both kernels."""
+    T, Hk, D = 600_000, 32, 128
+    k = torch.zeros((1, T, Hk, D), dtype=torch.bfloat16, device="cuda")
+    v = torch.zeros_like(k)
+    n = 512  # the two calls then cut the keys into the same steps
+    _, ks, vs = inputs(1, 40, n, 32, Hk, D, seed=70)
+    k[:, T - n:], v[:, T - n:] = ks, vs
+    for S in (1, 40, 300):
+        q = inputs(1, S, n, 32, Hk, D, seed=S)[0]
+        a = stl.window_attention(q, k, v, 100, 0)
+        b = stl.window_attention(q, ks, vs, 100, 0)
+        assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+
+
+def test_tiles_few_ctas_and_a_graph():
+    q, k, v = inputs(2, 200, 300, 8, 2, 128, seed=71)
+    lens = torch.tensor([300, 250], dtype=torch.int32, device="cuda")
+    want = stl.window_attention(q, k, v, 64, 4, lens=lens)
+    got = stl.window_attention(q, k, v, 64, 4, lens=lens, opts=stl.options(grid_ctas=3))
+    assert torch.equal(want[0], got[0]) and torch.equal(want[1], got[1])
+    out, lse = torch.zeros_like(q), torch.zeros(q.shape[:3], device="cuda")
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        stl.window_attention(q, k, v, 64, 4, lens=lens, out=out, lse=lse)
+    for now in ([300, 250], [200, 300], [7, 0]):
+        lens.copy_(torch.tensor(now, dtype=torch.int32))
+        graph.replay()
+        want = stl.window_attention(q, k, v, 64, 4, lens=lens)
+        torch.cuda.synchronize()
+        assert torch.equal(out, want[0]) and torch.equal(lse, want[1])
+
+
+def test_python_refusals():
+    q, k, v = inputs(1, 2, 50, 4, 2, 64, seed=72)
+    for bad in (dict(qa=q.float()), dict(ka=k[0]), dict(va=v[:, :-1]), dict(qa=q.cpu()), dict(ka=k.transpose(1, 2)), dict(lens=q),
+                dict(lens=torch.zeros(1, dtype=torch.int32)), dict(q_lens=torch.zeros(2, dtype=torch.int32, device="cuda")), dict(out=q.float()),
+                dict(va=None)):
+        with pytest.raises(ValueError):
+            stl.window_attention(**{**dict(qa=q, ka=k, va=v, window=8), **bad})
+    for bad in (dict(window=0), dict(sinks=-1), dict(scale=-2.0), dict(qa=inputs(1, 2, 50, 3, 2, 64, seed=1)[0])):
+        with pytest.raises(stl.StreamIndexError):
+            stl.window_attention(**{**dict(qa=q, ka=k, va=v, window=8), **bad})
