@@ -28,7 +28,11 @@
 //                half of S's columns (the columns read by then), and the row's
 //                sum.  O is rescaled only when a row's maximum has grown by more
 //                than 2^16 since it was last fixed: bf16 and fp32 keep their
-//                relative precision up there, and the sum is over the same P's.
+//                relative precision up there.  The output is divided by the sum
+//                of the P's as rounded, so that a weight near one is not off by
+//                its rounding (error against 64 bits on rows with a few large
+//                logits: 0.0023 of the norm with the unrounded sum, which lse
+//                takes, 0.0016 being the output's own rounding).
 // Keys are taken from the first one that the pair of tiles sees, 128 at a time,
 // the last block and the sinks' block cut to multiples of 32 columns, so a
 // window costs about its own length and not whole tiles of it.  Only columns
@@ -48,7 +52,6 @@ constexpr int kM = 128;        // rows of a tile (MMA M)
 constexpr int kN = 64;         // keys of a block
 constexpr int kWinThreads = 384;
 constexpr int kSoftWarp = 4;   // softmax warps 4-7: tile 0, 8-11: tile 1
-constexpr int kPolyEvery = 4;  // every so many pairs of exponentials run as polynomials
 constexpr float kGrow = 16.0f; // log2 growth of a maximum that rescales O
 
 template <int D>
@@ -382,7 +385,8 @@ __global__ void __launch_bounds__(kWinThreads, 1)
       const int ta = it.first(i), tb = ta + nq - 1;
       const int t = ta + min(qi, nq - 1);
       // limit: the maximum that asks for a new m; nothing before the first block
-      float m = neg_inf(), limit = neg_inf(), l = 0.0f;
+      // l: the sum of the weights; lr: of the weights as P holds them
+      float m = neg_inf(), limit = neg_inf(), l = 0.0f, lr = 0.0f;
       const int from = i ? it.from[1] : it.from[0], to = i ? it.to[1] : it.to[0];
       const bool any = to > from;
       for (int n = from; n < it.blocks && any; ++n) {
@@ -444,6 +448,7 @@ __global__ void __launch_bounds__(kWinThreads, 1)
             }
             tc_fence_after();
             l *= a;
+            lr *= a;
 #pragma unroll 1
             for (int c = 0; c < D / 16; ++c) {
               uint32_t w[16];
@@ -466,34 +471,30 @@ __global__ void __launch_bounds__(kWinThreads, 1)
         }
         const float sub = m == neg_inf() ? 0.0f : -m;
         const uint64_t sl22 = pair2(sl2, sl2), sub2 = pair2(sub, sub);
-        uint64_t ls[2] = {0ull, 0ull};
+        uint64_t ls = 0ull, lsr = 0ull;
 #pragma unroll
         for (int c = 0; c < kN / 32; ++c) {
           if (c < chunks) {
             uint32_t w[16];
 #pragma unroll
             for (int e = 0; e < 32; e += 2) {
-              uint64_t xy = fma2(pair2(v[c][e], v[c][e + 1]), sl22, sub2);
               float x, y;
-              // part of the exponentials go through the FMA units
-              if ((e >> 1) % kPolyEvery == kPolyEvery - 1) {
-                xy = ex2_poly2(xy);
-                unpair2(xy, x, y);
-              } else {
-                unpair2(xy, x, y);
-                x = ex2(x);
-                y = ex2(y);
-                xy = pair2(x, y);
-              }
-              ls[(e >> 1) & 1] = add2(ls[(e >> 1) & 1], xy);
-              w[e >> 1] = pack_bf16x2(x, y);
+              unpair2(fma2(pair2(v[c][e], v[c][e + 1]), sl22, sub2), x, y);
+              x = ex2(x);
+              y = ex2(y);
+              const uint32_t both = pack_bf16x2(x, y);
+              w[e >> 1] = both;
+              ls = add2(ls, pair2(x, y));
+              lsr = add2(lsr, pair2(bf16_lo(both), bf16_hi(both)));
             }
             tmem_st16(b_col + c * 16, w);
           }
         }
         float l0, l1;
-        unpair2(add2(ls[0], ls[1]), l0, l1);
+        unpair2(ls, l0, l1);
         l += l0 + l1;
+        unpair2(lsr, l0, l1);
+        lr += l0 + l1;
         tmem_st_wait();
         tc_fence_before();
         mbar_arrive(smem_u32(&cs->p_ready[i][buf]));
@@ -508,7 +509,7 @@ __global__ void __launch_bounds__(kWinThreads, 1)
       if (any) {
         if (!mbar_wait_warp(smem_u32(&cs->pv_done[i][last]), ((npv >> last) & 1u) ^ 1u, ctl)) break;
         tc_fence_after();
-        const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+        const float inv = l == 0.0f ? 0.0f : 1.0f / lr;
         int64_t row_of[4];  // rows of this lane's group of four, -1: not live
 #pragma unroll
         for (int e = 0; e < 4; ++e)

@@ -117,30 +117,6 @@ SI_DEV float max3_nan(float a, float b, float c) {
   asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
   return r;
 }
-// 2^x of two numbers without the special function unit: x = n + f with
-// |f| <= 1/2 (adding 1.5 * 2^23 rounds to a whole n and leaves it in the low
-// bits), 2^f by a polynomial with p(0) = 1 fitted to the least largest relative
-// error (1.6e-7 in fp32), and n added to its exponent.  Below -127, and for
-// -inf, the result is 0; x is at most 100.
-SI_DEV uint64_t ex2_poly2(uint64_t x) {
-  float a, b;
-  unpair2(x, a, b);
-  x = pair2(fmaxf(a, -127.0f), fmaxf(b, -127.0f));
-  const uint64_t t = add2(x, pair2(12582912.0f, 12582912.0f));
-  const uint64_t n = add2(t, pair2(-12582912.0f, -12582912.0f));
-  const uint64_t f = fma2(n, pair2(-1.0f, -1.0f), x);
-  uint64_t q = fma2(f, pair2(0.0013264727f, 0.0013264727f), pair2(0.0096715126f, 0.0096715126f));
-  q = fma2(q, f, pair2(0.055507337f, 0.055507337f));
-  q = fma2(q, f, pair2(0.24022242f, 0.24022242f));
-  q = fma2(q, f, pair2(0.69314698f, 0.69314698f));
-  q = fma2(q, f, pair2(1.0f, 1.0f));
-  float ta, tb, qa, qb;
-  unpair2(t, ta, tb);
-  unpair2(q, qa, qb);
-  return pair2(__uint_as_float(__float_as_uint(qa) + (__float_as_uint(ta) << 23)),
-               __uint_as_float(__float_as_uint(qb) + (__float_as_uint(tb) << 23)));
-}
-
 // D (+)= A B, 16 x 8 x 16, fp32 accumulation.
 SI_DEV void mma_f16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
   asm volatile(
