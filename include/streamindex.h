@@ -362,7 +362,8 @@ int si_sparse_attention(const void* qa, const void* ka, const void* va, const in
  * d in {64, 128} (SI_ERR_DIM); window >= 1, sinks >= 0, scale finite and >= 0
  * (SI_ERR_OPTIONS); tensors 16-byte aligned, lens, q_lens and lse 4-byte.
  * Options: key_chunk > 0 makes the CTAs of few rows share the keys, at least
- * that many each (0: the library's choice); timeout_ms; grid_ctas.
+ * that many each (0: the library's choice); timeout_ms; grid_ctas; debug_flags
+ * (calls whose rows fill 128-row tiles).
  * Workspace: caller-provided, at least si_window_attention_workspace_size
  * bytes (partial results of rows whose keys several CTAs share; 0 if none).
  */

@@ -310,6 +310,7 @@ int si_window_attention(const void* qa, const void* ka, const void* va, const in
   w.scale_log2 = std::max(p.scale_log2, FLT_MIN);  // times -inf for an unseen key: not NaN
   w.err = dev->err;
   w.timeout_ns = (uint64_t)o.timeout_ms * 1000000ull;
+  w.debug_flags = o.debug_flags;
   CUtensorMap tm_q, tm_k, tm_v;
   if ((rc = make_map4(&tm_q, qa, d, H, S, B, p.G, w.QT)) ||
       (rc = make_map4(&tm_k, ka, d, H_k, T, B, 1, 32)) ||
@@ -417,6 +418,7 @@ int si_cache4_attention(const void* qa, const void* pages, int n_pages, const in
   p.lse = lse;
   p.scale_log2 = scale * k_scale * 1.4426950408889634f;
   p.v_scale = v_scale;
+  p.debug_flags = o.debug_flags;
   if (p.row_tile < 128)
     return status(launch_attn_rows(p, d, static_cast<cudaStream_t>(stream)));
   if (cache4_tiles_smem(d) > (size_t)dev->max_smem) return SI_ERR_UNSUPPORTED;

@@ -27,7 +27,8 @@
 // grown by more than 2^5 since it was last fixed; with the scale of 2^10 a
 // probability then stays below fp16's largest number.
 // Registers: the softmax threads take what the producers and MMA warps leave.
-// Every wait is bounded; a CTA that gives up records the error word and leaves.
+// Every wait is bounded; a CTA that gives up records the error word, lets its
+// MMAs end, still meets its cluster, and leaves.
 #include <cooperative_groups.h>
 
 #include "si_attn.cuh"
@@ -56,6 +57,7 @@ struct TileCtl {
   uint64_t kv_full[2][kSlots], kv_empty[2][kSlots];
   uint64_t s_full[2][2], p_ready[2][2], pv_done[2][2];
   uint64_t q_full, q_empty, ml_full, o_free;
+  uint64_t idle[2];               // a CTA that gives up: its MMAs are done
   uint64_t mask[2][kSlots];       // keys of a block that are there
   float factor[kM];               // 2^-x of the rows scaled by 2^x
   float xm[2][kM], xl[2][kM];     // the pipelines' maxima and sums
@@ -132,6 +134,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_cache4_tiles(const __grid_const
     mbar_init(smem_u32(&cs->q_empty), 2);
     mbar_init(smem_u32(&cs->ml_full), 2 * kM);
     mbar_init(smem_u32(&cs->o_free), 2 * kM);
+    mbar_init(smem_u32(&cs->idle[0]), 1);
+    mbar_init(smem_u32(&cs->idle[1]), 1);
     cs->abort = 0u;
     mbar_fence_init();
   }
@@ -211,6 +215,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_cache4_tiles(const __grid_const
           }
         }
       }
+      if (*ctl.abort) umma_drain(&cs->idle[i], leader);
     }
     stand_by(p);
   } else if (warp >= 8) {
@@ -318,7 +323,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_cache4_tiles(const __grid_const
         if (!is_v && lane == 0)
           reinterpret_cast<uint32_t*>(&cs->mask[i][slot])[warp & 1] = m;
         fence_async();
-        mbar_arrive(smem_u32(&cs->kv_full[i][slot]));
+        if (!((p.debug_flags & 1) && n == 0)) mbar_arrive(smem_u32(&cs->kv_full[i][slot]));
         if (++slot == (uint32_t)kSlots) slot = 0, phase ^= 1u;
       }
     }

@@ -42,7 +42,7 @@
 // NaN; a row that comes out NaN is computed again by the formula
 // (exact_row_keys), so what a row does not see does not reach it.
 // Every wait is bounded; a CTA that gives up records the error word, lets its
-// copies land and leaves.
+// copies and MMAs end and leaves.
 #include "si_attn.cuh"
 
 namespace si {
@@ -66,6 +66,7 @@ struct WinCfg {
 
 struct WinCtl {
   uint64_t kv_full[12], kv_empty[12], kv_land;
+  uint64_t idle[2];  // a CTA that gives up: its MMAs are done
   uint64_t q_full, q_empty, s_full[2][2], p_ready[2][2], pv_done[2][2];  // [tile][buffer]
   uint32_t tmem_base;
   uint32_t abort;
@@ -166,6 +167,8 @@ __global__ void __launch_bounds__(kWinThreads, 1)
       mbar_init(smem_u32(&cs->kv_full[i]), 1);
       mbar_init(smem_u32(&cs->kv_empty[i]), 2);  // both MMA warps
     }
+    mbar_init(smem_u32(&cs->idle[0]), 1);
+    mbar_init(smem_u32(&cs->idle[1]), 1);
     mbar_init(smem_u32(&cs->kv_land), 1);
     mbar_init(smem_u32(&cs->q_full), 1);
     mbar_init(smem_u32(&cs->q_empty), 2);
@@ -211,7 +214,7 @@ __global__ void __launch_bounds__(kWinThreads, 1)
         const uint32_t bar = smem_u32(mend ? &cs->kv_land : &cs->kv_full[slot]);
         if (lane == 0) {
           mbar_arrive_expect_tx(bar, (uint32_t)cols * D * 2);
-          for (int c = 0; c < cols; c += 32)
+          for (int c = (p.debug_flags & 1) && at == 0 ? cols : 0; c < cols; c += 32)
 #pragma unroll
             for (int h = 0; h < D / 64; ++h)
               tma_load_4d(dst + h * C::kHalf + c * 128, is_v ? &tm_v : &tm_k, bar, 64 * h, it.hk,
@@ -364,6 +367,7 @@ __global__ void __launch_bounds__(kWinThreads, 1)
         }
       }
     }
+    if (*ctl.abort) umma_drain(&cs->idle[i], leader);
   } else if (warp >= kSoftWarp) {
     // ------------------------------------------------------------ softmax
     const int i = (warp - kSoftWarp) >> 2;

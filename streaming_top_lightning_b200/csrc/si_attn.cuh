@@ -284,6 +284,18 @@ SI_DEV bool elect_one() {
   return r != 0u;
 }
 
+// Waits, at most a millisecond, for the MMAs issued so far (a CTA that gives up
+// frees its TMEM only then).  By the warp that issued them.
+SI_DEV void umma_drain(uint64_t* bar, bool leader) {
+  if (leader) {
+    umma_commit(smem_u32(bar));
+    const uint64_t end = globaltimer() + 1000000ull;
+    while (!mbar_try_wait(smem_u32(bar), 0u) && globaltimer() < end) {
+    }
+  }
+  __syncwarp();
+}
+
 // Transposes the 4 x 4 pieces of four neighbouring lanes: lane q's piece e
 // becomes lane e's piece q.
 SI_DEV uint4 shfl_xor4(uint4 x, int m) {

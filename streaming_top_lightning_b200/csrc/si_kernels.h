@@ -138,6 +138,7 @@ struct RowsParams {
   float2* part_ml;     // [B*Hk*S*G, splits] (maximum in log2 units, sum)
   int64_t* tile_start; // kShared: [B*Hk*tiles] where a tile's steps begin
   int64_t* share_out;  // kShared: steps of a CTA
+  int debug_flags;     // 128-row tiles, bit 0: no first block (timeout test)
 };
 // CTAs of a tile width that an SM holds.
 int attn_rows_ctas(int D, bool cache4, int row_tile);
@@ -163,6 +164,7 @@ struct WinParams {
   float scale_log2;
   uint32_t* err;
   uint64_t timeout_ns;
+  int debug_flags;            // bit 0: the first K block is never loaded (timeout test)
 };
 size_t window_tiles_smem(int D);
 cudaError_t launch_window_tiles(const CUtensorMap& tm_q, const CUtensorMap& tm_k,
