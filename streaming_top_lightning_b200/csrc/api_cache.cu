@@ -33,14 +33,14 @@ int check_attention(int B, int S, int H, int H_k, int d) {
 
 // The plan over a call's keys: the tile width (the narrowest of 8, 16 and 32
 // rows that holds a kv head's rows, so that keys are read once; over a 4-bit
-// cache 128-row tensor-core tiles from 33 rows on), how the CTAs share the
+// cache 128-row tensor-core tiles from 17 rows on), how the CTAs share the
 // tiles' keys, and the bytes of partial results.  keys: what one query may see
 // at most; even: that all sequences are likely to see as many.
 int plan_rows(RowsParams* p, int64_t keys, bool cache4, bool even, int key_chunk, int sms, int d,
               size_t* bytes) {
   const bool listed = p->topk > 0;
   const int64_t rows = listed ? p->G : std::min<int64_t>((int64_t)p->S * p->G, 1 << 20);
-  p->row_tile = rows <= 8 ? 8 : rows <= 16 ? 16 : (rows <= 32 || !cache4) ? 32 : 128;
+  p->row_tile = rows <= 8 ? 8 : rows <= 16 ? 16 : cache4 ? 128 : 32;
   const int rt = p->row_tile;
   const int64_t per = listed ? (int64_t)p->S * ((p->G + rt - 1) / rt)
                              : ((int64_t)p->S * p->G + rt - 1) / rt;
@@ -120,14 +120,42 @@ int place_partials(RowsParams* p, int d, size_t need, void* ws, size_t ws_bytes)
 
 // Whether a window call runs in 128-row tensor-core tiles: from so many
 // (query, head) rows per kv head on, unless the caller fixed key chunks.
-constexpr int kTileRows = 64;
+constexpr int kTileRows = 17;
+// What a pair of tiles costs besides its blocks of 64 keys, and the join of
+// chunks of them, in blocks.
+constexpr int kItemBlocks = 6, kJoinBlocks = 20;
 bool window_in_tiles(int S, int G, int key_chunk) {
   return G <= 128 && (int64_t)S * G >= kTileRows && key_chunk == 0;
 }
 
+// How 128-row tiles share a pair's keys, and the bytes of partial results.
+int plan_window_tiles(const RowsParams& p, int sms, int d, WinParams* w, size_t* bytes) {
+  w->QT = 128 / p.G;
+  w->pairs = (int)(((int64_t)p.S + 2 * w->QT - 1) / (2 * w->QT));
+  const int64_t pairs = (int64_t)p.B * p.Hk * w->pairs;
+  // a pair's queries see a little more than one of them
+  const int64_t most = std::min<int64_t>(p.S, 2 * w->QT);
+  const int64_t blocks = (std::min<int64_t>(p.T, (int64_t)p.window + most - 1) + 63) / 64 +
+                         (std::min<int64_t>(p.sinks, p.T) + 63) / 64;
+  int64_t best = (pairs + sms - 1) / sms * (blocks + kItemBlocks);
+  w->splits = 1;
+  w->chunk = (int)blocks;
+  for (int64_t n = 2; n <= 32 && pairs * n <= 2 * sms; ++n) {
+    const int64_t c = (blocks + n - 1) / n, s = (blocks + c - 1) / c;
+    const int64_t cost = (pairs * s + sms - 1) / sms * (c + kItemBlocks) + kJoinBlocks;
+    if (cost < best) best = cost, w->chunk = (int)c, w->splits = (int)s;
+  }
+  w->items = pairs * w->splits;
+  if (w->items >= ((int64_t)1 << 31)) return SI_ERR_DIM;
+  const int64_t rows = (int64_t)p.B * p.S * p.H * w->splits;
+  *bytes = w->splits == 1 ? 0 : align256((size_t)rows * d * sizeof(float)) +
+                                    align256((size_t)rows * sizeof(float2));
+  return SI_OK;
+}
+
 // Sizes of a window call and its plan.
 int window_problem(int B, int S, int T, int H, int H_k, int d, int window, int sinks,
-                   const si_options* opt, RowsParams* p, Opts* o, size_t* bytes) {
+                   const si_options* opt, RowsParams* p, WinParams* w, Opts* o, size_t* bytes) {
   int rc = check_attention(B, S, H, H_k, d);
   if (rc) return rc;
   if (T < 1 || T >= (1 << 30) || (int64_t)B * T * H_k >= ((int64_t)1 << 31)) return SI_ERR_DIM;
@@ -136,10 +164,9 @@ int window_problem(int B, int S, int T, int H, int H_k, int d, int window, int s
   p->B = B, p->S = S, p->T = T, p->H = H, p->Hk = H_k, p->G = H / H_k;
   p->window = std::min(window, kWindowMax);
   p->sinks = std::min(sinks, kWindowMax);
-  *bytes = 0;
-  if (window_in_tiles(S, p->G, o->key_chunk)) return SI_OK;
   int max_smem = 0, sms = 0;
   plan_limits(&max_smem, &sms);
+  if (window_in_tiles(S, p->G, o->key_chunk)) return plan_window_tiles(*p, sms, d, w, bytes);
   return plan_rows(p, std::min<int64_t>(T, (int64_t)p->window + p->sinks), false, true,
                    o->key_chunk, sms, d, bytes);
 }
@@ -263,9 +290,10 @@ int si_window_attention_workspace_size(int B, int S, int T, int H, int H_k, int 
                                        int sinks, const si_options* opt, size_t* bytes) {
   if (!bytes) return SI_ERR_NULL;
   RowsParams p{};
+  WinParams w{};
   Opts o;
   size_t need = 0;
-  const int rc = window_problem(B, S, T, H, H_k, d, window, sinks, opt, &p, &o, &need);
+  const int rc = window_problem(B, S, T, H, H_k, d, window, sinks, opt, &p, &w, &o, &need);
   if (rc == SI_OK) *bytes = need;
   return rc;
 }
@@ -276,14 +304,17 @@ int si_window_attention(const void* qa, const void* ka, const void* va, const in
                         const si_options* opt, void* workspace, size_t ws_bytes, void* stream) {
   if (!qa || !ka || !va || !out) return SI_ERR_NULL;
   RowsParams p{};
+  WinParams w{};
   Opts o;
   size_t need = 0;
-  int rc = window_problem(B, S, T, H, H_k, d, window, sinks, opt, &p, &o, &need);
+  int rc = window_problem(B, S, T, H, H_k, d, window, sinks, opt, &p, &w, &o, &need);
   if (rc) return rc;
   if (!(scale >= 0.0f) || scale == INFINITY) return SI_ERR_OPTIONS;
   if (!aligned16(qa) || !aligned16(ka) || !aligned16(va) || !aligned16(out) || !aligned4(lens) ||
       !aligned4(q_lens) || !aligned4(lse))
     return SI_ERR_ALIGN;
+  const bool tiles = window_in_tiles(S, p.G, o.key_chunk);
+  p.splits = tiles ? w.splits : p.splits;
   if ((rc = place_partials(&p, d, need, workspace, ws_bytes))) return rc;
   DevInfo* dev;
   if ((rc = dev_info(&dev))) return rc;
@@ -296,16 +327,12 @@ int si_window_attention(const void* qa, const void* ka, const void* va, const in
   p.q_lens = q_lens;
   p.scale_log2 = scale * 1.4426950408889634f;
   p.v_scale = 1.0f;
-  if (!window_in_tiles(S, p.G, o.key_chunk))
-    return status(launch_attn_rows(p, d, static_cast<cudaStream_t>(stream)));
+  if (!tiles) return status(launch_attn_rows(p, d, static_cast<cudaStream_t>(stream)));
   if (window_tiles_smem(d) > (size_t)dev->max_smem) return SI_ERR_UNSUPPORTED;
-  WinParams w{};
   w.q = p.q, w.k = p.k, w.v = p.v, w.out = p.out, w.lse = lse;
   w.lens = lens, w.q_lens = q_lens;
   w.B = B, w.S = S, w.T = T, w.H = H, w.Hk = H_k, w.G = p.G;
-  w.QT = 128 / p.G;
-  w.pairs = (int)(((int64_t)S + 2 * w.QT - 1) / (2 * w.QT));
-  w.items = (int64_t)B * H_k * w.pairs;
+  w.part_o = p.part_o, w.part_ml = p.part_ml;
   w.window = p.window, w.sinks = p.sinks;
   w.scale_log2 = std::max(p.scale_log2, FLT_MIN);  // times -inf for an unseen key: not NaN
   w.err = dev->err;

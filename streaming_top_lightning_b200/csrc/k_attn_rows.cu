@@ -354,7 +354,7 @@ SI_DEV bool share_of(const RowsParams& p, Share& job) {
 
 // CTAs that an SM's registers hold.
 constexpr int row_ctas(int D, int MODE, int NT) {
-  return NT == 4 ? 2 : (D == 128 && MODE == 0 ? 2 : (NT == 1 ? 4 : 3));
+  return MODE == 0 && (D == 128 || NT == 4) ? 2 : (NT == 1 ? 4 : 3);
 }
 
 }  // namespace
@@ -969,9 +969,9 @@ cudaError_t launch(const RowsParams& p, cudaStream_t stream) {
 
 template <int D, int MODE>
 cudaError_t launch_nt(const RowsParams& p, cudaStream_t stream) {
-  return p.row_tile == 8    ? launch<D, MODE, 1>(p, stream)
-         : p.row_tile == 16 ? launch<D, MODE, 2>(p, stream)
-                            : launch<D, MODE, 4>(p, stream);
+  if constexpr (MODE == 0)
+    if (p.row_tile == 32) return launch<D, MODE, 4>(p, stream);
+  return p.row_tile == 8 ? launch<D, MODE, 1>(p, stream) : launch<D, MODE, 2>(p, stream);
 }
 
 }  // namespace

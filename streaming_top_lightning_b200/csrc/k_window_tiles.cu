@@ -87,18 +87,24 @@ struct WinItem {
   int len, q_len;
   int live, QT;      // live queries of the pair, queries of a full tile
   int t0;            // position of the first query
-  KeySpan span;      // of both tiles
+  KeySpan span;      // of both tiles, cut to the item's chunk of it
+  int sink_base;     // first sink of the chunk
+  int chunk, pieces; // the chunk, of so many that hold the pair's keys
   int blocks, win_blocks;
-  // the window blocks that each tile sees; both see the sinks (where there are
-  // blocks of them, every query of the pair lies behind them)
+  // the window blocks that each tile sees, and whether it sees the sinks' blocks
+  // (where there are any, every query of the pair lies behind them)
   int from[2], to[2];
+  bool sinks[2];
   // live queries of tile i (0: none) and the position of its first
   SI_DEV int nq(int i) const { return clampi(live - i * QT, 0, QT); }
   SI_DEV int first(int i) const { return t0 + i * QT; }
 };
 
+template <bool SPLIT>
 SI_DEV bool win_item(const WinParams& p, int id, WinItem& it) {
-  const int bh = id / p.pairs, pair = id - bh * p.pairs;
+  const int all = SPLIT ? p.pairs * p.splits : p.pairs, bh = id / all;
+  it.chunk = SPLIT ? (id - bh * all) / p.pairs : 0;
+  const int pair = id - bh * all - it.chunk * p.pairs;
   it.b = bh / p.Hk;
   it.hk = bh - it.b * p.Hk;
   it.i0 = pair * 2 * p.QT;
@@ -111,6 +117,8 @@ SI_DEV bool win_item(const WinParams& p, int id, WinItem& it) {
   it.span = key_span<1>(it.t0, it.t0 + it.live - 1, it.len, p.window, p.sinks);
   it.win_blocks = (it.span.end - it.span.base + kN - 1) / kN;
   it.blocks = it.win_blocks + (it.span.sink_end + kN - 1) / kN;
+  it.pieces = 1;
+  it.sink_base = 0;
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
     // first key of the tile's first query, last position of its last
@@ -118,14 +126,33 @@ SI_DEV bool win_item(const WinParams& p, int id, WinItem& it) {
     const int hi = min(it.span.end, it.first(i) + nq);
     it.from[i] = max(0, (p.sinks > it.span.base ? 0 : lo - it.span.base) / kN);
     it.to[i] = nq == 0 || hi <= 0 ? 0 : (hi - it.span.base + kN - 1) / kN;
+    it.sinks[i] = it.to[i] > 0 && it.span.sink_end > 0;
   }
-  return true;
+  if (SPLIT && it.blocks > p.chunk) {
+    it.pieces = (it.blocks + p.chunk - 1) / p.chunk;
+    // the window blocks of the chunk, then the sinks'
+    const int w0 = min(it.chunk * p.chunk, it.win_blocks), s0 = it.chunk * p.chunk - w0;
+    it.blocks = min(p.chunk, it.blocks - it.chunk * p.chunk);
+    it.win_blocks = min(it.blocks, it.win_blocks - w0);
+    it.span.base += w0 * kN;
+    it.span.end = min(it.span.end, it.span.base + it.win_blocks * kN);
+    it.sink_base = s0 * kN;
+    it.span.sink_end = min(it.span.sink_end, (s0 + it.blocks - it.win_blocks) * kN);
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      it.from[i] = clampi(it.from[i] - w0, 0, it.win_blocks);
+      it.to[i] = clampi(it.to[i] - w0, 0, it.win_blocks);
+      it.sinks[i] = it.sinks[i] && it.blocks > it.win_blocks;
+      if (it.to[i] <= it.from[i]) it.from[i] = it.to[i] = it.win_blocks;
+    }
+  }
+  return !SPLIT || it.chunk < it.pieces;
 }
 
 // First key of block n, the keys it holds, and its columns (a multiple of 32).
 // The sinks' blocks come last: the first maximum is then that of many keys.
 SI_DEV int block_key(const WinItem& it, int n) {
-  return n < it.win_blocks ? it.span.base + n * kN : (n - it.win_blocks) * kN;
+  return n < it.win_blocks ? it.span.base + n * kN : it.sink_base + (n - it.win_blocks) * kN;
 }
 SI_DEV int block_keys(const WinItem& it, int n) {
   return min(kN, (n < it.win_blocks ? it.span.end : it.span.sink_end) - block_key(it, n));
@@ -148,7 +175,8 @@ SI_DEV int ring_block(int blocks, int x, bool& is_v) {
 }
 }  // namespace
 
-template <int D>
+// SPLIT: chunks of a pair's keys are items of their own.
+template <int D, bool SPLIT>
 __global__ void __launch_bounds__(kWinThreads, 1)
     k_window_tiles(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                    const __grid_constant__ CUtensorMap tm_v, const WinParams p) {
@@ -198,7 +226,7 @@ __global__ void __launch_bounds__(kWinThreads, 1)
     bool ok = true;
     for (int id = blockIdx.x; ok && id < p.items; id += gridDim.x) {
       WinItem it;
-      if (!win_item(p, id, it)) continue;
+      if (!win_item<SPLIT>(p, id, it)) continue;
       for (int x = 0; ok && x < 2 * it.blocks; ++x, ++at) {
         bool is_v;
         const int n = ring_block(it.blocks, x, is_v);
@@ -256,7 +284,7 @@ __global__ void __launch_bounds__(kWinThreads, 1)
       uint32_t n = 0;
       for (int id = blockIdx.x; id < p.items; id += gridDim.x) {
         WinItem it;
-        if (!win_item(p, id, it) || it.blocks == 0) continue;
+        if (!win_item<SPLIT>(p, id, it) || it.blocks == 0) continue;
         if (!mbar_wait(smem_u32(&cs->q_empty), (n & 1u) ^ 1u, ctl)) break;
         ++n;
         const int tiles = it.live > p.QT ? 2 : 1;
@@ -294,14 +322,14 @@ __global__ void __launch_bounds__(kWinThreads, 1)
     bool ok = true;
     for (int id = blockIdx.x; ok && id < p.items; id += gridDim.x) {
       WinItem it;
-      if (!uniform(win_item(p, id, it))) continue;
+      if (!uniform(win_item<SPLIT>(p, id, it))) continue;
       const int blocks = uniform(it.blocks), wins = uniform(it.win_blocks);
       if (blocks == 0) continue;
       const int from = uniform(i ? it.from[1] : it.from[0]), to = uniform(i ? it.to[1] : it.to[0]);
       // columns of the last window block and the last of the sinks
-      const int win_cols = uniform(columns(it.span.end - it.span.base - (it.win_blocks - 1) * kN));
-      const int sink_cols =
-          uniform(columns(it.span.sink_end - (it.blocks - it.win_blocks - 1) * kN));
+      const int win_cols = uniform(columns(block_keys(it, it.win_blocks - 1)));
+      const int sink_cols = uniform(columns(block_keys(it, it.blocks - 1)));
+      const bool sinks = uniform(i ? it.sinks[1] : it.sinks[0]);
       if (!mbar_wait_warp(smem_u32(&cs->q_full), items & 1u, ctl)) break;
       ++items;
       uint32_t begun = 0u;
@@ -316,7 +344,7 @@ __global__ void __launch_bounds__(kWinThreads, 1)
         cols0 = cols1;
         cols1 = cols2;
         cols2 = m == wins - 1 ? win_cols : (m == blocks - 1 ? sink_cols : kN);
-        if (m < blocks && ((m >= from && m < to) || (m >= wins && to > 0))) see |= 4u;
+        if (m < blocks && ((m >= from && m < to) || (m >= wins && sinks))) see |= 4u;
         if (n >= 0) {
           if (!(ok = mbar_wait_warp(smem_u32(&cs->kv_full[slot]), phase, ctl))) break;
           if (see & 1u) {  // O += P V
@@ -383,7 +411,7 @@ __global__ void __launch_bounds__(kWinThreads, 1)
     bool stop = false;
     for (int id = blockIdx.x; !stop && id < p.items; id += gridDim.x) {
       WinItem it;
-      if (!win_item(p, id, it) || it.nq(i) == 0) continue;
+      if (!win_item<SPLIT>(p, id, it) || it.nq(i) == 0) continue;
       const int qi = row / p.G;  // query of the row within the tile
       const int nq = it.nq(i);
       const int ta = it.first(i), tb = ta + nq - 1;
@@ -392,7 +420,7 @@ __global__ void __launch_bounds__(kWinThreads, 1)
       // l: the sum of the weights; lr: of the weights as P holds them
       float m = neg_inf(), limit = neg_inf(), l = 0.0f, lr = 0.0f;
       const int from = i ? it.from[1] : it.from[0], to = i ? it.to[1] : it.to[0];
-      const bool any = to > from;
+      const bool any = to > from || (i ? it.sinks[1] : it.sinks[0]);
       for (int n = from; n < it.blocks && any; ++n) {
         if (n == to) {  // on to the sinks
           n = it.win_blocks;
@@ -509,11 +537,16 @@ __global__ void __launch_bounds__(kWinThreads, 1)
       const bool live = qi < nq;
       const int64_t orow =
           ((int64_t)it.b * p.S + it.i0 + i * p.QT + qi) * p.H + it.hk * p.G + row % p.G;
+      // a chunk of a row's keys: its place among the row's partial results
+      const bool whole = !SPLIT || it.pieces == 1;
+      const int64_t at = orow * p.splits + it.chunk;
       bool bad = false;
       if (any) {
         if (!mbar_wait_warp(smem_u32(&cs->pv_done[i][last]), ((npv >> last) & 1u) ^ 1u, ctl)) break;
         tc_fence_after();
-        const float inv = l == 0.0f ? 0.0f : 1.0f / lr;
+        // a chunk's sums are those of the weights before their rounding, which is
+        // what the join divides by
+        const float inv = l == 0.0f ? 0.0f : (whole ? 1.0f : l) / lr;
         int64_t row_of[4];  // rows of this lane's group of four, -1: not live
 #pragma unroll
         for (int e = 0; e < 4; ++e)
@@ -527,9 +560,18 @@ __global__ void __launch_bounds__(kWinThreads, 1)
           uint32_t w[16];
 #pragma unroll
           for (int e = 0; e < 32; e += 2) {
-            const float x = v[e] * inv, y = v[e + 1] * inv;
-            bad |= x != x || y != y;
-            w[e >> 1] = pack_bf16x2(x, y);
+            v[e] *= inv, v[e + 1] *= inv;
+            bad |= v[e] != v[e] || v[e + 1] != v[e + 1];
+            w[e >> 1] = pack_bf16x2(v[e], v[e + 1]);
+          }
+          if (!whole) {
+            if (live) {
+              float4* po = reinterpret_cast<float4*>(p.part_o + at * D + c * 32);
+#pragma unroll
+              for (int e = 0; e < 8; ++e)
+                po[e] = make_float4(v[4 * e], v[4 * e + 1], v[4 * e + 2], v[4 * e + 3]);
+            }
+            continue;
           }
           // four lanes exchange 16-byte pieces, so that a store writes 64
           // consecutive bytes of each of eight rows
@@ -546,11 +588,13 @@ __global__ void __launch_bounds__(kWinThreads, 1)
           }
         }
         tc_fence_before();
-      } else if (live) {
+      } else if (live && whole) {
         for (int c = 0; c < D / 8; ++c)
           reinterpret_cast<uint4*>(p.out + orow * D)[c] = make_uint4(0u, 0u, 0u, 0u);
       }
-      if (live && p.lse)
+      if (live && !whole)
+        p.part_ml[at] = make_float2(l == 0.0f ? neg_inf() : m, l);
+      else if (live && p.lse)
         p.lse[orow] = l == 0.0f ? neg_inf() : (m + log2f(l)) * 0.6931471805599453f;
       // rows by the formula (see the head of the file)
       __syncwarp();
@@ -568,8 +612,16 @@ __global__ void __launch_bounds__(kWinThreads, 1)
 #pragma unroll 1
         for (int part = 0; part < 2; ++part)
           exact_row_keys<D>(p.q + orr * D, p.k + first, p.v + first, stride,
-                            part ? it.span.base : 0, part ? it.span.end : it.span.sink_end, tr,
-                            it.len, p.window, p.sinks, sl2, lane, rm, rl, ro);
+                            part ? it.span.base : it.sink_base,
+                            part ? it.span.end : it.span.sink_end, tr, it.len, p.window, p.sinks,
+                            sl2, lane, rm, rl, ro);
+        if (!whole) {
+          const int64_t to = orr * p.splits + it.chunk;
+#pragma unroll
+          for (int e = 0; e < D / 32; ++e) p.part_o[to * D + lane * (D / 32) + e] = ro[e];
+          if (lane == 0) p.part_ml[to] = make_float2(rl == 0.0f ? neg_inf() : rm, rl);
+          continue;
+        }
         const float rinv = rl == 0.0f ? 0.0f : 1.0f / rl;
         uint32_t* dst = reinterpret_cast<uint32_t*>(p.out + orr * D) + lane * (D / 64);
 #pragma unroll
@@ -588,21 +640,66 @@ __global__ void __launch_bounds__(kWinThreads, 1)
   }
 }
 
+// Joins the chunks of a row, a warp a row; rows of one chunk are written already.
+template <int D>
+__global__ void __launch_bounds__(128) k_window_join(const WinParams p) {
+  constexpr int E = D / 32;
+  const int lane = threadIdx.x & 31, heads = p.G;
+  const int at = blockIdx.x * 4 + (threadIdx.x >> 5);  // B*S*H < 2^31
+  if (at >= p.B * p.S * p.H) return;
+  // (b, query, head) and the item that its pair of tiles is
+  const int head = at % p.H, bq = at / p.H, i = bq % p.S, b = bq / p.S;
+  WinItem it;
+  if (i >= seq_len(p.q_lens, b, p.S)) return;
+  if (!win_item<true>(p, (b * p.Hk + head / heads) * p.pairs * p.splits + i / (2 * p.QT), it) ||
+      it.pieces == 1)
+    return;
+  const int64_t first = (int64_t)at * p.splits;
+  float top = neg_inf();
+  for (int s = lane; s < it.pieces; s += 32) top = fmaxf(top, p.part_ml[first + s].x);
+#pragma unroll
+  for (int x = 16; x > 0; x >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, x));
+  float o[E], sum = 0.0f;
+#pragma unroll
+  for (int e = 0; e < E; ++e) o[e] = 0.0f;
+#pragma unroll 4
+  for (int s = 0; s < it.pieces; ++s) {
+    // a chunk without a key for the row has no sums
+    const float2 v = p.part_ml[first + s];
+    if (v.y == 0.0f) continue;
+    const float f = ex2(v.x - top);
+    sum = fmaf(v.y, f, sum);
+    const float* po = p.part_o + (first + s) * D + lane * E;
+#pragma unroll
+    for (int e = 0; e < E; ++e) o[e] = fmaf(po[e], f, o[e]);
+  }
+  const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+  uint32_t* dst = reinterpret_cast<uint32_t*>(p.out + (int64_t)at * D) + lane * (E / 2);
+#pragma unroll
+  for (int e = 0; e < E / 2; ++e) dst[e] = pack_bf16x2(o[2 * e] * inv, o[2 * e + 1] * inv);
+  if (lane == 0 && p.lse)
+    p.lse[at] = sum == 0.0f ? neg_inf() : (top + log2f(sum)) * 0.6931471805599453f;
+}
+
 size_t window_tiles_smem(int D) { return D == 128 ? WinCfg<128>::kSmem : WinCfg<64>::kSmem; }
 
 cudaError_t launch_window_tiles(const CUtensorMap& tm_q, const CUtensorMap& tm_k,
                                 const CUtensorMap& tm_v, const WinParams& p, int D, int grid,
                                 cudaStream_t stream) {
   const size_t smem = window_tiles_smem(D);
-  const void* fn = D == 128 ? reinterpret_cast<const void*>(k_window_tiles<128>)
-                            : reinterpret_cast<const void*>(k_window_tiles<64>);
+  const auto fn = p.splits > 1 ? (D == 128 ? k_window_tiles<128, true> : k_window_tiles<64, true>)
+                               : (D == 128 ? k_window_tiles<128, false> : k_window_tiles<64, false>);
   const cudaError_t e =
       cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;
-  if (D == 128)
-    k_window_tiles<128><<<grid, kWinThreads, smem, stream>>>(tm_q, tm_k, tm_v, p);
-  else
-    k_window_tiles<64><<<grid, kWinThreads, smem, stream>>>(tm_q, tm_k, tm_v, p);
+  fn<<<grid, kWinThreads, smem, stream>>>(tm_q, tm_k, tm_v, p);
+  if (p.splits > 1) {
+    const unsigned ctas = (unsigned)(((int64_t)p.B * p.S * p.H + 3) / 4);
+    if (D == 128)
+      k_window_join<128><<<ctas, 128, 0, stream>>>(p);
+    else
+      k_window_join<64><<<ctas, 128, 0, stream>>>(p);
+  }
   return cudaGetLastError();
 }
 

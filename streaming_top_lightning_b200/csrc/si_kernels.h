@@ -159,7 +159,10 @@ struct WinParams {
   int B, S, T, H, Hk, G;
   int QT;                     // queries of a 128-row tile: 128 / G
   int pairs;                  // pairs of tiles per batch and kv head
-  int64_t items;              // B * Hk * pairs
+  int splits, chunk;          // chunks of a pair's keys at most; blocks of 64 keys of a chunk
+  float* part_o;              // splits > 1: [B*S*H, splits, D] partial results
+  float2* part_ml;            // [B*S*H, splits] (maximum in log2 units, sum)
+  int64_t items;              // B * Hk * pairs * splits
   int window, sinks;
   float scale_log2;
   uint32_t* err;
