@@ -31,11 +31,29 @@ int check_attention(int B, int S, int H, int H_k, int d) {
   return SI_OK;
 }
 
-// The plan over a call's keys: the tile width (the narrowest of 8, 16 and 32
-// rows that holds a kv head's rows, so that keys are read once; over a 4-bit
-// cache 128-row tensor-core tiles from 17 rows on), how the CTAs share the
-// tiles' keys, and the bytes of partial results.  keys: what one query may see
-// at most; even: that all sequences are likely to see as many.
+// The plan over a call's keys: the tile width, how the CTAs share the tiles'
+// keys, and the bytes of partial results.  keys: what one query may see at
+// most; even: that all sequences are likely to see as many.
+//
+// Tile width: the narrowest of 8, 16 and 32 rows that holds a kv head's rows,
+// so that keys are read once; over a 4-bit cache 128-row tensor-core tiles from
+// 17 rows on.  (B200, one kv head's 32 rows and 64 of them at D = 128: 28.8 us in
+// 32-row tiles and 17 in 128-row ones for one sequence of 4,096 keys, 72.8 and
+// 63.6 for eight of 16,384, 76.7 and 51.4 for 32 of 4,096.  With 16 rows the
+// 16-row tiles take 20.7, 44.5 and 45.4.)
+//
+// Sharing, tiles below 128 rows:
+//  kSplit, a CTA a tile, where all tiles are resident at once, see as much, and
+//    the places left idle would save less than a join costs: 32 steps.  (32
+//    sequences, 8 kv heads, window 1,024: 25.4 us; 33.9 in equal shares, 37 in
+//    fixed chunks and a join.  12 such sequences, 96 tiles: window 512 13.3 us
+//    and 18.5 in shares, window 2,048 34.9 and 29.)  Also where tiles are many
+//    times the places.
+//  kCluster, a tile's chunks in one cluster that joins them, for calls of few
+//    steps whose clusters are all resident (three drafted tokens of four
+//    sequences: 13.9 us, with a join kernel 19.3; 32 ragged sequences of up to
+//    8,192 keys in clusters 81 us, in shares 58).
+//  kShared else: one wave of CTAs, each with an equal share of all steps.
 int plan_rows(RowsParams* p, int64_t keys, bool cache4, bool even, int key_chunk, int sms, int d,
               size_t* bytes) {
   const bool listed = p->topk > 0;
@@ -76,8 +94,10 @@ int plan_rows(RowsParams* p, int64_t keys, bool cache4, bool even, int key_chunk
     const int64_t n = std::min<int64_t>(8, std::max<int64_t>(1, room / tiles));
     if (key_chunk == 0 && steps <= least) {
       p->share = kSplit;
-    } else if (key_chunk == 0 && ((even && 2 * tiles > sms && tiles <= room) || tiles > 8 * room)) {
-      p->share = kSplit;  // a CTA a tile fills the GPU evenly, or many times over
+    } else if (key_chunk == 0 &&
+               ((even && 2 * tiles > sms && tiles <= room && steps * (room - tiles) <= 32 * room) ||
+                tiles > 8 * room)) {
+      p->share = kSplit;
     } else if (key_chunk == 0 && n > 1 && steps <= n * least * 2) {
       p->share = kCluster;
       chunk = std::max<int64_t>(least, (steps + n - 1) / n);
@@ -119,7 +139,10 @@ int place_partials(RowsParams* p, int d, size_t need, void* ws, size_t ws_bytes)
 }
 
 // Whether a window call runs in 128-row tensor-core tiles: from so many
-// (query, head) rows per kv head on, unless the caller fixed key chunks.
+// (query, head) rows per kv head on, unless the caller fixed key chunks.  (B200,
+// 8 heads a kv head, D = 128: 32 rows over a window of 512 take 22.7 us in 32-row
+// tiles and 14.5 in 128-row ones for one sequence, 37.2 and 26.5 for 64; 16 rows
+// 14.5 in 16-row tiles and 14.5, 19.2 and 26.2.)
 constexpr int kTileRows = 17;
 // What a pair of tiles costs besides its blocks of 64 keys, and the join of
 // chunks of them, in blocks.
@@ -128,7 +151,11 @@ bool window_in_tiles(int S, int G, int key_chunk) {
   return G <= 128 && (int64_t)S * G >= kTileRows && key_chunk == 0;
 }
 
-// How 128-row tiles share a pair's keys, and the bytes of partial results.
+// How 128-row tiles share a pair's keys, and the bytes of partial results: the
+// number of chunks that makes rounds of CTAs times a chunk's cost least.  (B200,
+// D = 64, 256 rows of each of two kv heads over 32,768 keys: 483 us whole, 37 in
+// chunks; D = 128, four kv heads, window 2,048: 40.2 and 26.3, window 512: 16.5
+// and 24.7, where the rule takes them whole.)
 int plan_window_tiles(const RowsParams& p, int sms, int d, WinParams* w, size_t* bytes) {
   w->QT = 128 / p.G;
   w->pairs = (int)(((int64_t)p.S + 2 * w->QT - 1) / (2 * w->QT));

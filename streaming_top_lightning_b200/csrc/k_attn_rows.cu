@@ -39,6 +39,13 @@
 // (2^-11 relative down to 2^-24 of the row's largest); the sum takes them
 // unrounded.
 //
+// Measured on B200 (D = 128): 32 sequences, 32 heads on 8 kv heads, a window of
+// 1,024 bf16 keys, 25.4 us, 5.3 TB/s; the same heads over ragged 4-bit caches of
+// up to 8,192 keys, 57 us, 2.7 TB/s of the 6.6 that a copy reaches: the warps'
+// instructions (about 800 for 32 keys: codes to fp16, products, transpositions)
+// take 59 % of the issue slots and half of the ALUs' time.  Five CTAs an SM with
+// two stages took 64 us, shares weighted by a CTA's start 60.
+//
 // bf16 keys: bf16 products, probabilities rounded to bf16 (2^-8).
 #include <cooperative_groups.h>
 
@@ -929,7 +936,9 @@ __global__ void __launch_bounds__(128) k_attn_join(const __grid_constant__ RowsP
 
 namespace {
 
-// Up to 24 chunks a warp takes a row, beyond that four.
+// Up to 24 chunks a warp takes a row, beyond that four.  (500 ragged sequences
+// of up to 1,024 keys, few pieces each: 62.9 us with one warp, 75 with four; one
+// sequence of 131,072 keys: 47.2 and 29.1.)
 template <int D, int KS, int RT, bool SHARED>
 cudaError_t launch_join(const RowsParams& p, cudaStream_t stream) {
   const int64_t rows = (int64_t)p.B * p.Hk * p.S * p.G;

@@ -1,5 +1,5 @@
 // Attention of many query rows over a 4-bit paged cache on the tensor cores:
-// 33 and more (query, head) rows of a kv head, as a layer has whose 128 heads
+// 17 and more (query, head) rows of a kv head, as a layer has whose 128 heads
 // share one key row.  Formula, key rule, number formats and roundings are those
 // of k_attn_rows.cu's 4-bit path.
 //
@@ -26,6 +26,12 @@
 // write into its ring.  O is rescaled when a row's maximum has
 // grown by more than 2^5 since it was last fixed; with the scale of 2^10 a
 // probability then stays below fp16's largest number.
+// Measured on B200: 64 queries of 128 heads over 2,048 listed entries each (one
+// kv head, D = 128) take 33 us, 261 TFLOP/s; in 32-row tiles 117, and 62 before
+// clusters joined the chunks.  8.6 GFLOP and 24 MB would take 5.2 us: with 16
+// blocks a pipeline most of the time goes into the page and entry loads before
+// the first block, the producers' conversions and the join.  Eight sequences of
+// 16,384 keys, 128 rows of each of 4 kv heads: 65 us.
 // Registers: the softmax threads take what the producers and MMA warps leave.
 // Every wait is bounded; a CTA that gives up records the error word, lets its
 // MMAs end, still meets its cluster, and leaves.

