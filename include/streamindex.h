@@ -359,8 +359,8 @@ int si_sparse_attention(const void* qa, const void* ka, const void* va, const in
  * probabilities rounded to bf16 for the weighted sum (2^-8 each), out rounded
  * once.  The same inputs and plan give the same bits.
  * Limits: B, S, T >= 1; T < 2^30; H a multiple of H_k; B*S*H, B*T*H_k < 2^31;
- * d in {64, 128} (SI_ERR_DIM); window >= 1, sinks >= 0, scale finite and >= 0
- * (SI_ERR_OPTIONS); tensors 16-byte aligned, lens, q_lens and lse 4-byte.
+ * d in {64, 128} (SI_ERR_DIM); window >= 1, sinks >= 0, scale >= 0 and, times
+ * log2(e), finite (SI_ERR_OPTIONS); tensors 16-byte aligned, lens, q_lens and lse 4-byte.
  * Options: key_chunk > 0 makes the CTAs of few rows share the keys, at least
  * that many each (0: the library's choice); timeout_ms; grid_ctas; debug_flags
  * (calls whose rows fill 128-row tiles).
@@ -428,7 +428,8 @@ int si_cache4_read(void* k, void* v, int B, int S, int H_k, int d, const void* p
  * with fp32 accumulation (a query row is scaled into fp16's range by a power
  * of two), softmax in fp32, the probabilities rounded to fp16 (2^-11).
  * Limits: H a multiple of H_k, B*S*H < 2^31, B*width < 2^31, topk <= 2048
- * when idx is given (SI_ERR_TOPK).
+ * when idx is given (SI_ERR_TOPK); scale * k_scale as si_window_attention's
+ * scale (SI_ERR_OPTIONS).
  */
 int si_cache4_attention(const void* qa, const void* pages, int n_pages, const int32_t* table,
                         int width, int page, const int32_t* lens, const int32_t* q_lens,

@@ -22,6 +22,9 @@ int page_shift_of(int page, int lo, int hi) {
   return s;
 }
 
+// Softmax scales, finite in log2 units too; false for NaN.
+bool scale_finite(float s) { return s >= 0.0f && s * 1.4426950408889634f <= FLT_MAX; }
+
 bool scale_ok(float g) { return g >= 0x1p-60f && g <= 0x1p60f; }  // false for NaN
 
 // Sizes that the two attention calls share.
@@ -336,7 +339,7 @@ int si_window_attention(const void* qa, const void* ka, const void* va, const in
   size_t need = 0;
   int rc = window_problem(B, S, T, H, H_k, d, window, sinks, opt, &p, &w, &o, &need);
   if (rc) return rc;
-  if (!(scale >= 0.0f) || scale == INFINITY) return SI_ERR_OPTIONS;
+  if (!scale_finite(scale)) return SI_ERR_OPTIONS;
   if (!aligned16(qa) || !aligned16(ka) || !aligned16(va) || !aligned16(out) || !aligned4(lens) ||
       !aligned4(q_lens) || !aligned4(lse))
     return SI_ERR_ALIGN;
@@ -453,7 +456,7 @@ int si_cache4_attention(const void* qa, const void* pages, int n_pages, const in
   size_t need = 0;
   int rc = cache4_problem(width, page, topk, B, S, H, H_k, d, window, sinks, opt, &p, &o, &need);
   if (rc) return rc;
-  if (!(scale >= 0.0f) || scale == INFINITY || !scale_ok(k_scale) || !scale_ok(v_scale))
+  if (!scale_ok(k_scale) || !scale_ok(v_scale) || !scale_finite(scale * k_scale))
     return SI_ERR_OPTIONS;
   if (!aligned16(qa) || !aligned16(pages) || !aligned16(out) || !aligned4(table) ||
       !aligned4(lens) || !aligned4(q_lens) || !aligned4(idx) || !aligned4(lse))

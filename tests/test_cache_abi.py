@@ -147,3 +147,11 @@ def test_plan_is_the_same_for_the_size_and_the_call(lib):
                 assert 0 <= n.value < 4 << 30
                 last = n.value
             assert last >= 0
+
+
+def test_scales_that_overflow(lib):
+    """A softmax scale has to be finite in log2 units and with the keys' scale in it."""
+    assert window(lib, scale=3e38) == -8
+    for scale, ks in ((3e38, 1.0), (1e25, 2.0 ** 60)):
+        assert lib.si_cache4_attention(FAKE, FAKE, 4, FAKE, 4, 16, FAKE, None, None, 0, 1, 1, 8, 2, 64, 0, 0, scale, ks, 1.0, FAKE, None,
+                                       None, None, 0, None) == -8
