@@ -7,9 +7,10 @@
 // One thread takes one block: 32 bytes in, 8 bytes of codes and one scale
 // out, neighbouring threads on neighbouring blocks.  Measured on B200: chunks
 // of up to 4,096 rows of four ragged sequences, 8 kv heads of 128 elements,
-// appended in 17 us, 71 % of the issue slots taken and 61 % of the ALUs' time:
-// bound by the rounding's instructions.  Append and read together take 31-35 us,
-// with two blocks a thread 39.  The quotient
+// appended in 14 us and read in 12.5 (24 MB and as much: launch, lengths, table
+// and data are a chain of loads).  Before NaNs and saturated blocks had a path of
+// their own the rounding's instructions bound the append, at 17.  Append and read
+// together take 31 us, with two blocks a thread 39.  The quotient
 // is Markstein's correctly rounded one (reciprocal rounded to nearest, product,
 // one residual step; "Computation of elementary functions on the IBM RISC
 // System/6000 processor", 1990), a third of a division's instructions: ties
@@ -86,13 +87,19 @@ __global__ void __launch_bounds__(kThreads) k_cache4_append(const Cache4Params p
   for (int i = 0; i < 8; ++i) {
     x[2 * i] = bf16_lo(w[i]);
     x[2 * i + 1] = bf16_hi(w[i]);
-  }
-#pragma unroll
-  for (int i = 0; i < 16; ++i) {
-    x[i] = x[i] == x[i] ? x[i] : 0.0f;
-    amax = fmaxf(amax, fabsf(x[i]));
+    amax = max3_abs_nan(amax, x[2 * i], x[2 * i + 1]);
   }
   const float g = bl.is_v ? p.v_scale : p.k_scale;
+  // a NaN, or elements that the largest scale does not reach
+  const bool odd = !(amax <= 6.0f * 448.0f * g);
+  if (odd) {
+    amax = 0.0f;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      x[i] = x[i] == x[i] ? x[i] : 0.0f;
+      amax = fmaxf(amax, fabsf(x[i]));
+    }
+  }
   uint16_t sb;
   asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;"
       : "=h"(sb)
@@ -102,12 +109,24 @@ __global__ void __launch_bounds__(kThreads) k_cache4_append(const Cache4Params p
   uint32_t out[2] = {0u, 0u};
   if (gs > 0.0f) {
     float y[16];
+    if (!odd) {
+      // quotients of less than 9, two at a time
+      const uint64_t rcp2 = pair2(rcp, rcp), neg2 = pair2(-gs, -gs);
 #pragma unroll
-    for (int i = 0; i < 16; ++i) {
-      // up to 8 the quotient is exact to rounding; past that it is stored as 6
-      const float m = fabsf(x[i]);
-      const float q = fminf(m * rcp, 8.0f);
-      y[i] = copysignf(fmaf(fmaf(-q, gs, m), rcp, q), x[i]);
+      for (int i = 0; i < 16; i += 2) {
+        const uint64_t m = pair2(x[i], x[i + 1]), q = mul2(m, rcp2);
+        unpair2(fma2(fma2(q, neg2, m), rcp2, q), y[i], y[i + 1]);
+        y[i] = copysignf(y[i], x[i]);  // of zeros
+        y[i + 1] = copysignf(y[i + 1], x[i + 1]);
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        // up to 8 the quotient is exact to rounding; past that it is stored as 6
+        const float m = fabsf(x[i]);
+        const float q = fminf(m * rcp, 8.0f);
+        y[i] = copysignf(fmaf(fmaf(-q, gs, m), rcp, q), x[i]);
+      }
     }
 #pragma unroll
     for (int i = 0; i < 8; ++i)
