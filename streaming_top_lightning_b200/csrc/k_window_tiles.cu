@@ -65,15 +65,7 @@ constexpr int kWinThreads = 384;
 constexpr int kSoftWarp = 4;   // softmax warps 4-7: tile 0, 8-11: tile 1
 constexpr float kGrow = 16.0f; // log2 growth of a maximum that rescales O
 
-template <int D>
-struct WinCfg {
-  static constexpr uint32_t kQ = kM * D * 2;      // one Q tile
-  static constexpr uint32_t kQHalf = kM * 128;    // its 64-column half
-  static constexpr uint32_t kBlock = kN * D * 2;  // one K or V block
-  static constexpr uint32_t kHalf = kN * 128;     // its 64-column half
-  static constexpr int kSlots = D == 128 ? 10 : 12;
-  static constexpr size_t kSmem = 2 * (size_t)kQ + kSlots * (size_t)kBlock + 1024 + 512;
-};
+constexpr int kListed = 256;  // sequences whose live pairs a CTA lists
 
 struct WinCtl {
   uint64_t kv_full[12], kv_empty[12], kv_land;
@@ -81,6 +73,19 @@ struct WinCtl {
   uint64_t q_full, q_empty, s_full[2][2], p_ready[2][2], pv_done[2][2];  // [tile][buffer]
   uint32_t tmem_base;
   uint32_t abort;
+  int starts[kListed + 1];  // LISTED: live pairs of the sequences before each one
+  int items;
+};
+
+template <int D>
+struct WinCfg {
+  static constexpr uint32_t kQ = kM * D * 2;      // one Q tile
+  static constexpr uint32_t kQHalf = kM * 128;    // its 64-column half
+  static constexpr uint32_t kBlock = kN * D * 2;  // one K or V block
+  static constexpr uint32_t kHalf = kN * 128;     // its 64-column half
+  static constexpr int kSlots = D == 128 ? 10 : 12;
+  static constexpr size_t kSmem =
+      2 * (size_t)kQ + kSlots * (size_t)kBlock + 1024 + sizeof(WinCtl);
 };
 
 SI_DEV void tma_load_4d(uint32_t dst, const CUtensorMap* map, uint32_t bar, int c0, int c1, int c2,
@@ -111,13 +116,26 @@ struct WinItem {
   SI_DEV int first(int i) const { return t0 + i * QT; }
 };
 
-template <bool SPLIT>
-SI_DEV bool win_item(const WinParams& p, int id, WinItem& it) {
-  const int all = SPLIT ? p.pairs * p.splits : p.pairs, bh = id / all;
-  it.chunk = SPLIT ? (id - bh * all) / p.pairs : 0;
-  const int pair = id - bh * all - it.chunk * p.pairs;
-  it.b = bh / p.Hk;
-  it.hk = bh - it.b * p.Hk;
+template <bool SPLIT, bool LISTED>
+SI_DEV bool win_item(const WinParams& p, int id, const int* starts, WinItem& it) {
+  int pairs = p.pairs, b = 0;
+  if constexpr (LISTED) {  // the sequence whose live pairs hold the item
+    const int unit = id / (SPLIT ? p.Hk * p.splits : p.Hk);
+    for (int hi = p.B; hi - b > 1;) {
+      const int mid = (b + hi) >> 1;
+      if (starts[mid] <= unit)
+        b = mid;
+      else
+        hi = mid;
+    }
+    pairs = starts[b + 1] - starts[b];
+    id -= starts[b] * (SPLIT ? p.Hk * p.splits : p.Hk);
+  }
+  const int all = SPLIT ? pairs * p.splits : pairs, bh = id / all;
+  it.chunk = SPLIT ? (id - bh * all) / pairs : 0;
+  const int pair = id - bh * all - it.chunk * pairs;
+  it.b = LISTED ? b : bh / p.Hk;
+  it.hk = LISTED ? bh : bh - it.b * p.Hk;
   it.i0 = pair * 2 * p.QT;
   it.len = seq_len(p.lens, it.b, p.T);
   it.q_len = seq_len(p.q_lens, it.b, p.S);
@@ -186,8 +204,11 @@ SI_DEV int ring_block(int blocks, int x, bool& is_v) {
 }
 }  // namespace
 
-// SPLIT: chunks of a pair's keys are items of their own.
-template <int D, bool SPLIT>
+// SPLIT: chunks of a pair's keys are items of their own.  LISTED: sequences have
+// query rows of their own number, and a CTA's items are every so-many-th of
+// those that have rows (8 ragged chunks of up to 1,024 queries, window 1,024:
+// 99 us, 113-118 without; the longer way to an item costs a full prompt 5 %).
+template <int D, bool SPLIT, bool LISTED>
 __global__ void __launch_bounds__(kWinThreads, 1)
     k_window_tiles(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                    const __grid_constant__ CUtensorMap tm_v, const WinParams p) {
@@ -225,6 +246,31 @@ __global__ void __launch_bounds__(kWinThreads, 1)
     tmem_alloc(smem_u32(&cs->tmem_base), 512);
     tmem_relinquish();
   }
+  if (LISTED && warp == 2) {
+    int live[kListed / 32], sum = 0;
+#pragma unroll
+    for (int e = 0; e < kListed / 32; ++e) {
+      const int b = lane * (kListed / 32) + e;
+      live[e] = b < p.B ? (seq_len(p.q_lens, b, p.S) + 2 * p.QT - 1) / (2 * p.QT) : 0;
+      sum += live[e];
+    }
+    int at = sum;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xFFFFFFFFu, at, o);
+      if (lane >= o) at += y;
+    }
+    at -= sum;
+#pragma unroll
+    for (int e = 0; e < kListed / 32; ++e) {
+      cs->starts[lane * (kListed / 32) + e] = at;
+      at += live[e];
+    }
+    if (lane == 31) {
+      cs->starts[kListed] = at;
+      cs->items = at * p.Hk * p.splits;
+    }
+  }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -235,9 +281,9 @@ __global__ void __launch_bounds__(kWinThreads, 1)
     // ------------------------------------------------------------ K and V
     uint32_t at = 0, lands = 0;  // blocks issued; blocks mended
     bool ok = true;
-    for (int id = blockIdx.x; ok && id < p.items; id += gridDim.x) {
+    for (int id = blockIdx.x; ok && id < (LISTED ? cs->items : p.items); id += gridDim.x) {
       WinItem it;
-      if (!win_item<SPLIT>(p, id, it)) continue;
+      if (!win_item<SPLIT, LISTED>(p, id, cs->starts, it)) continue;
       for (int x = 0; ok && x < 2 * it.blocks; ++x, ++at) {
         bool is_v;
         const int n = ring_block(it.blocks, x, is_v);
@@ -293,9 +339,9 @@ __global__ void __launch_bounds__(kWinThreads, 1)
     // ------------------------------------------------------------ Q
     if (lane == 0) {
       uint32_t n = 0;
-      for (int id = blockIdx.x; id < p.items; id += gridDim.x) {
+      for (int id = blockIdx.x; id < (LISTED ? cs->items : p.items); id += gridDim.x) {
         WinItem it;
-        if (!win_item<SPLIT>(p, id, it) || it.blocks == 0) continue;
+        if (!win_item<SPLIT, LISTED>(p, id, cs->starts, it) || it.blocks == 0) continue;
         if (!mbar_wait(smem_u32(&cs->q_empty), (n & 1u) ^ 1u, ctl)) break;
         ++n;
         const int tiles = it.live > p.QT ? 2 : 1;
@@ -329,11 +375,11 @@ __global__ void __launch_bounds__(kWinThreads, 1)
     const uint64_t qd = sdesc_sw128(uniform(base) + i * C::kQ);
     const uint64_t kd0 = sdesc_sw128(uniform(ring)), vd0 = sdesc_mn(uniform(ring), C::kHalf);
     uint32_t slot = 0, phase = 0;  // of the next block in the ring
-    uint32_t items = 0, np = 0;
+    uint32_t nq = 0, np = 0;
     bool ok = true;
-    for (int id = blockIdx.x; ok && id < p.items; id += gridDim.x) {
+    for (int id = blockIdx.x; ok && id < (LISTED ? cs->items : p.items); id += gridDim.x) {
       WinItem it;
-      if (!uniform(win_item<SPLIT>(p, id, it))) continue;
+      if (!uniform(win_item<SPLIT, LISTED>(p, id, cs->starts, it))) continue;
       const int blocks = uniform(it.blocks), wins = uniform(it.win_blocks);
       if (blocks == 0) continue;
       const int from = uniform(i ? it.from[1] : it.from[0]), to = uniform(i ? it.to[1] : it.to[0]);
@@ -341,8 +387,8 @@ __global__ void __launch_bounds__(kWinThreads, 1)
       const int win_cols = uniform(columns(block_keys(it, it.win_blocks - 1)));
       const int sink_cols = uniform(columns(block_keys(it, it.blocks - 1)));
       const bool sinks = uniform(i ? it.sinks[1] : it.sinks[0]);
-      if (!mbar_wait_warp(smem_u32(&cs->q_full), items & 1u, ctl)) break;
-      ++items;
+      if (!mbar_wait_warp(smem_u32(&cs->q_full), nq & 1u, ctl)) break;
+      ++nq;
       uint32_t begun = 0u;
       // The first two blocks' scores, then for each block its values and the
       // scores of the one two further on, into the buffer of the same parity:
@@ -420,9 +466,9 @@ __global__ void __launch_bounds__(kWinThreads, 1)
     uint32_t ns = 0, npv = 0;
     int last = 0;
     bool stop = false;
-    for (int id = blockIdx.x; !stop && id < p.items; id += gridDim.x) {
+    for (int id = blockIdx.x; !stop && id < (LISTED ? cs->items : p.items); id += gridDim.x) {
       WinItem it;
-      if (!win_item<SPLIT>(p, id, it) || it.nq(i) == 0) continue;
+      if (!win_item<SPLIT, LISTED>(p, id, cs->starts, it) || it.nq(i) == 0) continue;
       const int qi = row / p.G;  // query of the row within the tile
       const int nq = it.nq(i);
       const int ta = it.first(i), tb = ta + nq - 1;
@@ -662,7 +708,8 @@ __global__ void __launch_bounds__(128) k_window_join(const WinParams p) {
   const int head = at % p.H, bq = at / p.H, i = bq % p.S, b = bq / p.S;
   WinItem it;
   if (i >= seq_len(p.q_lens, b, p.S)) return;
-  if (!win_item<true>(p, (b * p.Hk + head / heads) * p.pairs * p.splits + i / (2 * p.QT), it) ||
+  if (!win_item<true, false>(p, (b * p.Hk + head / heads) * p.pairs * p.splits + i / (2 * p.QT), nullptr,
+                      it) ||
       it.pieces == 1)
     return;
   const int64_t first = (int64_t)at * p.splits;
@@ -692,14 +739,22 @@ __global__ void __launch_bounds__(128) k_window_join(const WinParams p) {
     p.lse[at] = sum == 0.0f ? neg_inf() : (top + log2f(sum)) * 0.6931471805599453f;
 }
 
+namespace {
+template <int D>
+auto window_tiles(const WinParams& p) {
+  const bool listed = p.q_lens && p.B > 1 && p.B <= kListed;
+  return p.splits > 1 ? (listed ? k_window_tiles<D, true, true> : k_window_tiles<D, true, false>)
+                      : (listed ? k_window_tiles<D, false, true> : k_window_tiles<D, false, false>);
+}
+}  // namespace
+
 size_t window_tiles_smem(int D) { return D == 128 ? WinCfg<128>::kSmem : WinCfg<64>::kSmem; }
 
 cudaError_t launch_window_tiles(const CUtensorMap& tm_q, const CUtensorMap& tm_k,
                                 const CUtensorMap& tm_v, const WinParams& p, int D, int grid,
                                 cudaStream_t stream) {
   const size_t smem = window_tiles_smem(D);
-  const auto fn = p.splits > 1 ? (D == 128 ? k_window_tiles<128, true> : k_window_tiles<64, true>)
-                               : (D == 128 ? k_window_tiles<128, false> : k_window_tiles<64, false>);
+  const auto fn = D == 128 ? window_tiles<128>(p) : window_tiles<64>(p);
   const cudaError_t e =
       cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;

@@ -131,3 +131,31 @@ def test_workspace_refusals():
     small = torch.empty(16, dtype=torch.uint8, device="cuda")
     with pytest.raises(stl.StreamIndexError):
         stl.window_attention(q, k, v, 3000, 4, workspace=small)
+
+
+@pytest.mark.parametrize("S,T", [(20, 40), (70, 3000)])
+@pytest.mark.parametrize("B", [2, 6, 255, 256, 257])
+def test_sequences_without_rows(B, S, T):
+    """Rows of some sequences only, on both sides of the number of sequences that a CTA lists."""
+    if B > 6 and T > 1000:
+        T = 200
+    g = torch.Generator().manual_seed(B)
+    q_lens = torch.randint(0, S + 1, (B,), generator=g)
+    q_lens[torch.rand((B,), generator=g) < 0.5] = 0
+    lens = (q_lens + torch.randint(0, T - S + 1, (B,), generator=g)).tolist()
+    q_lens = q_lens.tolist()
+    q, k, v = inputs(B, S, T, 4, 2, 64, seed=B)
+    out, lse = run(q, k, v, T - 10, 3, lens, q_lens)
+    some = {0, 1, 2, B // 2, B - 3, B - 2, B - 1}
+    rows = {(b, i) for b in some for i in (0, 1, S // 2, S - 1)}
+    check(q, k, v, T - 10, 3, lens, q_lens, out, lse, u=U, rows=rows, fill=7.0)
+    # the rows that no query has, all of them
+    dead = torch.arange(S)[None] >= torch.tensor(q_lens)[:, None]
+    assert bool((out.cpu()[dead] == 7).all()) and bool((lse.cpu()[dead] == 7).all())
+    assert bool((lse.cpu()[~dead] != 7).all())
+
+
+def test_no_rows_at_all():
+    q, k, v = inputs(3, 40, 50, 4, 2, 128, seed=3)
+    out, lse = run(q, k, v, 20, 0, [50, 7, 0], [0, 0, 0])
+    assert bool((out == 7).all()) and bool((lse == 7).all())
