@@ -41,7 +41,7 @@
 //
 // Measured on B200 (D = 128): 32 sequences, 32 heads on 8 kv heads, a window of
 // 1,024 bf16 keys, 25.4 us, 5.3 TB/s; the same heads over ragged 4-bit caches of
-// up to 8,192 keys, 57 us, 2.7 TB/s of the 6.6 that a copy reaches: the warps'
+// up to 8,192 keys, 55 us, 2.8 TB/s of the 6.6 that a copy reaches: the warps'
 // instructions (about 800 for 32 keys: codes to fp16, products, transpositions)
 // take 59 % of the issue slots and half of the ALUs' time.  Five CTAs an SM with
 // two stages took 64 us, shares weighted by a CTA's start 60.
@@ -381,6 +381,7 @@ __global__ void __launch_bounds__(kRowWarps * 32, row_ctas(D, MODE, NT))
   int u_lo, u_hi, split;
   __shared__ Share job;
   if (p.share == kShared) {
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the join, see launch_join
     if (!share_of<RT, KS>(p, job)) return;
   } else {
     const uint32_t tile = blockIdx.x / (uint32_t)p.splits;
@@ -854,6 +855,7 @@ template <int D, int KS, int RT, int W, bool SHARED>
 __global__ void __launch_bounds__(128) k_attn_join(const __grid_constant__ RowsParams p) {
   constexpr int E = D / 32;
   __shared__ float sh_o[4][D], sh_l[4], sh_top[4];
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rows = (uint32_t)(p.S * p.G), at32 = W == 1 ? blockIdx.x * 4 + warp : blockIdx.x;
   if (at32 >= (uint32_t)(p.B * p.Hk) * rows) return;  // B*S*H < 2^31
@@ -938,15 +940,24 @@ namespace {
 
 // Up to 24 chunks a warp takes a row, beyond that four.  (500 ragged sequences
 // of up to 1,024 keys, few pieces each: 62.9 us with one warp, 75 with four; one
-// sequence of 131,072 keys: 47.2 and 29.1.)
+// sequence of 131,072 keys: 47.2 and 29.1.)  The join's CTAs are brought up
+// while the chunks' run out and wait for their end (32 ragged sequences of up to
+// 8,192 keys: 54.9 us, else 56.5; 200 of up to 2,048: 71 and 76.8).
 template <int D, int KS, int RT, bool SHARED>
 cudaError_t launch_join(const RowsParams& p, cudaStream_t stream) {
   const int64_t rows = (int64_t)p.B * p.Hk * p.S * p.G;
-  if (p.splits <= 24)
-    k_attn_join<D, KS, RT, 1, SHARED><<<(unsigned)((rows + 3) / 4), 128, 0, stream>>>(p);
-  else
-    k_attn_join<D, KS, RT, 4, SHARED><<<(unsigned)rows, 128, 0, stream>>>(p);
-  return cudaGetLastError();
+  const bool few = p.splits <= 24;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3((unsigned)(few ? (rows + 3) / 4 : rows));
+  cfg.blockDim = dim3(128);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr{};
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(
+      &cfg, few ? k_attn_join<D, KS, RT, 1, SHARED> : k_attn_join<D, KS, RT, 4, SHARED>, p);
 }
 
 template <int D, int MODE, int NT>
