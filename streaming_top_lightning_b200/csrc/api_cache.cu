@@ -46,12 +46,16 @@ int check_attention(int B, int S, int H, int H_k, int d) {
 // 16-row tiles take 20.7, 44.5 and 45.4.)
 //
 // Sharing, tiles below 128 rows:
-//  kSplit, a CTA a tile, where all tiles are resident at once, see as much, and
-//    the places left idle would save less than a join costs: 32 steps.  (32
+//  kSplit, a CTA a tile, where tiles see as much and the places that the last
+//    round of CTAs leaves idle would save less than a join costs: 32 steps of
+//    rows of 128 elements (of any rows where a cluster would do).  (bf16, 32
 //    sequences, 8 kv heads, window 1,024: 25.4 us; 33.9 in equal shares, 37 in
 //    fixed chunks and a join.  12 such sequences, 96 tiles: window 512 13.3 us
-//    and 18.5 in shares, window 2,048 34.9 and 29.)  Also where tiles are many
-//    times the places.
+//    and 18.5 in shares, window 2,048 34.9 and 29.  64 sequences, two rounds on
+//    296 places, window 1,024: 61.4 and 71.7, with rows of 64 36.9 and 47.5; 48
+//    sequences, window 2,048: 98.3 and 92.1, with rows of 64 55.8 and 61.7.
+//    4-bit, 128 sequences on 592 places, window 512: 32.7 and 43.)
+//    Also where tiles are many times the places.
 //  kCluster, a tile's chunks in one cluster that joins them, for calls of few
 //    steps whose clusters are all resident (three drafted tokens of four
 //    sequences: 13.9 us, with a join kernel 19.3; 32 ragged sequences of up to
@@ -95,13 +99,16 @@ int plan_rows(RowsParams* p, int64_t keys, bool cache4, bool even, int key_chunk
     const int64_t least = 8;  // two steps of 32 keys for each of a CTA's warps
     // clusters of up to eight, as long as the GPU holds all of them at once
     const int64_t n = std::min<int64_t>(8, std::max<int64_t>(1, room / tiles));
+    const bool few = n > 1 && steps <= n * least * 2;  // a cluster's share is a few steps
+    const int64_t idle = (room - tiles % room) % room;
     if (key_chunk == 0 && steps <= least) {
       p->share = kSplit;
     } else if (key_chunk == 0 &&
-               ((even && 2 * tiles > sms && tiles <= room && steps * (room - tiles) <= 32 * room) ||
+               ((even && 2 * tiles > sms &&
+                 steps * idle * (few ? 128 : d) <= 32 * room * 128) ||
                 tiles > 8 * room)) {
       p->share = kSplit;
-    } else if (key_chunk == 0 && n > 1 && steps <= n * least * 2) {
+    } else if (key_chunk == 0 && few) {
       p->share = kCluster;
       chunk = std::max<int64_t>(least, (steps + n - 1) / n);
     } else {
@@ -197,8 +204,8 @@ int window_problem(int B, int S, int T, int H, int H_k, int d, int window, int s
   int max_smem = 0, sms = 0;
   plan_limits(&max_smem, &sms);
   if (window_in_tiles(S, p->G, o->key_chunk)) return plan_window_tiles(*p, sms, d, w, bytes);
-  return plan_rows(p, std::min<int64_t>(T, (int64_t)p->window + p->sinks), false, true,
-                   o->key_chunk, sms, d, bytes);
+  return plan_rows(p, std::min<int64_t>(T, (int64_t)p->window + p->sinks), false,
+                   true, o->key_chunk, sms, d, bytes);
 }
 
 int cache4_problem(int width, int page, int topk, int B, int S, int H, int H_k, int d, int window,

@@ -359,15 +359,29 @@ SI_DEV bool share_of(const RowsParams& p, Share& job) {
   return true;
 }
 
-// CTAs that an SM's registers hold.
-constexpr int row_ctas(int D, int MODE, int NT) {
-  return MODE == 0 && (D == 128 || NT == 4) ? 2 : (NT == 1 ? 4 : 3);
+// Dynamic shared memory of a CTA: its warps' rings, or the join of the warps.
+template <int D, int MODE, int NT>
+constexpr size_t row_smem() {
+  constexpr size_t ring = (size_t)kRowWarps * Source<D, MODE, NT>::kStages *
+                          Source<D, MODE, NT>::kStageBytes;
+  constexpr size_t join = (size_t)kRowWarps * 8 * NT * (D + 4) * sizeof(float);
+  return ring > join ? ring : join;
+}
+
+// CTAs that an SM holds: of those that its registers do, as many as its 228 KB
+// of shared memory do (a CTA has 1 KB of the system's and up to 1.5 KB of static
+// arrays besides).  bf16 rings of 96 KB leave room for two.
+template <int D, int MODE, int NT>
+constexpr int row_ctas() {
+  constexpr int regs = NT == 1 ? 4 : (NT == 2 ? 3 : 2);
+  constexpr int smem = (int)(228 * 1024 / (row_smem<D, MODE, NT>() + 2560));
+  return regs < smem ? regs : smem;
 }
 
 }  // namespace
 
 template <int D, int MODE, int NT>
-__global__ void __launch_bounds__(kRowWarps * 32, row_ctas(D, MODE, NT))
+__global__ void __launch_bounds__(kRowWarps * 32, row_ctas<D, MODE, NT>())
     k_attn_rows(const __grid_constant__ RowsParams p) {
   using Src = Source<D, MODE, NT>;
   constexpr int KS = Src::KS, NST = Src::kStages, NG = KS / 16, RT = 8 * NT;
@@ -963,9 +977,7 @@ cudaError_t launch_join(const RowsParams& p, cudaStream_t stream) {
 template <int D, int MODE, int NT>
 cudaError_t launch(const RowsParams& p, cudaStream_t stream) {
   using Src = Source<D, MODE, NT>;
-  const size_t ring = (size_t)kRowWarps * Src::kStages * Src::kStageBytes;
-  const size_t join = (size_t)kRowWarps * 8 * NT * (D + 4) * sizeof(float);
-  const size_t smem = ring > join ? ring : join;
+  constexpr size_t smem = row_smem<D, MODE, NT>();
   cudaError_t e = cudaFuncSetAttribute(k_attn_rows<D, MODE, NT>,
                                        cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;
@@ -1001,7 +1013,17 @@ cudaError_t launch_attn_join_tiles(const RowsParams& p, int D, cudaStream_t stre
                   : launch_join<64, 64, 128, false>(p, stream);
 }
 
-int attn_rows_ctas(int D, bool cache4, int row_tile) { return row_ctas(D, cache4 ? 1 : 0, row_tile / 8); }
+template <int D>
+static int rows_ctas(bool cache4, int row_tile) {
+  if (cache4) return row_tile == 8 ? row_ctas<D, 1, 1>() : row_ctas<D, 1, 2>();
+  return row_tile == 8    ? row_ctas<D, 0, 1>()
+         : row_tile == 16 ? row_ctas<D, 0, 2>()
+                          : row_ctas<D, 0, 4>();
+}
+
+int attn_rows_ctas(int D, bool cache4, int row_tile) {
+  return D == 128 ? rows_ctas<128>(cache4, row_tile) : rows_ctas<64>(cache4, row_tile);
+}
 
 cudaError_t launch_attn_rows(const RowsParams& p, int D, cudaStream_t stream) {
   const int mode = !p.pages ? 0 : (p.idx ? 2 : 1);
