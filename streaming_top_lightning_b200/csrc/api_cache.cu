@@ -36,7 +36,7 @@ int check_attention(int B, int S, int H, int H_k, int d) {
 
 // The plan over a call's keys: the tile width, how the CTAs share the tiles'
 // keys, and the bytes of partial results.  keys: what one query may see at
-// most; even: that all sequences are likely to see as many.
+// most; spread: how far the sequences may differ in what they see.
 //
 // Tile width: the narrowest of 8, 16 and 32 rows that holds a kv head's rows,
 // so that keys are read once; over a 4-bit cache 128-row tensor-core tiles from
@@ -55,13 +55,20 @@ int check_attention(int B, int S, int H, int H_k, int d) {
 //    296 places, window 1,024: 61.4 and 71.7, with rows of 64 36.9 and 47.5; 48
 //    sequences, window 2,048: 98.3 and 92.1, with rows of 64 55.8 and 61.7.
 //    4-bit, 128 sequences on 592 places, window 512: 32.7 and 43.)
+//    A window of more than half the table may be longer than most sequences; the
+//    imbalance then counts as an eighth of the places left idle.  (bf16, 37
+//    ragged sequences and 37 full ones, a window as long as the table: 77.8 and
+//    111.7 us against 76.1 and 117.1 in shares at 4,096 tokens, 269 and 365
+//    against 201 and 369 at 16,384; 32 of 4,096: 75.5 and 100.4 against 68.5 and
+//    112.  4-bit, 74 sequences of up to 8,192: 139 and 154 against 113 and 160.)
 //    Also where tiles are many times the places.
 //  kCluster, a tile's chunks in one cluster that joins them, for calls of few
 //    steps whose clusters are all resident (three drafted tokens of four
 //    sequences: 13.9 us, with a join kernel 19.3; 32 ragged sequences of up to
 //    8,192 keys in clusters 81 us, in shares 58).
 //  kShared else: one wave of CTAs, each with an equal share of all steps.
-int plan_rows(RowsParams* p, int64_t keys, bool cache4, bool even, int key_chunk, int sms, int d,
+enum { kAlike, kUnknown, kUnlike };
+int plan_rows(RowsParams* p, int64_t keys, bool cache4, int spread, int key_chunk, int sms, int d,
               size_t* bytes) {
   const bool listed = p->topk > 0;
   const int64_t rows = listed ? p->G : std::min<int64_t>((int64_t)p->S * p->G, 1 << 20);
@@ -100,11 +107,11 @@ int plan_rows(RowsParams* p, int64_t keys, bool cache4, bool even, int key_chunk
     // clusters of up to eight, as long as the GPU holds all of them at once
     const int64_t n = std::min<int64_t>(8, std::max<int64_t>(1, room / tiles));
     const bool few = n > 1 && steps <= n * least * 2;  // a cluster's share is a few steps
-    const int64_t idle = (room - tiles % room) % room;
+    const int64_t idle = (room - tiles % room) % room + (spread == kUnknown ? room / 8 : 0);
     if (key_chunk == 0 && steps <= least) {
       p->share = kSplit;
     } else if (key_chunk == 0 &&
-               ((even && 2 * tiles > sms &&
+               ((spread != kUnlike && 2 * tiles > sms &&
                  steps * idle * (few ? 128 : d) <= 32 * room * 128) ||
                 tiles > 8 * room)) {
       p->share = kSplit;
@@ -190,8 +197,13 @@ int plan_window_tiles(const RowsParams& p, int sms, int d, WinParams* w, size_t*
   return SI_OK;
 }
 
-// Sizes of a window call and its plan.
-int window_problem(int B, int S, int T, int H, int H_k, int d, int window, int sinks,
+// Whether tokens see about as many keys in every sequence: where the window is
+// what bounds them.
+int spread_of(int window, int T) { return 2 * (int64_t)window <= T ? kAlike : kUnknown; }
+
+// Sizes of a window call and its plan.  full: all sequences have T tokens.  (A
+// size query does not know; what it answers is no less, see plan_rows.)
+int window_problem(int B, int S, int T, int H, int H_k, int d, int window, int sinks, bool full,
                    const si_options* opt, RowsParams* p, WinParams* w, Opts* o, size_t* bytes) {
   int rc = check_attention(B, S, H, H_k, d);
   if (rc) return rc;
@@ -205,7 +217,7 @@ int window_problem(int B, int S, int T, int H, int H_k, int d, int window, int s
   plan_limits(&max_smem, &sms);
   if (window_in_tiles(S, p->G, o->key_chunk)) return plan_window_tiles(*p, sms, d, w, bytes);
   return plan_rows(p, std::min<int64_t>(T, (int64_t)p->window + p->sinks), false,
-                   true, o->key_chunk, sms, d, bytes);
+                   full ? kAlike : spread_of(window, T), o->key_chunk, sms, d, bytes);
 }
 
 int cache4_problem(int width, int page, int topk, int B, int S, int H, int H_k, int d, int window,
@@ -230,7 +242,8 @@ int cache4_problem(int width, int page, int topk, int B, int S, int H, int H_k, 
   plan_limits(&max_smem, &sms);
   const int64_t keys =
       topk ? topk : std::min<int64_t>(p->T, (int64_t)p->window + p->sinks);
-  return plan_rows(p, keys, true, topk > 0 || window > 0, o->key_chunk, sms, d, bytes);
+  return plan_rows(p, keys, true, topk ? kAlike : window ? spread_of(window, p->T) : kUnlike,
+                   o->key_chunk, sms, d, bytes);
 }
 
 // The sizes of a call on the rows of a 4-bit cache.
@@ -330,7 +343,7 @@ int si_window_attention_workspace_size(int B, int S, int T, int H, int H_k, int 
   WinParams w{};
   Opts o;
   size_t need = 0;
-  const int rc = window_problem(B, S, T, H, H_k, d, window, sinks, opt, &p, &w, &o, &need);
+  const int rc = window_problem(B, S, T, H, H_k, d, window, sinks, false, opt, &p, &w, &o, &need);
   if (rc == SI_OK) *bytes = need;
   return rc;
 }
@@ -344,7 +357,7 @@ int si_window_attention(const void* qa, const void* ka, const void* va, const in
   WinParams w{};
   Opts o;
   size_t need = 0;
-  int rc = window_problem(B, S, T, H, H_k, d, window, sinks, opt, &p, &w, &o, &need);
+  int rc = window_problem(B, S, T, H, H_k, d, window, sinks, !lens, opt, &p, &w, &o, &need);
   if (rc) return rc;
   if (!scale_finite(scale)) return SI_ERR_OPTIONS;
   if (!aligned16(qa) || !aligned16(ka) || !aligned16(va) || !aligned16(out) || !aligned4(lens) ||

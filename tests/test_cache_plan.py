@@ -53,6 +53,16 @@ def test_one_wave_of_ctas(lib, B, H, Hk):
     assert got[0] == got[1]
 
 
+@pytest.mark.parametrize("d", [64, 128])
+def test_long_windows_are_shared(lib, d):
+    """A window that may be longer than most sequences does not tie a call to its longest one."""
+    T = 1 << 16
+    assert window_size(lib, 37, 1, T, 32, 8, d, T) > 0
+    assert window_size(lib, 37, 1, T, 32, 8, d, 512) == 0  # a CTA a tile: all see as much
+    assert cache4_size(lib, T // 64, 64, 0, 74, 1, 32, 8, d, T) > 0
+    assert cache4_size(lib, T // 64, 64, 0, 74, 1, 32, 8, d, 512) == 0
+
+
 WINDOWS = [(B, S, T, H, Hk, d, w, n, chunk) for B in (1, 5, 64, 700) for S, T in ((1, 30), (1, 40000), (3, 5000), (40, 9000), (600, 60000))
            for H, Hk, d in ((1, 1, 64), (8, 2, 128), (24, 8, 64), (128, 1, 128)) for w, n in ((1, 0), (300, 4), (10 ** 9, 0)) for chunk in (0, 256)
            if B * S * H < 1 << 20]

@@ -1,5 +1,5 @@
 """The few-row kernel of the window attention where test_gpu_window.py does not go: d = 64 with keys
-that many CTAs share, tiles for several rounds of CTAs.  Tolerances: test_gpu_window.py."""
+that many CTAs share, tiles for several rounds of CTAs, windows as long as the table.  Tolerances: test_gpu_window.py."""
 
 from __future__ import annotations
 
@@ -22,6 +22,23 @@ def test_d64_shares(H, Hk, chunk):
     lens = [T, 0, 1, 33, 64, 700, 1999, T - 1, 2500]
     out, lse = run(q, k, v, T, 4, lens, [1, 1, 1, 0, 1, 1, 1, 1, 1], opts=stl.options(key_chunk=chunk) if chunk else None)
     check(q, k, v, T, 4, lens, [1, 1, 1, 0, 1, 1, 1, 1, 1], out, lse, fill=7.0)
+
+
+@pytest.mark.parametrize("D,T", [(64, 20000), (128, 9000)])
+def test_ragged_under_a_long_window(D, T):
+    """A tile for each of the places, a window as long as the table: ragged sequences share the CTAs,
+    and without lengths each tile has one and needs no workspace."""
+    B, H, Hk = 37, 16, 8
+    g = torch.Generator(device="cuda").manual_seed(D)
+    q, k, v = (torch.randn(s, generator=g, device="cuda").to(torch.bfloat16) for s in ((B, 1, H, D), (B, T, Hk, D), (B, T, Hk, D)))
+    lens = [T, 0, 1] + [int(x) for x in np.random.default_rng(D).integers(0, T, B - 3)]
+    none = torch.empty(0, dtype=torch.uint8, device="cuda")
+    with pytest.raises(stl.StreamIndexError):
+        run(q, k, v, T, 0, lens, workspace=none)
+    for n, (out, lse) in ((lens, run(q, k, v, T, 0, lens)), ([T] * B, run(q, k, v, T, 0, workspace=none))):
+        for b in (0, 1, 2, 7, B - 1):
+            one = slice(b, b + 1)
+            check(q[one], k[one], v[one], T, 0, n[one], [1], out[one], lse[one])
 
 
 @pytest.mark.parametrize("D", [64, 128])
