@@ -423,7 +423,9 @@ int si_cache4_read(void* k, void* v, int B, int S, int H_k, int d, const void* p
  * rule with lens[b] in T's place (window and sinks must be 0):
  *   J(b,i) = { idx[b,i,r] : 0 <= r < topk, 0 <= idx[b,i,r] < lens[b] }
  * entries count as often as they are listed.  out, lse, q_lens, H, H_k and
- * options as in si_window_attention.
+ * options as in si_window_attention.  A scale byte that is NaN (si_cache4_append
+ * writes none) reaches the rows that see its key: a value's their 16 elements, a
+ * key's all of the row; other rows are as if it were a number.
  * Arithmetic: codes times block scales are exact in fp16; products in fp16
  * with fp32 accumulation (a query row is scaled into fp16's range by a power
  * of two), softmax in fp32, the probabilities rounded to fp16 (2^-11).

@@ -173,10 +173,11 @@ struct Cache4 {
   }
 
   // O^T += V^T P^T over 16 keys; MASKED: `live` says which keys of the group may
-  // be read (the others' codes count as zero).
+  // be read (the others' codes count as zero), `nans` which keys' NaN scales
+  // count as zero here.
   template <bool MASKED>
   SI_DEV void values(uint32_t vc, uint32_t vs, int lane, const uint32_t (&pf)[NT][2], uint32_t live,
-                     RowState<D, NT>& st) const {
+                     uint32_t nans, RowState<D, NT>& st) const {
     const int n = lane >> 2, c = lane & 3;
     uint32_t sp[2], w[4][D / 64];
 #pragma unroll
@@ -197,6 +198,7 @@ struct Cache4 {
           asm volatile("ld.shared.u8 %0, [%1];" : "=r"(b[i]) : "r"(vs + key * 4 + (n >> 1)));
         }
         if (MASKED && !((live >> key) & 1u)) b[i] = 0u;
+        if (MASKED && ((nans >> key) & 1u) && e4m3_nan(b[i])) b[i] = 0u;
       }
       sp[t] = e4m3x2(__byte_perm(b[0], b[1], 0x0040));
     }
@@ -390,6 +392,7 @@ template <int D, int MODE, int NT>
 __global__ void __launch_bounds__(kRowWarps * 32, row_ctas<D, MODE, NT>())
     k_attn_rows(const __grid_constant__ RowsParams p) {
   using Src = Source<D, MODE, NT>;
+  using Src4 = Cache4<D, NT>;
   constexpr int KS = Src::KS, NST = Src::kStages, NG = KS / 16, RT = 8 * NT;
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ float sh_m[kRowWarps][RT], sh_l[kRowWarps][RT];
@@ -581,6 +584,23 @@ __global__ void __launch_bounds__(kRowWarps * 32, row_ctas<D, MODE, NT>())
       live = __ballot_sync(0xFFFFFFFFu,
                            ((vm >> lane) & 1u) && span_holds(span, u, j0 + lane, p.sinks));
     if constexpr (MASKED && MODE == 2) live = vm;
+    // Keys that have a NaN among their value scales, where rows see different
+    // keys: a weight of zero times it would be NaN.  They count as zero in the
+    // products, and the rows that see them get their NaN below.
+    uint32_t nans = 0u;
+    const uint32_t v_scales = at + 2 * Src4::kCodes + Src4::kScales;
+    if constexpr (MASKED && MODE == 1) {
+      if (ti.t_min != ti.t_max) {
+        uint32_t any = 0u;
+#pragma unroll
+        for (int i = 0; i < D / 64; ++i) {
+          uint32_t w;
+          asm volatile("ld.shared.b32 %0, [%1];" : "=r"(w) : "r"(v_scales + lane * (D / 16) + 4 * i));
+          any |= e4m3_nans(w);
+        }
+        nans = __ballot_sync(0xFFFFFFFFu, any != 0u) & live;
+      }
+    }
     // scores to log2 units, unseen keys to -inf
     float mx[NT][2];
 #pragma unroll
@@ -666,7 +686,26 @@ __global__ void __launch_bounds__(kRowWarps * 32, row_ctas<D, MODE, NT>())
       else
         src.template values<MASKED>(at + Src::kCodes + g * 8 * D,
                                     at + 2 * Src::kCodes + Src::kScales + g * D, lane, pf,
-                                    live >> (16 * g), st);
+                                    live >> (16 * g), nans >> (16 * g), st);
+    }
+    if constexpr (MASKED && MODE == 1) {
+      for (uint32_t left = nans; left; left &= left - 1u) {
+        // a thread's elements of a row lie in one block of 16
+        const int key = __ffs((int)left) - 1;
+        uint32_t b;
+        asm volatile("ld.shared.u8 %0, [%1];" : "=r"(b) : "r"(v_scales + key * (D / 16) + r * D / 128));
+        if (!e4m3_nan(b)) continue;
+#pragma unroll
+        for (int x = 0; x < NT; ++x)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const int t = ti.len - ti.q_len + (ti.row0 + min(8 * x + 2 * c + e, ti.rows - 1)) / p.G;
+            if (!sees(j0 + key, t, ti.len, p.window, p.sinks)) continue;
+#pragma unroll
+            for (int i = 0; i < D / 16; ++i)
+              st.o[x][i][e] = st.o[x][i][2 + e] = __int_as_float(0x7FC00000);
+          }
+      }
     }
   };
 

@@ -65,6 +65,7 @@ struct TileCtl {
   uint64_t q_full, q_empty, ml_full, o_free;
   uint64_t idle[2];               // a CTA that gives up: its MMAs are done
   uint64_t mask[2][kSlots];       // keys of a block that are there
+  uint64_t nans[2][kSlots];       // not 0: a value scale of the block is NaN
   float factor[kM];               // 2^-x of the rows scaled by 2^x
   float xm[2][kM], xl[2][kM];     // the pipelines' maxima and sums
   uint32_t tmem_base;
@@ -101,6 +102,33 @@ SI_DEV void stand_by(const RowsParams& p) {
   if (p.share != kCluster || !find_tile<kM>(p, blockIdx.x / p.splits, ti)) return;
   cluster_sync();
   cluster_sync();
+}
+
+// The blocks of 16 elements whose NaN value scale a row at position t sees, among
+// the 64 keys from j0 on that are there.  By the whole warp.
+template <int D>
+SI_DEV uint32_t nan_blocks(const RowsParams& p, const Tile& ti, int j0, uint64_t there, int t,
+                           int lane) {
+  const int page = 1 << p.page_shift;
+  uint32_t seen = 0u;
+#pragma unroll 1
+  for (int h = 0; h < kN; h += 32) {
+    const int j = j0 + h + lane;
+    uint32_t bits = 0u;
+    if ((there >> (h + lane)) & 1u) {
+      const int64_t pg = __ldg(p.table + (int64_t)ti.b * p.width + (j >> p.page_shift));
+      const uint8_t* s = p.pages + pg * p.page_bytes + (int64_t)ti.hk * cache4_block<D>(page) +
+                         page * D + (page + (j & (page - 1))) * (D / 16);
+#pragma unroll 1
+      for (int c = 0; c < D / 16; ++c) bits |= (uint32_t)e4m3_nan(__ldg(s + c)) << c;
+    }
+#pragma unroll 1
+    for (int x = 0; x < 32; ++x) {
+      const uint32_t b = __shfl_sync(0xFFFFFFFFu, bits, x);
+      if (b && sees(j0 + h + x, t, ti.len, p.window, p.sinks)) seen |= b;
+    }
+  }
+  return seen;
 }
 
 // Blocks of pipeline i.
@@ -306,6 +334,19 @@ __global__ void __launch_bounds__(kThreads, 1) k_cache4_tiles(const __grid_const
         pg1 = page_of(j2);
         j1 = j2;
         j2 = key_of(n + 3);
+        if (!LISTED && is_v) {
+          // A NaN scale counts as zero in the products (a weight of zero times it
+          // would be NaN); the softmax looks up which rows it reaches.  The rows
+          // of a listed tile all see the same keys.
+          uint32_t odd = 0u;
+#pragma unroll
+          for (int x = 0; x < L; ++x) odd |= e4m3_nans(cur_s[x]);
+          const bool any = __any_sync(0xFFFFFFFFu, odd != 0u);
+          if (any)
+#pragma unroll
+            for (int x = 0; x < L; ++x) cur_s[x] &= ~((e4m3_nans(cur_s[x]) >> 7) * 0xFFu);
+          if (lane == 0) reinterpret_cast<uint32_t*>(&cs->nans[i][slot])[warp & 1] = any;
+        }
 #pragma unroll
         for (int x = 0; x < L; ++x) {
           const int row = key0 + x * R + sub;
@@ -352,6 +393,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_cache4_tiles(const __grid_const
       const int t = ti.len - ti.q_len + (ti.row0 + min(row, ti.rows - 1)) / p.G;
       const int blocks = pipe_blocks(it, i), others = pipe_blocks(it, i ^ 1);
       float m = neg_inf(), limit = neg_inf(), l = 0.0f, f = 0.0f;
+      uint32_t bad = 0u;  // blocks of 16 elements that a NaN scale reaches
       if (it.hi > it.lo) {
         // Q to fp16, scaled by a power of two a row (k_attn_rows.cu): 16 rows a
         // warp, D/8 lanes a row
@@ -406,6 +448,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_cache4_tiles(const __grid_const
           break;
         }
         const uint64_t there = cs->mask[i][kslot];
+        const bool odd = !LISTED && cs->nans[i][kslot] != 0u;
         if (++kslot == (uint32_t)kSlots) kslot = 0, kphase ^= 1u;
         ns ^= 1u << buf;
         tc_fence_after();
@@ -437,6 +480,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_cache4_tiles(const __grid_const
               if (!((seen >> e) & 1u)) v[c][e] = neg_inf();
           }
         }
+        if (odd) bad |= nan_blocks<D>(p, ti, j0, there, t, lane);
         float mx[4] = {neg_inf(), neg_inf(), neg_inf(), neg_inf()};
 #pragma unroll
         for (int c = 0; c < kN / 32; ++c)
@@ -520,6 +564,26 @@ __global__ void __launch_bounds__(kThreads, 1) k_cache4_tiles(const __grid_const
       if (blocks == 0 && n_ml > 0 &&
           !mbar_wait_warp(smem_u32(&cs->o_free), (n_ml - 1) & 1u, ctl))
         break;
+      if (__any_sync(0xFFFFFFFFu, bad != 0u)) {
+        // NaN into the row's elements of those blocks
+        const int last = (blocks - 1) & 1;
+        if (!mbar_wait_warp(smem_u32(&cs->pv_done[i][last]), ((mine >> last) & 1u) ^ 1u, ctl)) break;
+        tc_fence_after();
+#pragma unroll 1
+        for (int c = 0; c < D / 16; ++c) {
+          uint32_t w[16];
+          tmem_ld16(o_col + c * 16, w);
+          tmem_ld_wait();
+#pragma unroll
+          for (int e = 0; e < 16; ++e) {
+            asm volatile("" : "+r"(w[e]));
+            if ((bad >> c) & 1u) w[e] = 0x7FC00000u;
+          }
+          tmem_st16(o_col + c * 16, w);
+        }
+        tmem_st_wait();
+        tc_fence_before();
+      }
       cs->xm[i][row] = m;
       cs->xl[i][row] = l;
       mbar_arrive(smem_u32(&cs->ml_full));

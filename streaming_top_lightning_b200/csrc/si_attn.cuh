@@ -177,6 +177,9 @@ SI_DEV uint32_t e4m3x2(uint32_t w) {
       : "r"(w));
   return r;
 }
+// Whether an E4M3 byte is NaN, and a word's NaN bytes (0x80 in their places).
+SI_DEV bool e4m3_nan(uint32_t b) { return (b & 0x7Fu) == 0x7Fu; }
+SI_DEV uint32_t e4m3_nans(uint32_t w) { return ((w & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u; }
 SI_DEV uint32_t hmul2(uint32_t a, uint32_t b) {
   uint32_t r;
   asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
