@@ -388,13 +388,14 @@ int si_window_attention(const void* qa, const void* ka, const void* va, const in
   w.err = dev->err;
   w.timeout_ns = (uint64_t)o.timeout_ms * 1000000ull;
   w.debug_flags = o.debug_flags;
-  CUtensorMap tm_q, tm_k, tm_v;
-  if ((rc = make_map4(&tm_q, qa, d, H, S, B, p.G, w.QT)) ||
-      (rc = make_map4(&tm_k, ka, d, H_k, T, B, 1, 32)) ||
-      (rc = make_map4(&tm_v, va, d, H_k, T, B, 1, 32)))
+  CUtensorMap tm_q, tm_k, tm_v, tm_vs;
+  if ((rc = make_map4(&tm_q, qa, d, H, S, B, p.G, w.QT, S)) ||
+      (rc = make_map4(&tm_k, ka, d, H_k, T, B, 1, 32, T)) ||
+      (rc = make_map4(&tm_v, va, d, H_k, T, B, 1, 32, T)) ||
+      (rc = make_map4(&tm_vs, va, d, H_k, p.sinks > 0 ? std::min(p.sinks, T) : T, B, 1, 32, T)))
     return rc;
   const int most = o.grid_ctas > 0 ? o.grid_ctas : dev->sms;
-  return status(launch_window_tiles(tm_q, tm_k, tm_v, w, d, (int)std::min<int64_t>(most, w.items),
+  return status(launch_window_tiles(tm_q, tm_k, tm_v, tm_vs, w, d, (int)std::min<int64_t>(most, w.items),
                                     static_cast<cudaStream_t>(stream)));
 }
 

@@ -813,14 +813,41 @@ __global__ void __launch_bounds__(kRowWarps * 32, row_ctas<D, MODE, NT>())
     bool bad = false;
 #pragma unroll
     for (int i = 0; i < kPer; ++i) bad |= o[i] != o[i];
-    if (bad && row < ti.rows) atomicOr(&sh_nan, 1u << row);
+    // (rows whose weights are NaN are so by what they see, and rows of one query
+    // see the same keys)
+    if (bad && row < ti.rows && sum == sum && ti.t_min != ti.t_max) atomicOr(&sh_nan, 1u << row);
     __syncthreads();
-    if (sh_nan) {  // rows by the formula (see exact_row_keys)
+    if (sh_nan) {  // rows by the formula (si_attn.cuh)
       const int64_t stride = (int64_t)p.Hk * D;
       const int64_t first = ((int64_t)ti.b * p.T) * stride + (int64_t)ti.hk * D;
+      // the keys that the steps have brought
+      const int u_w = max(u_lo, span.sink_steps), ss = span.sink_steps;
+      const int w_lo = step_key<KS>(span, u_w), w_hi = min(span.end, step_key<KS>(span, max(u_hi, ss)));
+      const int s_lo = min(u_lo, ss) * KS, s_hi = min(span.sink_end, min(u_hi, ss) * KS);
       for (int x = warp; x < ti.rows; x += kRowWarps) {
         if (!((sh_nan >> x) & 1u)) continue;
         const int t = ti.len - ti.q_len + (ti.row0 + x) / p.G;
+        uint32_t nans = 0u;
+        if (unseen_bad<D>(p.v + first, stride, max(w_lo, span.lo), w_hi, t, p.window, p.sinks,
+                          lane) ||
+            unseen_bad<D>(p.v + first, stride, s_lo, s_hi, t, p.window, p.sinks, lane)) {
+#pragma unroll
+          for (int e = 0; e < D / 32; ++e) {
+            float y = 0.0f;
+#pragma unroll
+            for (int w = 0; w < kRowWarps; ++w)
+              y += sh_o[(w * RT + x) * kPad + lane * (D / 32) + e];
+            nans |= (uint32_t)(y != y) << e;
+          }
+          nans = unexplained<D>(p.v + first, stride, w_lo, w_hi, t, ti.len, p.window, p.sinks, lane,
+                                nans);
+          nans = unexplained<D>(p.v + first, stride, s_lo, s_hi, t, ti.len, p.window, p.sinks, lane,
+                                nans);
+        }
+        if (!__any_sync(0xFFFFFFFFu, nans != 0u)) {
+          if (lane == 0) atomicAnd(&sh_nan, ~(1u << x));
+          continue;
+        }
         float m = neg_inf(), l = 0.0f, acc[D / 32];
 #pragma unroll
         for (int e = 0; e < D / 32; ++e) acc[e] = 0.0f;

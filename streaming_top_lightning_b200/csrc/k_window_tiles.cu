@@ -39,8 +39,11 @@
 // that a boundary crosses are compared with positions.
 //
 // A masked column's probability is 0, and 0 times an infinity or NaN in V is
-// NaN; a row that comes out NaN is computed again by the formula
-// (exact_row_keys), so what a row does not see does not reach it.
+// NaN; a row that comes out NaN by a value that it does not see is computed again
+// by the formula (si_attn.cuh), so what a row does not see does not reach it.  The
+// values behind the sinks in their block, which no row sees there but every item
+// loads, are zeros of the TMA.  While rows are computed again the waits' clocks
+// stand still.
 // Where pairs of tiles are few and their keys many, the keys are cut into chunks
 // that are items of their own (SPLIT), their results kept in fp32 and joined by
 // k_window_join (plan_window_tiles says when, with the times).
@@ -73,6 +76,7 @@ struct WinCtl {
   uint64_t q_full, q_empty, s_full[2][2], p_ready[2][2], pv_done[2][2];  // [tile][buffer]
   uint32_t tmem_base;
   uint32_t abort;
+  uint32_t busy;  // softmax warps that compute rows again
   int starts[kListed + 1];  // LISTED: live pairs of the sequences before each one
   int items;
 };
@@ -211,7 +215,8 @@ SI_DEV int ring_block(int blocks, int x, bool& is_v) {
 template <int D, bool SPLIT, bool LISTED>
 __global__ void __launch_bounds__(kWinThreads, 1)
     k_window_tiles(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
-                   const __grid_constant__ CUtensorMap tm_v, const WinParams p) {
+                   const __grid_constant__ CUtensorMap tm_v,
+                   const __grid_constant__ CUtensorMap tm_vs, const WinParams p) {
   using C = WinCfg<D>;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
@@ -240,6 +245,7 @@ __global__ void __launch_bounds__(kWinThreads, 1)
       }
     }
     cs->abort = 0u;
+    cs->busy = 0u;
     mbar_fence_init();
   }
   if (warp == 1) {
@@ -275,7 +281,7 @@ __global__ void __launch_bounds__(kWinThreads, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = cs->tmem_base;
-  const Ctl ctl{p.err, &cs->abort, p.timeout_ns, nullptr};
+  const Ctl ctl{p.err, &cs->abort, p.timeout_ns, nullptr, &cs->busy};
 
   if (warp == 0) {
     // ------------------------------------------------------------ K and V
@@ -297,13 +303,14 @@ __global__ void __launch_bounds__(kWinThreads, 1)
         // keys past the sequence's end lie in the block's last columns
         const bool mend = is_v && j0 + cols > it.len;
         const uint32_t bar = smem_u32(mend ? &cs->kv_land : &cs->kv_full[slot]);
+        // keys behind the sinks in their block read as zeros (seen by no row there)
+        const CUtensorMap* map = !is_v ? &tm_k : (n < it.win_blocks ? &tm_v : &tm_vs);
         if (lane == 0) {
           mbar_arrive_expect_tx(bar, (uint32_t)cols * D * 2);
           for (int c = (p.debug_flags & 1) && at == 0 ? cols : 0; c < cols; c += 32)
 #pragma unroll
             for (int h = 0; h < D / 64; ++h)
-              tma_load_4d(dst + h * C::kHalf + c * 128, is_v ? &tm_v : &tm_k, bar, 64 * h, it.hk,
-                          j0 + c, it.b);
+              tma_load_4d(dst + h * C::kHalf + c * 128, map, bar, 64 * h, it.hk, j0 + c, it.b);
         }
         __syncwarp();
         if (mend) {
@@ -653,9 +660,12 @@ __global__ void __launch_bounds__(kWinThreads, 1)
         p.part_ml[at] = make_float2(l == 0.0f ? neg_inf() : m, l);
       else if (live && p.lse)
         p.lse[orow] = l == 0.0f ? neg_inf() : (m + log2f(l)) * 0.6931471805599453f;
-      // rows by the formula (see the head of the file)
+      // rows by the formula (see the head of the file); a row whose maximum is NaN
+      // has seen a score that makes it NaN
       __syncwarp();
-      uint32_t again = __ballot_sync(0xFFFFFFFFu, bad && live);
+      uint32_t again = __ballot_sync(0xFFFFFFFFu, bad && live && m == m);
+      if (again && lane == 0) atomicAdd(&cs->busy, 1u);
+      const bool looked = again != 0u;
       while (again) {
         const int r = __ffs(again) - 1;
         again &= again - 1;
@@ -663,6 +673,31 @@ __global__ void __launch_bounds__(kWinThreads, 1)
         const int64_t orr = __shfl_sync(0xFFFFFFFFu, orow, r);
         const int64_t stride = (int64_t)p.Hk * D;
         const int64_t first = (int64_t)it.b * p.T * stride + (int64_t)it.hk * D;
+        // the keys that its blocks have brought
+        const int last_s = it.blocks - 1, last_w = it.win_blocks - 1;
+        const int w_end = last_w < 0 ? it.span.base
+                                     : min(it.len, block_key(it, last_w) +
+                                                       columns(block_keys(it, last_w)));
+        const int s_end = last_s == last_w ? it.sink_base
+                                           : min(min(it.len, p.sinks),
+                                                 block_key(it, last_s) +
+                                                     columns(block_keys(it, last_s)));
+        if (!unseen_bad<D>(p.v + first, stride, it.span.base, w_end, tr, p.window, p.sinks, lane) &&
+            !unseen_bad<D>(p.v + first, stride, it.sink_base, s_end, tr, p.window, p.sinks, lane))
+          continue;
+        uint32_t nans = 0u;
+#pragma unroll
+        for (int e = 0; e < D / 32; ++e) {
+          const int d = lane * (D / 32) + e;
+          const float x = whole ? __uint_as_float((uint32_t)p.out[orr * D + d] << 16)
+                                : p.part_o[(orr * p.splits + it.chunk) * D + d];
+          nans |= (uint32_t)(x != x) << e;
+        }
+        nans = unexplained<D>(p.v + first, stride, it.span.base, it.span.end, tr, it.len, p.window,
+                              p.sinks, lane, nans);
+        nans = unexplained<D>(p.v + first, stride, it.sink_base, it.span.sink_end, tr, it.len,
+                              p.window, p.sinks, lane, nans);
+        if (!__any_sync(0xFFFFFFFFu, nans != 0u)) continue;
         float rm = neg_inf(), rl = 0.0f, ro[D / 32];
 #pragma unroll
         for (int e = 0; e < D / 32; ++e) ro[e] = 0.0f;
@@ -686,6 +721,8 @@ __global__ void __launch_bounds__(kWinThreads, 1)
         if (lane == 0 && p.lse)
           p.lse[orr] = rl == 0.0f ? neg_inf() : (rm + log2f(rl)) * 0.6931471805599453f;
       }
+      __syncwarp();
+      if (looked && lane == 0) atomicSub(&cs->busy, 1u);
     }
   }
 
@@ -751,14 +788,14 @@ auto window_tiles(const WinParams& p) {
 size_t window_tiles_smem(int D) { return D == 128 ? WinCfg<128>::kSmem : WinCfg<64>::kSmem; }
 
 cudaError_t launch_window_tiles(const CUtensorMap& tm_q, const CUtensorMap& tm_k,
-                                const CUtensorMap& tm_v, const WinParams& p, int D, int grid,
-                                cudaStream_t stream) {
+                                const CUtensorMap& tm_v, const CUtensorMap& tm_vs,
+                                const WinParams& p, int D, int grid, cudaStream_t stream) {
   const size_t smem = window_tiles_smem(D);
   const auto fn = D == 128 ? window_tiles<128>(p) : window_tiles<64>(p);
   const cudaError_t e =
       cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;
-  fn<<<grid, kWinThreads, smem, stream>>>(tm_q, tm_k, tm_v, p);
+  fn<<<grid, kWinThreads, smem, stream>>>(tm_q, tm_k, tm_v, tm_vs, p);
   if (p.splits > 1) {
     const unsigned ctas = (unsigned)(((int64_t)p.B * p.S * p.H + 3) / 4);
     if (D == 128)

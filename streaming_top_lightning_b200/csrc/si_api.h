@@ -38,9 +38,9 @@ int make_map(CUtensorMap* m, const void* base, CUtensorMapDataType dt, uint64_t 
 
 // Tensor map of a bf16 [d3, d2, d1, d0] tensor (d0 fastest) with 64-element
 // rows in the 128-byte swizzle: a {64, box1, box2, 1} box; what lies outside
-// reads as zero.
+// reads as zero.  d2 of pitch2 such planes are in it.
 int make_map4(CUtensorMap* m, const void* base, uint64_t d0, uint64_t d1, uint64_t d2, uint64_t d3,
-              uint32_t box1, uint32_t box2);
+              uint32_t box1, uint32_t box2, uint64_t pitch2);
 
 struct Opts {
   int key_chunk, scratch_mb, grid_ctas, timeout_ms, debug_flags, row_finish, key_tile,

@@ -339,37 +339,106 @@ SI_DEV uint32_t below(int n) { return n >= 32 ? 0xFFFFFFFFu : (n <= 0 ? 0u : (1u
 
 SI_DEV void fence_async() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 
+// Kernels that multiply whole tiles give a row NaN when the value of a key that
+// it does not see holds an infinity or NaN (0 times that value).  Rows that came
+// out NaN are looked at by a whole warp, D/32 elements of a bf16 row per lane:
+// where unseen_bad finds such a value, and a NaN of the row is not one that it has
+// seen itself (unexplained), the row is computed again (exact_row_keys).  A key
+// is unseen by some row of a tile, but in its blocks, for a few tiles only, so
+// one bad value costs a few tiles' rows however many see it.  (B200, 8,192 queries
+// of 64 heads, window 1,024, 0.30 ms: with a NaN token among the sinks 0.8 ms, with
+// one elsewhere 8.3, the time of one tile's rows; 169 and 172 when every row that
+// came out NaN was computed again.)
+template <int D>
+SI_DEV uint2 value_bits(const uint16_t* v, int lane) {
+  if constexpr (D == 128) return __ldg(reinterpret_cast<const uint2*>(v) + lane);
+  return make_uint2(__ldg(reinterpret_cast<const uint32_t*>(v) + lane), 0u);
+}
+
+// Whether one of the keys [lo, hi) that the query at t does not see has a value
+// that is not finite.
+template <int D>
+SI_DEV bool unseen_bad(const uint16_t* v, int64_t key_stride, int lo, int hi, int t, int window,
+                       int sinks, int lane) {
+  uint32_t bad = 0u;
+#pragma unroll 1
+  for (int part = 0; part < 2; ++part) {
+    const int a = part ? max(lo, t + 1) : max(lo, sinks);
+    const int b = part ? hi : min(hi, t - window + 1);
+#pragma unroll 4
+    for (int j = a; j < b; ++j) {
+      const uint2 w = value_bits<D>(v + j * key_stride, lane);
+      // an exponent of ones carries into the sign's place
+      bad |= (((w.x & 0x7F807F80u) + 0x00800080u) | ((w.y & 0x7F807F80u) + 0x00800080u)) & 0x80008000u;
+    }
+  }
+  return __any_sync(0xFFFFFFFFu, bad != 0u);
+}
+
+// Of a lane's elements in `nans` those that are not NaN in any key of [lo, hi)
+// that the query sees.
+template <int D>
+SI_DEV uint32_t unexplained(const uint16_t* v, int64_t key_stride, int lo, int hi, int t, int len,
+                            int window, int sinks, int lane, uint32_t nans) {
+  for (int j0 = lo; j0 < hi && __any_sync(0xFFFFFFFFu, nans != 0u); j0 += 8) {
+    uint2 w[8];  // asked for together
+#pragma unroll
+    for (int x = 0; x < 8; ++x)
+      w[x] = value_bits<D>(v + (int64_t)min(j0 + x, hi - 1) * key_stride, lane);
+#pragma unroll
+    for (int x = 0; x < 8; ++x) {
+      if (j0 + x >= hi || !sees(j0 + x, t, len, window, sinks)) continue;
+#pragma unroll
+      for (int e = 0; e < D / 32; ++e)
+        if ((((e < 2 ? w[x].x : w[x].y) >> (16 * (e & 1))) & 0x7FFFu) > 0x7F80u) nans &= ~(1u << e);
+    }
+  }
+  return nans;
+}
+
 // One query row by the formula, by a whole warp: the keys [j_lo, j_hi) of a
-// bf16 source that the row sees, D/32 dims per lane.  Kernels that multiply
-// whole tiles give a row NaN when a key that it does not see holds an infinity
-// or NaN (0 times that value); such rows are computed again here.
+// bf16 source that the row sees.
 template <int D>
 SI_DEV void exact_row_keys(const uint16_t* qr, const uint16_t* k, const uint16_t* v,
                            int64_t key_stride, int j_lo, int j_hi, int t, int len, int window,
                            int sinks, float scale_log2, int lane, float& m, float& l,
                            float (&o)[D / 32]) {
-  for (int j = j_lo; j < j_hi; ++j) {
-    if (!sees(j, t, len, window, sinks)) continue;
-    float dot = 0.0f;
+  const uint2 qw = value_bits<D>(qr, lane);
+  for (int j0 = j_lo; j0 < j_hi; j0 += 8) {
+    uint2 kw[8], vw[8];  // asked for together; keys that the row does not see are not used
+    float dot[8];
 #pragma unroll
-    for (int e = 0; e < D / 32; ++e) {
-      const int d = lane * (D / 32) + e;
-      dot = fmaf(__uint_as_float((uint32_t)qr[d] << 16),
-                 __uint_as_float((uint32_t)k[j * key_stride + d] << 16), dot);
+    for (int x = 0; x < 8; ++x) {
+      const int64_t at = (int64_t)min(j0 + x, j_hi - 1) * key_stride;
+      kw[x] = value_bits<D>(k + at, lane);
+      vw[x] = value_bits<D>(v + at, lane);
     }
 #pragma unroll
-    for (int x = 16; x > 0; x >>= 1) dot += __shfl_xor_sync(0xFFFFFFFFu, dot, x);
-    const float s = dot * scale_log2;
-    const float mn = fmaxf(m, s);  // ignores a NaN score, which makes the weight NaN below
-    const float a = mn == neg_inf() ? 1.0f : ex2(m - mn);
-    const float w = mn == neg_inf() && s == s ? 0.0f : ex2(s - mn);
-    l = l * a + w;
-#pragma unroll
-    for (int e = 0; e < D / 32; ++e) {
-      const float vv = __uint_as_float((uint32_t)v[j * key_stride + lane * (D / 32) + e] << 16);
-      o[e] = fmaf(o[e], a, w * vv);
+    for (int x = 0; x < 8; ++x) {
+      dot[x] = fmaf(bf16_hi(qw.x), bf16_hi(kw[x].x), bf16_lo(qw.x) * bf16_lo(kw[x].x));
+      if (D == 128)
+        dot[x] = fmaf(bf16_hi(qw.y), bf16_hi(kw[x].y),
+                      fmaf(bf16_lo(qw.y), bf16_lo(kw[x].y), dot[x]));
     }
-    m = mn;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1)
+#pragma unroll
+      for (int x = 0; x < 8; ++x) dot[x] += __shfl_xor_sync(0xFFFFFFFFu, dot[x], o);
+#pragma unroll
+    for (int x = 0; x < 8; ++x) {
+      if (j0 + x >= j_hi || !sees(j0 + x, t, len, window, sinks)) continue;
+      const float s = dot[x] * scale_log2;
+      const float mn = fmaxf(m, s);  // ignores a NaN score, which makes the weight NaN below
+      const float a = mn == neg_inf() ? 1.0f : ex2(m - mn);
+      const float w = mn == neg_inf() && s == s ? 0.0f : ex2(s - mn);
+      l = l * a + w;
+#pragma unroll
+      for (int e = 0; e < D / 32; ++e) {
+        const uint32_t two = e < 2 ? vw[x].x : vw[x].y;
+        o[e] = fmaf(o[e], a, w * ((e & 1) ? bf16_hi(two) : bf16_lo(two)));
+      }
+      m = mn;
+    }
   }
 }
 

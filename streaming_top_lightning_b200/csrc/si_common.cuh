@@ -67,6 +67,9 @@ struct Ctl {
   volatile uint32_t* abort;  // CTA-wide abort flag in shared memory
   uint64_t timeout_ns;       // limit for any single wait
   unsigned long long* role;  // [grid][kRoleSlots] counters (profiling build), else null
+  // in shared memory, or null: while it is not zero a warp is at work whose length
+  // has nothing to do with the limit, and the waits' clocks stand still
+  volatile uint32_t* busy = nullptr;
 };
 
 SI_DEV long long role_t0() {
@@ -150,12 +153,14 @@ SI_DEV bool mbar_wait(uint32_t bar, uint32_t parity, const Ctl& c, int slot = -1
 }
 SI_DEV bool mbar_wait_(uint32_t bar, uint32_t parity, const Ctl& c) {
   if (mbar_try_wait(bar, parity)) return true;
-  const uint64_t t0 = globaltimer();
+  uint64_t t0 = globaltimer();
   uint32_t n = 0;
   while (!mbar_try_wait(bar, parity)) {
     if ((++n & 15u) == 0u) {
       if (*c.abort) return false;
-      if (globaltimer() - t0 > c.timeout_ns) {
+      if (c.busy && *c.busy) {
+        t0 = globaltimer();
+      } else if (globaltimer() - t0 > c.timeout_ns) {
         raise_abort(c, SI_DEVERR_TIMEOUT);
         return false;
       }
@@ -188,7 +193,7 @@ SI_DEV bool mbar_wait_warp_(uint32_t bar, uint32_t parity, const Ctl& c) {
     if ((n & 15u) == 15u) {
       int stop = 0;
       if (lane == 0) {
-        if (t0 == 0) t0 = globaltimer();
+        if (t0 == 0 || (c.busy && *c.busy)) t0 = globaltimer();
         if (*c.abort) {
           stop = 1;
         } else if (globaltimer() - t0 > c.timeout_ns) {

@@ -170,9 +170,10 @@ struct WinParams {
   int debug_flags;            // bit 0: the first K block is never loaded (timeout test)
 };
 size_t window_tiles_smem(int D);
+// tm_vs: the sinks' values alone.
 cudaError_t launch_window_tiles(const CUtensorMap& tm_q, const CUtensorMap& tm_k,
-                                const CUtensorMap& tm_v, const WinParams& p, int D, int grid,
-                                cudaStream_t stream);
+                                const CUtensorMap& tm_v, const CUtensorMap& tm_vs,
+                                const WinParams& p, int D, int grid, cudaStream_t stream);
 
 // Rows of a 4-bit paged cache (k_cache4.cu): append reads k, v [B,S,Hk,D]
 // bf16, read writes k_out, v_out of that shape.
