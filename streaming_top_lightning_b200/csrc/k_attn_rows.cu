@@ -44,7 +44,9 @@
 // up to 8,192 keys, 55 us, 2.8 TB/s of the 6.6 that a copy reaches: the warps'
 // instructions (about 800 for 32 keys: codes to fp16, products, transpositions)
 // take 59 % of the issue slots and half of the ALUs' time.  Five CTAs an SM with
-// two stages took 64 us, shares weighted by a CTA's start 60.
+// two stages took 64 us, shares weighted by a CTA's start 60.  Tiles of 16 rows of
+// 128 elements spill 96 to 224 bytes a thread at three CTAs an SM, 8-row tiles up to
+// 24 at four, 32-row tiles 208 at 255 registers.
 //
 // bf16 keys: bf16 products, probabilities rounded to bf16 (2^-8).  The output is
 // divided by the sum of the probabilities as rounded, so that a weight near one
@@ -173,11 +175,10 @@ struct Cache4 {
   }
 
   // O^T += V^T P^T over 16 keys; MASKED: `live` says which keys of the group may
-  // be read (the others' codes count as zero), `nans` which keys' NaN scales
-  // count as zero here.
+  // be read (the others' codes count as zero).
   template <bool MASKED>
   SI_DEV void values(uint32_t vc, uint32_t vs, int lane, const uint32_t (&pf)[NT][2], uint32_t live,
-                     uint32_t nans, RowState<D, NT>& st) const {
+                     RowState<D, NT>& st) const {
     const int n = lane >> 2, c = lane & 3;
     uint32_t sp[2], w[4][D / 64];
 #pragma unroll
@@ -198,7 +199,6 @@ struct Cache4 {
           asm volatile("ld.shared.u8 %0, [%1];" : "=r"(b[i]) : "r"(vs + key * 4 + (n >> 1)));
         }
         if (MASKED && !((live >> key) & 1u)) b[i] = 0u;
-        if (MASKED && ((nans >> key) & 1u) && e4m3_nan(b[i])) b[i] = 0u;
       }
       sp[t] = e4m3x2(__byte_perm(b[0], b[1], 0x0040));
     }
@@ -284,6 +284,70 @@ struct Bf16Rows {
 
   static SI_DEV int element(int i, int r, int h) { return 16 * i + r + 8 * h; }
 };
+
+// exact_row_keys for the keys [s_lo, s_hi) and [w_lo, w_hi) of a row's sequence in
+// 4-bit pages; the results to out [D] and ml.  (A call: inline, drafted tokens
+// took 10.8 us for 10.3.)
+template <int D>
+__device__ __noinline__ void exact_row_pages(const uint16_t* qr, const int32_t* table,
+                                             const uint8_t* head, int64_t page_bytes, int n_pages,
+                                             int page_shift, int s_lo, int s_hi, int w_lo, int w_hi,
+                                             int t, int len, int window, int sinks,
+                                             float scale_log2, float* out, float2* ml) {
+  const int page = 1 << page_shift, lane = threadIdx.x & 31;
+  const uint2 qw = value_bits<D>(qr, lane);
+  float m = neg_inf(), l = 0.0f, o[D / 32];
+#pragma unroll
+  for (int e = 0; e < D / 32; ++e) o[e] = 0.0f;
+  // The lane's elements of a row from its codes and scale.  An E2M1 number's lower
+  // bits are the fp16 number 2^-14 of it.
+  auto numbers = [&](const uint8_t* codes, const uint8_t* scales, float (&x)[D / 32]) {
+    const uint32_t c = D == 128 ? (uint32_t)__ldg(reinterpret_cast<const uint16_t*>(codes) + lane)
+                                : (uint32_t)__ldg(codes + lane);
+    const float f = __half2float(__ushort_as_half(
+                        (uint16_t)e4m3x2((uint32_t)__ldg(scales + lane * (D / 32) / 16)))) *
+                    16384.0f;
+#pragma unroll
+    for (int e = 0; e < D / 32; ++e) {
+      const uint32_t n = c >> (4 * e);
+      x[e] = __half2float(__ushort_as_half((uint16_t)((n & 7u) << 9 | (n & 8u) << 12))) * f;
+    }
+  };
+#pragma unroll 1
+  for (int part = 0; part < 2; ++part) {
+    const int j_hi = part ? w_hi : s_hi;
+#pragma unroll 1
+    for (int j0 = part ? w_lo : s_lo; j0 < j_hi; j0 += 4) {
+      float dot[4], v[4][D / 32];
+      bool see[4];
+#pragma unroll
+      for (int x = 0; x < 4; ++x) {
+        const int j = j0 + x;
+        see[x] = j < j_hi && sees(j, t, len, window, sinks);
+        const int pg = see[x] ? __ldg(table + (j >> page_shift)) : -1;
+        see[x] = see[x] && pg >= 0 && pg < n_pages;
+        const int slot = see[x] ? j & (page - 1) : 0;
+        const uint8_t* kc = head + (int64_t)(see[x] ? pg : 0) * page_bytes + slot * (D / 2);
+        const uint8_t* ks = kc - slot * (D / 2) + page * D + slot * (D / 16);
+        float k[D / 32];
+        numbers(kc, ks, k);
+        numbers(kc + page * (D / 2), ks + page * (D / 16), v[x]);
+        dot[x] = bf16_lo(qw.x) * k[0] + bf16_hi(qw.x) * k[1];
+        if constexpr (D == 128) dot[x] += bf16_lo(qw.y) * k[2] + bf16_hi(qw.y) * k[3];
+      }
+#pragma unroll
+      for (int i = 16; i > 0; i >>= 1)
+#pragma unroll
+        for (int x = 0; x < 4; ++x) dot[x] += __shfl_xor_sync(0xFFFFFFFFu, dot[x], i);
+#pragma unroll
+      for (int x = 0; x < 4; ++x)
+        if (see[x]) exact_key<D>(dot[x] * scale_log2, v[x], m, l, o);
+    }
+  }
+#pragma unroll
+  for (int e = 0; e < D / 32; ++e) out[lane * (D / 32) + e] = o[e];
+  if (lane == 0) *ml = make_float2(m, l);
+}
 
 // MODE 0: bf16 keys; 1: 4-bit pages; 2: 4-bit pages, listed entries.
 template <int D, int MODE, int NT>
@@ -388,11 +452,13 @@ constexpr int row_ctas() {
 
 }  // namespace
 
-template <int D, int MODE, int NT>
+// MANY: calls of several queries a sequence, whose tiles' rows may see different
+// keys (bf16 keys: every call).  Over 4-bit pages a decode batch takes 55.7 us with
+// the code for that and 54.7 without.
+template <int D, int MODE, int NT, bool MANY>
 __global__ void __launch_bounds__(kRowWarps * 32, row_ctas<D, MODE, NT>())
     k_attn_rows(const __grid_constant__ RowsParams p) {
   using Src = Source<D, MODE, NT>;
-  using Src4 = Cache4<D, NT>;
   constexpr int KS = Src::KS, NST = Src::kStages, NG = KS / 16, RT = 8 * NT;
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ float sh_m[kRowWarps][RT], sh_l[kRowWarps][RT];
@@ -584,23 +650,6 @@ __global__ void __launch_bounds__(kRowWarps * 32, row_ctas<D, MODE, NT>())
       live = __ballot_sync(0xFFFFFFFFu,
                            ((vm >> lane) & 1u) && span_holds(span, u, j0 + lane, p.sinks));
     if constexpr (MASKED && MODE == 2) live = vm;
-    // Keys that have a NaN among their value scales, where rows see different
-    // keys: a weight of zero times it would be NaN.  They count as zero in the
-    // products, and the rows that see them get their NaN below.
-    uint32_t nans = 0u;
-    const uint32_t v_scales = at + 2 * Src4::kCodes + Src4::kScales;
-    if constexpr (MASKED && MODE == 1) {
-      if (ti.t_min != ti.t_max) {
-        uint32_t any = 0u;
-#pragma unroll
-        for (int i = 0; i < D / 64; ++i) {
-          uint32_t w;
-          asm volatile("ld.shared.b32 %0, [%1];" : "=r"(w) : "r"(v_scales + lane * (D / 16) + 4 * i));
-          any |= e4m3_nans(w);
-        }
-        nans = __ballot_sync(0xFFFFFFFFu, any != 0u) & live;
-      }
-    }
     // scores to log2 units, unseen keys to -inf
     float mx[NT][2];
 #pragma unroll
@@ -686,26 +735,7 @@ __global__ void __launch_bounds__(kRowWarps * 32, row_ctas<D, MODE, NT>())
       else
         src.template values<MASKED>(at + Src::kCodes + g * 8 * D,
                                     at + 2 * Src::kCodes + Src::kScales + g * D, lane, pf,
-                                    live >> (16 * g), nans >> (16 * g), st);
-    }
-    if constexpr (MASKED && MODE == 1) {
-      for (uint32_t left = nans; left; left &= left - 1u) {
-        // a thread's elements of a row lie in one block of 16
-        const int key = __ffs((int)left) - 1;
-        uint32_t b;
-        asm volatile("ld.shared.u8 %0, [%1];" : "=r"(b) : "r"(v_scales + key * (D / 16) + r * D / 128));
-        if (!e4m3_nan(b)) continue;
-#pragma unroll
-        for (int x = 0; x < NT; ++x)
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const int t = ti.len - ti.q_len + (ti.row0 + min(8 * x + 2 * c + e, ti.rows - 1)) / p.G;
-            if (!sees(j0 + key, t, ti.len, p.window, p.sinks)) continue;
-#pragma unroll
-            for (int i = 0; i < D / 16; ++i)
-              st.o[x][i][e] = st.o[x][i][2 + e] = __int_as_float(0x7FC00000);
-          }
-      }
+                                    live >> (16 * g), st);
     }
   };
 
@@ -810,16 +840,17 @@ __global__ void __launch_bounds__(kRowWarps * 32, row_ctas<D, MODE, NT>())
     const float fit = sum == 0.0f ? 0.0f : __fdividef(sum, rsum);
 #pragma unroll
     for (int i = 0; i < kPer; ++i) o[i] *= fit;
+  }
+  // Rows that are NaN by a value that they do not see, by the formula (si_attn.cuh).
+  // Rows of one query see the same keys; where the sum is NaN too, a score that the
+  // row sees is.
+  if (MANY && ti.t_min != ti.t_max) {
     bool bad = false;
 #pragma unroll
     for (int i = 0; i < kPer; ++i) bad |= o[i] != o[i];
-    // (rows whose weights are NaN are so by what they see, and rows of one query
-    // see the same keys)
-    if (bad && row < ti.rows && sum == sum && ti.t_min != ti.t_max) atomicOr(&sh_nan, 1u << row);
+    if (bad && row < ti.rows && sum == sum) atomicOr(&sh_nan, 1u << row);
     __syncthreads();
-    if (sh_nan) {  // rows by the formula (si_attn.cuh)
-      const int64_t stride = (int64_t)p.Hk * D;
-      const int64_t first = ((int64_t)ti.b * p.T) * stride + (int64_t)ti.hk * D;
+    if (sh_nan) {
       // the keys that the steps have brought
       const int u_w = max(u_lo, span.sink_steps), ss = span.sink_steps;
       const int w_lo = step_key<KS>(span, u_w), w_hi = min(span.end, step_key<KS>(span, max(u_hi, ss)));
@@ -827,49 +858,56 @@ __global__ void __launch_bounds__(kRowWarps * 32, row_ctas<D, MODE, NT>())
       for (int x = warp; x < ti.rows; x += kRowWarps) {
         if (!((sh_nan >> x) & 1u)) continue;
         const int t = ti.len - ti.q_len + (ti.row0 + x) / p.G;
-        uint32_t nans = 0u;
-        if (unseen_bad<D>(p.v + first, stride, max(w_lo, span.lo), w_hi, t, p.window, p.sinks,
-                          lane) ||
-            unseen_bad<D>(p.v + first, stride, s_lo, s_hi, t, p.window, p.sinks, lane)) {
+        const uint16_t* qr = p.q + out_row(p, ti, ti.row0 + x) * D;
+        if constexpr (MODE == 1) {
+          exact_row_pages<D>(qr, p.table + (int64_t)ti.b * p.width,
+                             p.pages + (int64_t)ti.hk * cache4_block<D>(page), p.page_bytes, p.n_pages, p.page_shift, s_lo,
+                             s_hi, w_lo, w_hi, t, ti.len, p.window, p.sinks, p.scale_log2,
+                             sh_o + x * kPad, reinterpret_cast<float2*>(sh_o + x * kPad + D));
+        } else {
+          const int64_t stride = (int64_t)p.Hk * D;
+          const int64_t first = ((int64_t)ti.b * p.T) * stride + (int64_t)ti.hk * D;
+          uint32_t nans = 0u;
+          if (unseen_bad<D>(p.v + first, stride, max(w_lo, span.lo), w_hi, t, p.window, p.sinks,
+                            lane) ||
+              unseen_bad<D>(p.v + first, stride, s_lo, s_hi, t, p.window, p.sinks, lane)) {
 #pragma unroll
-          for (int e = 0; e < D / 32; ++e) {
-            float y = 0.0f;
+            for (int e = 0; e < D / 32; ++e) {
+              float y = 0.0f;
 #pragma unroll
-            for (int w = 0; w < kRowWarps; ++w)
-              y += sh_o[(w * RT + x) * kPad + lane * (D / 32) + e];
-            nans |= (uint32_t)(y != y) << e;
+              for (int w = 0; w < kRowWarps; ++w)
+                y += sh_o[(w * RT + x) * kPad + lane * (D / 32) + e];
+              nans |= (uint32_t)(y != y) << e;
+            }
+            nans = unexplained<D>(p.v + first, stride, w_lo, w_hi, t, ti.len, p.window, p.sinks,
+                                  lane, nans);
+            nans = unexplained<D>(p.v + first, stride, s_lo, s_hi, t, ti.len, p.window, p.sinks,
+                                  lane, nans);
           }
-          nans = unexplained<D>(p.v + first, stride, w_lo, w_hi, t, ti.len, p.window, p.sinks, lane,
-                                nans);
-          nans = unexplained<D>(p.v + first, stride, s_lo, s_hi, t, ti.len, p.window, p.sinks, lane,
-                                nans);
-        }
-        if (!__any_sync(0xFFFFFFFFu, nans != 0u)) {
-          if (lane == 0) atomicAnd(&sh_nan, ~(1u << x));
-          continue;
-        }
-        float m = neg_inf(), l = 0.0f, acc[D / 32];
+          if (!__any_sync(0xFFFFFFFFu, nans != 0u)) {
+            if (lane == 0) atomicAnd(&sh_nan, ~(1u << x));
+            continue;
+          }
+          float m = neg_inf(), l = 0.0f, acc[D / 32];
 #pragma unroll
-        for (int e = 0; e < D / 32; ++e) acc[e] = 0.0f;
-        for (int u = u_lo; u < u_hi; ++u) {
-          const int j0 = step_key<KS>(span, u);
-          const int hi = min(j0 + KS, u < span.sink_steps ? span.sink_end : span.end);
-          exact_row_keys<D>(p.q + out_row(p, ti, ti.row0 + x) * D, p.k + first, p.v + first, stride,
-                            j0, hi, t, ti.len, p.window, p.sinks, p.scale_log2, lane, m, l, acc);
-        }
+          for (int e = 0; e < D / 32; ++e) acc[e] = 0.0f;
+          exact_row_keys<D>(qr, p.k + first, p.v + first, stride, s_lo, s_hi, t, ti.len, p.window,
+                            p.sinks, p.scale_log2, lane, m, l, acc);
+          exact_row_keys<D>(qr, p.k + first, p.v + first, stride, w_lo, w_hi, t, ti.len, p.window,
+                            p.sinks, p.scale_log2, lane, m, l, acc);
 #pragma unroll
-        for (int e = 0; e < D / 32; ++e) sh_o[x * kPad + lane * (D / 32) + e] = acc[e];
-        if (lane == 0) {
-          sh_m[0][x] = m;
-          sh_l[0][x] = l;
+          for (int e = 0; e < D / 32; ++e) sh_o[x * kPad + lane * (D / 32) + e] = acc[e];
+          if (lane == 0) *reinterpret_cast<float2*>(sh_o + x * kPad + D) = make_float2(m, l);
         }
       }
       __syncthreads();
       if ((sh_nan >> row) & 1u) {
-        top = sh_m[0][row];
-        sum = sh_l[0][row];
+        // in the weights' units, 2^kProbShift over 4-bit pages
+        const float unit = MODE == 1 ? 1024.0f : 1.0f;
+        top = sh_o[row * kPad + D];
+        sum = sh_o[row * kPad + D + 1] * unit;
 #pragma unroll
-        for (int i = 0; i < kPer; ++i) o[i] = sh_o[row * kPad + part * kPer + i];
+        for (int i = 0; i < kPer; ++i) o[i] = sh_o[row * kPad + part * kPer + i] * unit;
       }
     }
   }
@@ -1067,11 +1105,11 @@ cudaError_t launch_join(const RowsParams& p, cudaStream_t stream) {
       &cfg, few ? k_attn_join<D, KS, RT, 1, SHARED> : k_attn_join<D, KS, RT, 4, SHARED>, p);
 }
 
-template <int D, int MODE, int NT>
+template <int D, int MODE, int NT, bool MANY>
 cudaError_t launch(const RowsParams& p, cudaStream_t stream) {
   using Src = Source<D, MODE, NT>;
   constexpr size_t smem = row_smem<D, MODE, NT>();
-  cudaError_t e = cudaFuncSetAttribute(k_attn_rows<D, MODE, NT>,
+  cudaError_t e = cudaFuncSetAttribute(k_attn_rows<D, MODE, NT, MANY>,
                                        cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;
   const int64_t ctas =
@@ -1087,7 +1125,7 @@ cudaError_t launch(const RowsParams& p, cudaStream_t stream) {
   attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
   cfg.attrs = &attr;
   cfg.numAttrs = p.share == kCluster ? 1 : 0;
-  e = cudaLaunchKernelEx(&cfg, k_attn_rows<D, MODE, NT>, p);
+  e = cudaLaunchKernelEx(&cfg, k_attn_rows<D, MODE, NT, MANY>, p);
   if (e != cudaSuccess || p.share != kShared) return e;
   return launch_join<D, Src::KS, 8 * NT, true>(p, stream);
 }
@@ -1095,8 +1133,12 @@ cudaError_t launch(const RowsParams& p, cudaStream_t stream) {
 template <int D, int MODE>
 cudaError_t launch_nt(const RowsParams& p, cudaStream_t stream) {
   if constexpr (MODE == 0)
-    if (p.row_tile == 32) return launch<D, MODE, 4>(p, stream);
-  return p.row_tile == 8 ? launch<D, MODE, 1>(p, stream) : launch<D, MODE, 2>(p, stream);
+    if (p.row_tile == 32) return launch<D, MODE, 4, true>(p, stream);
+  if (MODE == 0 || (MODE == 1 && p.S > 1))
+    return p.row_tile == 8 ? launch<D, MODE, 1, MODE != 2>(p, stream)
+                           : launch<D, MODE, 2, MODE != 2>(p, stream);
+  return p.row_tile == 8 ? launch<D, MODE, 1, MODE == 0>(p, stream)
+                         : launch<D, MODE, 2, MODE == 0>(p, stream);
 }
 
 }  // namespace

@@ -396,6 +396,18 @@ SI_DEV uint32_t unexplained(const uint16_t* v, int64_t key_stride, int lo, int h
   return nans;
 }
 
+// A key of score s (log2 units) into a row's running maximum, sum and values.
+template <int D>
+SI_DEV void exact_key(float s, const float (&v)[D / 32], float& m, float& l, float (&o)[D / 32]) {
+  const float mn = fmaxf(m, s);  // ignores a NaN score, which makes the weight NaN below
+  const float a = mn == neg_inf() ? 1.0f : ex2(m - mn);
+  const float w = mn == neg_inf() && s == s ? 0.0f : ex2(s - mn);
+  l = l * a + w;
+#pragma unroll
+  for (int e = 0; e < D / 32; ++e) o[e] = fmaf(o[e], a, w * v[e]);
+  m = mn;
+}
+
 // One query row by the formula, by a whole warp: the keys [j_lo, j_hi) of a
 // bf16 source that the row sees.
 template <int D>
@@ -427,17 +439,13 @@ SI_DEV void exact_row_keys(const uint16_t* qr, const uint16_t* k, const uint16_t
 #pragma unroll
     for (int x = 0; x < 8; ++x) {
       if (j0 + x >= j_hi || !sees(j0 + x, t, len, window, sinks)) continue;
-      const float s = dot[x] * scale_log2;
-      const float mn = fmaxf(m, s);  // ignores a NaN score, which makes the weight NaN below
-      const float a = mn == neg_inf() ? 1.0f : ex2(m - mn);
-      const float w = mn == neg_inf() && s == s ? 0.0f : ex2(s - mn);
-      l = l * a + w;
+      float vv[D / 32];
 #pragma unroll
       for (int e = 0; e < D / 32; ++e) {
         const uint32_t two = e < 2 ? vw[x].x : vw[x].y;
-        o[e] = fmaf(o[e], a, w * ((e & 1) ? bf16_hi(two) : bf16_lo(two)));
+        vv[e] = (e & 1) ? bf16_hi(two) : bf16_lo(two);
       }
-      m = mn;
+      exact_key<D>(dot[x] * scale_log2, vv, m, l, o);
     }
   }
 }
