@@ -337,7 +337,9 @@ int si_sparse_attention(const void* qa, const void* ka, const void* va, const in
 /*
  * si_window_attention: each query attends to the most recent tokens of its
  * sequence and to its first few (the sinks), the branch of a sparse-attention
- * layer beside the selected entries.  Row i of batch b (i < q_lens[b]) is the
+ * layer beside the selected entries.  The caller joins it with a result over other
+ * keys by the two lse: those of si_cache4_attention; si_sparse_attention gives
+ * none.  Row i of batch b (i < q_lens[b]) is the
  * token at position t = lens[b] - q_lens[b] + i: the call's queries are the
  * newest tokens of their sequences, a whole prompt (q_lens = lens), a chunk of
  * one, or a single token.  Query head h reads kv head h / (H / H_k):

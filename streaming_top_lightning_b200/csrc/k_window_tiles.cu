@@ -15,17 +15,16 @@
 // key block is loaded once for 256 rows, and the softmax of one tile runs while
 // the tensor cores work for the other:
 //   warp 0       K and V blocks by TMA into a ring, in the order of use
-//                (K0 V0 K1 V1 ...); rows of V past the sequence's end are
-//                overwritten with zeros (0 times whatever they hold would
+//                (K0 K1 V0 K2 V1 K3 ...); rows of V past the sequence's end
+//                are overwritten with zeros (0 times whatever they hold would
 //                reach the sums)
 //   warp 2       the two Q tiles by TMA
-//   warp 1       S_i = Q_i K^T into TMEM, then O_i += P_i V with P_i read from
-//                TMEM: PV_0(n-1) S_0(n) PV_1(n-1) S_1(n) ...  An MMA's
-//                completion covers those before it, so when S_i(n) is there
-//                O_i holds everything up to n-1 and nobody writes it.
-//   warps 4-11   softmax, four warps a tile, a thread a row: the maximum over
-//                the tile's columns, then P = 2^(s - m) in bf16 over the first
-//                half of S's columns (the columns read by then), and the row's
+//   warps 1, 3   a tile each: S = Q K^T of a block into one of two buffers in
+//                TMEM, two blocks ahead of the softmax, then O += P V with P
+//                read from TMEM
+//   warps 4-11   softmax, four warps a tile, a thread a row: the block's 64
+//                scores to registers, their maximum, then P = 2^(s - m) in bf16
+//                over the first half of the buffer's columns, and the row's
 //                sum.  O is rescaled only when a row's maximum has grown by more
 //                than 2^16 since it was last fixed: bf16 and fp32 keep their
 //                relative precision up there.  The output is divided by the sum
@@ -33,7 +32,7 @@
 //                its rounding (error against 64 bits on rows with a few large
 //                logits: 0.0023 of the norm with the unrounded sum, which lse
 //                takes, 0.0016 being the output's own rounding).
-// Keys are taken from the first one that the pair of tiles sees, 128 at a time,
+// Keys are taken from the first one that the pair of tiles sees, 64 at a time,
 // the last block and the sinks' block cut to multiples of 32 columns, so a
 // window costs about its own length and not whole tiles of it.  Only columns
 // that a boundary crosses are compared with positions.
@@ -51,7 +50,9 @@
 // Measured on B200: 8,192 queries of 64 heads, 8 kv heads, D = 128, window 1,024
 // take 293 us in a burst (880 TFLOP/s) and 331-337 sustained at the power limit
 // (770 TFLOP/s); the tensor cores alone would take 156 at the dense peak.  They
-// are active for 46 % of the time and the exponentials' unit for 47 %.  Before,
+// are active for 46 % of the time and the exponentials' unit for 47 %: two softmax
+// warps a scheduler do not hide one another's chains (scores from TMEM, maximum,
+// exponentials, store), and the two units work in turn more than at once.  Before,
 // with 128-key blocks and one score buffer 489, scores read from TMEM twice 510.
 // A part of the exponentials as polynomials on the FMA units gave nothing under
 // the power limit and is not kept.
