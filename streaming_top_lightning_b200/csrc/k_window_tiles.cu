@@ -683,8 +683,10 @@ __global__ void __launch_bounds__(kWinThreads, 1)
                                            : min(min(it.len, p.sinks),
                                                  block_key(it, last_s) +
                                                      columns(block_keys(it, last_s)));
+        // (behind the sinks in their block no row sees a key, though it may in a block
+        // of the window: as from before the sequence)
         if (!unseen_bad<D>(p.v + first, stride, it.span.base, w_end, tr, p.window, p.sinks, lane) &&
-            !unseen_bad<D>(p.v + first, stride, it.sink_base, s_end, tr, p.window, p.sinks, lane))
+            !unseen_bad<D>(p.v + first, stride, it.span.sink_end, s_end, -1, p.window, p.sinks, lane))
           continue;
         uint32_t nans = 0u;
 #pragma unroll

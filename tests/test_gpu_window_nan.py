@@ -73,3 +73,23 @@ def test_values_that_are_all_nan(S):
     v[:] = float("nan")
     out, lse = tw.run(q, k, v, 100, 4)
     assert torch.isnan(out).all() and torch.isfinite(lse).all()
+
+
+@pytest.mark.parametrize("H", [2, 40])
+@pytest.mark.parametrize("S,T,window,sinks", [(65, 65, 20, 60), (9, 65, 59, 68), (40, 3000, 2500, 700)])
+def test_infinite_values_in_both_blocks(H, S, T, window, sinks):
+    """A key behind the first sinks in their block and again in the window's: an infinity that a row
+    sees there is its result, whatever the masked columns make of it."""
+    q, k, v = tw.inputs(1, S, T, H, 1, 64, seed=S)
+    bad = [min(10, sinks - 1), min(30, sinks - 1), T - S // 2]
+    for e, j in enumerate(bad):
+        v[0, j, 0, e] = float("inf") if e % 2 else float("-inf")
+    out, lse = tw.run(q, k, v, window, sinks)
+    assert torch.isfinite(lse).all()
+    t = torch.arange(T - S, T)
+    for e, j in enumerate(bad):
+        sees = (t >= j) & ((t - j < window) | (j < sinks))
+        assert torch.equal(torch.isinf(out[0, :, :, e]).cpu(), sees[:, None].expand(S, H)), (e, j)
+        assert not torch.isnan(out[0, :, :, e]).any()
+    out[..., :3] = 0
+    assert torch.isfinite(out).all()
