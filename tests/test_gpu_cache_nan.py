@@ -8,7 +8,7 @@ import pytest
 import torch
 
 import streaming_top_lightning_b200 as stl
-from tests import _cache, test_gpu_cache4 as tc, test_gpu_window as tw
+from tests import _cache, test_gpu_cache4 as tc
 
 pytestmark = pytest.mark.gpu
 
